@@ -59,6 +59,9 @@ enum {
     MTP_STATUS_BAD_TOKEN = 2,  /* a token id outside [0, V); token 0 was used instead */
     MTP_STATUS_BAD_CTX = 4,    /* ctx_len[b] < 0 or ctx_len[b] + k > Lmax; clamped */
     MTP_STATUS_NONFINITE = 8,  /* a logit row without a finite maximum */
+    MTP_STATUS_BAD_ROWS = 32,  /* row_start decreases or leaves the rows; clamped */
+    MTP_STATUS_BAD_PAGE = 64,  /* a page-table entry outside the pool where a position needs
+                                  it: page 0 read in its place, an appended row dropped */
     MTP_STATUS_BOUNDS = 16     /* only a library built with MTP_BOUNDS: an index outside
                                   its buffer was found and that access skipped */
 };
@@ -386,6 +389,155 @@ int spec_verify_fused(int B, int k, int V, int d, float T, int mode,
                       int32_t *out_tok, int32_t *accept_len, int32_t *num_accepted,
                       void *ws, size_t ws_bytes, mtp_stream_t stream);
 
+/*
+ * The target's side of a speculative step: its K/V cache in pages, attention of
+ * the step's new rows over it, and the rules on its logits before spec_verify.
+ * The pages name none of these calls ([P4] "How the draft becomes real output"
+ * only says that the target runs once over every candidate position).
+ *
+ * New rows are ragged: row_start [B+1] int32 (device) holds where each
+ * sequence's rows begin; sequence b has rows row_start[b] .. row_start[b+1]-1 of
+ * the n_rows rows in the arrays (n_rows is how many rows the arrays hold; rows
+ * past row_start[B] are padding, never read for a result and left as they were
+ * in every output).  A sequence may have no rows.  Row i of sequence b sits at
+ * position ctx_len[b] + i: ctx_len [B] int32 counts the positions that were in
+ * the cache before the call, and no call changes it.  After a verification the
+ * caller advances it by accept_len; rejected rows are overwritten by the next
+ * append.  k + 1 rows a sequence verify, one row is plain decoding, more are a
+ * chunk of a prompt, and one call takes any mixture.
+ *
+ * Paged cache: pools k_pages, v_pages [n_pages, Hkv, page, Dh] bf16; position
+ * j of sequence b is slot j % page of page page_table[b, j / page].
+ *   page       positions per page: 16, 32, 64 or 128
+ *   Dh         32, 64 or 128;  Hq a multiple of Hkv, Hq / Hkv <= 8
+ *   page_table [B, max_pages] int32 (device).  Only the entries of positions
+ *              that a row sees (or is written to) are read: the others, of
+ *              pages not yet given or, under a window, already given back, may
+ *              hold anything.  Sequences may share pages that none appends to.
+ * n_pages * Hkv * page < 2^31 and max_pages * page <= 2^30.
+ */
+typedef struct {
+    int32_t Hkv, Dh, page, n_pages, max_pages;
+    void *k_pages, *v_pages;
+    const int32_t *page_table;
+} MtpPagedCache;
+
+/*
+ * Rotary positions.  The first rot_dim dims of each head rotate in pairs,
+ * (t, t + rot_dim/2) or (2t, 2t + 1); pair t at position p by the angle
+ * p * inv_freq[t]; sine and cosine are multiplied by `scale`.
+ *   turns    [rot_dim/2] uint64 (device), from mtp_rope_turns: inv_freq in turns
+ *            a position as 0.64 fixed-point fractions, so that far positions
+ *            lose nothing (the angle is exact to p * 2^-65 turns)
+ *   rot_dim  a multiple of 8, at most Dh
+ */
+enum { MTP_ROPE_HALF = 0, MTP_ROPE_INTERLEAVED = 1 };
+typedef struct {
+    const uint64_t *turns;
+    int32_t rot_dim, layout;
+    float scale;
+} MtpRope;
+
+/*
+ * Host helpers (no GPU).  mtp_rope_frequencies fills inv_freq [rot_dim/2] with
+ * base^(-2t/rot_dim), scaled for contexts longer than the trained one:
+ *   MTP_ROPE_SCALING_LINEAR  every frequency / factor (position interpolation)
+ *   MTP_ROPE_SCALING_YARN    by parts (the YaRN paper): pairs that turn more than
+ *       high_turns times over original_len positions keep their frequency, those
+ *       below low_turns are divided by factor, linear in between; *scale =
+ *       0.1 ln(factor) + 1, else 1.
+ * low_turns, high_turns and original_len are read by YARN only.
+ * mtp_rope_turns converts n frequencies (radians a position) to the table.
+ */
+enum { MTP_ROPE_SCALING_NONE = 0, MTP_ROPE_SCALING_LINEAR = 1, MTP_ROPE_SCALING_YARN = 2 };
+int mtp_rope_frequencies(int rot_dim, double base, int scaling, double factor, double low_turns,
+                         double high_turns, int original_len, double *inv_freq, float *scale);
+int mtp_rope_turns(int n, const double *inv_freq, uint64_t *turns);
+
+/*
+ * mtp_cache_append -- rotate the new rows' queries and keys and write keys and
+ * values into their page slots.
+ *   rope      NULL: nothing rotates (keys are copied, queries too)
+ *   q, k, v   bf16 rows of Hq*Dh, Hkv*Dh, Hkv*Dh, ldq / ldk / ldv elements apart
+ *             (multiples of 8: one projection's output may hold all three)
+ *   q_out     bf16 rows of Hq*Dh, ldqo elements apart; q itself (same stride) to
+ *             rotate in place; no other overlap.  q and q_out both NULL: keys
+ *             and values only.
+ * Products and sums are fp32, rounded once to bf16.  A row whose position lies
+ * past max_pages * page (MTP_STATUS_BAD_CTX) or in a page outside the pool
+ * (MTP_STATUS_BAD_PAGE) is rotated but not written.  Two rows that map to one
+ * slot (a page in two sequences' tables) are written in no defined order.
+ *   ws        at least 256 bytes, 256-byte aligned: the status word
+ */
+int mtp_cache_append(const MtpPagedCache *cache, const MtpRope *rope, int B, int Hq, int n_rows,
+                     const int32_t *row_start, const int32_t *ctx_len, const void *q, int64_t ldq,
+                     const void *k, int64_t ldk, const void *v, int64_t ldv, void *q_out,
+                     int64_t ldqo, void *ws, size_t ws_bytes, mtp_stream_t stream);
+
+/*
+ * mtp_paged_attn -- attention of the new rows over the paged cache, whose pages
+ * already hold the rows' own keys and values (mtp_cache_append).  The row at
+ * position p sees key j iff j <= p and (window == 0, or j > p - window, or
+ * j < sinks): causal, optionally within a sliding window whose first `sinks`
+ * positions stay visible.  Query head h reads kv head h / (Hq/Hkv).
+ *   max_rows  the largest number of rows of any sequence, if the host knows it
+ *             (0: not known).  It only chooses between kernels: any value gives
+ *             the same function.
+ *   q         bf16 rows of Hq*Dh, ldq elements apart (a multiple of 8)
+ *   scale     softmax scale; 0: 1/sqrt(Dh)
+ *   window    0: none;  sinks: ignored without a window
+ *   out       bf16 rows of Hq*Dh, ldo elements apart; must not overlap q
+ *   lse       [n_rows, Hq] fp32, or NULL: ln sum_j exp(scale q.k_j)
+ *   ws        mtp_paged_attn_workspace_size() bytes, 256-byte aligned
+ * A row that sees no key (a ctx_len past the cache) gets zeros and lse -inf.
+ * Scores, softmax statistics and output sums are fp32; the softmax weights are
+ * rounded to bf16 for their product with V.  What no row of a sequence sees may
+ * hold anything, NaN included; a V row that one of its rows sees has to be
+ * finite.  Results are the same bit for bit from run to run.
+ */
+size_t mtp_paged_attn_workspace_size(int B, int n_rows, int max_rows, int Hq, int Hkv, int Dh);
+int mtp_paged_attn(const MtpPagedCache *cache, int B, int Hq, int n_rows, int max_rows,
+                   const int32_t *row_start, const int32_t *ctx_len, const void *q, int64_t ldq,
+                   float scale, int window, int sinks, void *out, int64_t ldo, float *lse, void *ws,
+                   size_t ws_bytes, mtp_stream_t stream);
+
+/*
+ * spec_adjust_logits -- penalties for repeated tokens, biases and a grammar mask
+ * on the target's logits of every candidate position, before spec_verify.
+ * Position j of sequence b follows its history and its drafts 0 .. j-1.  With
+ * c = occurrences of token v in history[prompt_len ..] and in those drafts,
+ * and seen = c > 0 or v in history[0 .. prompt_len):
+ *   x = logits;  if seen: x = x > 0 ? x / rep : x * rep;
+ *   x -= freq * c;  if c > 0: x -= pres;  x += bias;  if not allowed: x = -inf
+ * All arrays are device memory, 16-byte aligned; a NULL one switches its rule off.
+ *   history    [B, hist_cap] int32; the first hist_len[b] are sequence b's prompt
+ *              and output so far (its last token included), the first
+ *              prompt_len[b] of them the prompt (prompt_len NULL: none).
+ *              Lengths are clamped to the array; ids outside [0, V) are skipped.
+ *   rep, freq, pres  [B] fp32; rep > 0
+ *   bias_tok, bias_val [B, bias_cap], bias_len [B]: sparse biases; a token that
+ *              is listed twice gets the sum, added in list order
+ *   mask       [B, k+1, ceil(V/32)] 32-bit words, bit v % 32 of word v / 32 set:
+ *              token v allowed (a grammar's state differs from position to position)
+ * k in 0..8 (0: plain decoding);  draft_tok [B, k] int32 (may be NULL if k = 0 or
+ * no penalty is on);  logits, out [B, k+1, V] fp32; out may be logits itself (in
+ * place: only what a rule changes is read and written) or must not overlap it.
+ * A row that is masked whole is -inf everywhere, which spec_verify reports
+ * (MTP_STATUS_NONFINITE).  Needs no workspace; sets no status.
+ */
+typedef struct {
+    const int32_t *history, *prompt_len, *hist_len;
+    int32_t hist_cap;
+    const float *rep, *freq, *pres;
+    const int32_t *bias_tok;
+    const float *bias_val;
+    const int32_t *bias_len;
+    int32_t bias_cap;
+    const uint32_t *mask;
+} MtpLogitRules;
+int spec_adjust_logits(int B, int k, int V, const MtpLogitRules *rules, const float *logits,
+                       const int32_t *draft_tok, float *out, mtp_stream_t stream);
+
 /* Wait for the stream, then copy the workspace's status word (MTP_STATUS_* bits)
  * to *status.  Returns MTP_OK or MTP_ERR_*. */
 int mtp_get_status(const void *ws, mtp_stream_t stream, int32_t *status);
@@ -453,7 +605,12 @@ enum {
     MTP_TK_TC_AUX = 31,     /* the batched path's prologue / select / scatter kernels */
     MTP_TK_FUSED_GEMM = 40, /* spec_verify_fused: head GEMM */
     MTP_TK_FUSED_AUX = 41,  /* spec_verify_fused: draft statistics, decisions and draws */
-    MTP_TK_CHAIN = 50       /* chain launch of several GEMV ops */
+    MTP_TK_CHAIN = 50,      /* chain launch of several GEMV ops */
+    MTP_TK_PAGED_ATTN = 60, /* paged attention: streaming kernel */
+    MTP_TK_PAGED_ATTN_TC = 61, /* paged attention: tensor-core kernel */
+    MTP_TK_PAGED_COMBINE = 62, /* paged attention: joins partial items */
+    MTP_TK_CACHE_APPEND = 63,  /* mtp_cache_append */
+    MTP_TK_LOGITS = 64         /* spec_adjust_logits */
 };
 typedef struct MtpTraceEntry {
     uint64_t launch;      /* the launch's grid id */

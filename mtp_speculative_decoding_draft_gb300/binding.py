@@ -23,6 +23,12 @@ STATUS_BAD_TOKEN = 2
 STATUS_BAD_CTX = 4
 STATUS_NONFINITE = 8
 STATUS_BOUNDS = 16
+STATUS_BAD_ROWS = 32
+STATUS_BAD_PAGE = 64
+
+ROPE_HALF = 0
+ROPE_INTERLEAVED = 1
+ROPE_SCALING_NONE, ROPE_SCALING_LINEAR, ROPE_SCALING_YARN = 0, 1, 2
 
 
 class MtpError(RuntimeError):
@@ -47,6 +53,24 @@ class MtpWeights(ctypes.Structure):
 
 class MtpModule(ctypes.Structure):
     _fields_ = [("w", MtpWeights), ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p)]
+
+
+class MtpPagedCache(ctypes.Structure):
+    _fields_ = [("Hkv", ctypes.c_int32), ("Dh", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
+class MtpRope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class MtpLogitRules(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p), ("hist_len", ctypes.c_void_p),
+                ("hist_cap", ctypes.c_int32), ("rep", ctypes.c_void_p), ("freq", ctypes.c_void_p),
+                ("pres", ctypes.c_void_p), ("bias_tok", ctypes.c_void_p), ("bias_val", ctypes.c_void_p),
+                ("bias_len", ctypes.c_void_p), ("bias_cap", ctypes.c_int32), ("mask", ctypes.c_void_p)]
 
 
 _LIB = None
@@ -100,6 +124,22 @@ def _lib():
         L.spec_verify_fused_workspace_size.restype = Z
         L.spec_verify_fused.argtypes = [I, I, I, I, F, I, P, P, P, P, P, P, P, P, P, P, Z, P]
         L.spec_verify_fused.restype = I
+        L64 = ctypes.c_int64
+        L.mtp_rope_frequencies.argtypes = [I, ctypes.c_double, I, ctypes.c_double, ctypes.c_double, ctypes.c_double, I,
+                                           P, ctypes.POINTER(ctypes.c_float)]
+        L.mtp_rope_frequencies.restype = I
+        L.mtp_rope_turns.argtypes = [I, P, P]
+        L.mtp_rope_turns.restype = I
+        L.mtp_cache_append.argtypes = [ctypes.POINTER(MtpPagedCache), ctypes.POINTER(MtpRope), I, I, I, P, P, P, L64,
+                                       P, L64, P, L64, P, L64, P, Z, P]
+        L.mtp_cache_append.restype = I
+        L.mtp_paged_attn_workspace_size.argtypes = [I, I, I, I, I, I]
+        L.mtp_paged_attn_workspace_size.restype = Z
+        L.mtp_paged_attn.argtypes = [ctypes.POINTER(MtpPagedCache), I, I, I, I, P, P, P, L64, F, I, I, P, L64, P, P, Z,
+                                     P]
+        L.mtp_paged_attn.restype = I
+        L.spec_adjust_logits.argtypes = [I, I, I, ctypes.POINTER(MtpLogitRules), P, P, P, P]
+        L.spec_adjust_logits.restype = I
         L.mtp_get_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
         L.mtp_get_status.restype = I
         L.mtp_clear_status.argtypes = [P, P]
@@ -396,6 +436,159 @@ def spec_verify_fused(B, k, V, d, T, mode, head, target_hidden, draft_logits, dr
         raise MtpError(rc, "spec_verify_fused")
 
 
+def make_paged_cache(k_pages, v_pages, page_table):
+    """MtpPagedCache over pools k_pages, v_pages [n_pages, Hkv, page, Dh] bf16 and
+    page_table [B, max_pages] int32 (CUDA tensors; the struct keeps them alive)."""
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must be [n_pages, Hkv, page, Dh] alike")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    n_pages, Hkv, page, Dh = k_pages.shape
+    c = MtpPagedCache(Hkv, Dh, page, n_pages, page_table.shape[1], _ptr(k_pages, "k_pages", torch.bfloat16),
+                      _ptr(v_pages, "v_pages", torch.bfloat16), _ptr(page_table, "page_table", torch.int32))
+    c.tensors = (k_pages, v_pages, page_table)
+    c.B = page_table.shape[0]
+    return c
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=ROPE_SCALING_NONE, factor=1.0, low_turns=1.0, high_turns=32.0,
+                     original_len=4096):
+    """(inv_freq [rot_dim/2] float64 CPU tensor, scale) of rotary positions, scaled
+    for long contexts (see mtp_rope_frequencies)."""
+    f = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float64)
+    scale = ctypes.c_float(1.0)
+    rc = _lib().mtp_rope_frequencies(int(rot_dim), float(base), int(scaling), float(factor), float(low_turns),
+                                     float(high_turns), int(original_len), f.data_ptr(), ctypes.byref(scale))
+    if rc != 0:
+        raise MtpError(rc, "mtp_rope_frequencies")
+    return f, float(scale.value)
+
+
+def rope_table(inv_freq):
+    """The table of make_rope (int64 CPU tensor of 0.64 fixed-point turns) from
+    inv_freq, radians a position (float64 CPU tensor)."""
+    f = inv_freq.to("cpu", torch.float64).contiguous()
+    t = torch.empty(f.numel(), dtype=torch.int64)
+    rc = _lib().mtp_rope_turns(int(f.numel()), f.data_ptr(), t.data_ptr())
+    if rc != 0:
+        raise MtpError(rc, "mtp_rope_turns")
+    return t
+
+
+def make_rope(turns, rot_dim, layout=ROPE_HALF, scale=1.0):
+    """MtpRope from a CUDA copy of rope_table()'s table (kept alive by the struct)."""
+    r = MtpRope(_ptr(turns, "turns", torch.int64, int(rot_dim) // 2), int(rot_dim), int(layout), float(scale))
+    r.tensors = (turns,)
+    return r
+
+
+def _rows(t, name, dtype=torch.bfloat16):
+    """(pointer, row stride in elements) of [n, heads, Dh] or [n, heads * Dh] rows
+    that are contiguous inside and a stride apart."""
+    if not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    st, sh = t.stride(), t.shape
+    if st[-1] != 1 or (len(sh) == 3 and sh[1] > 1 and st[1] != sh[2]) or len(sh) not in (2, 3):
+        raise ValueError("%s must be [rows, heads, Dh] or [rows, heads * Dh], contiguous within a row" % name)
+    return t.data_ptr(), st[0]
+
+
+def _row_args(cache, row_start, ctx_len):
+    B = ctx_len.numel()
+    if B > cache.B:
+        raise ValueError("page_table has %d sequences, ctx_len %d" % (cache.B, B))
+    return B, _ptr(row_start, "row_start", torch.int32, B + 1), _ptr(ctx_len, "ctx_len", torch.int32, B)
+
+
+def mtp_cache_append(cache, rope, row_start, ctx_len, q, k, v, q_out, ws, stream=None):
+    """Rotate the new rows' q and k (rope None: not) and write k, v into the pages
+    of cache (make_paged_cache).  q, k, v, q_out: bf16 [rows, heads, Dh], rows any
+    multiple of 8 elements apart; q and q_out may be None together."""
+    B, rs, cl = _row_args(cache, row_start, ctx_len)
+    n, w = k.shape[0], cache.Hkv * cache.Dh
+    kp, ldk = _rows(k, "k")
+    vp, ldv = _rows(v, "v")
+    qp = qo = None
+    ldq = ldqo = Hq = 0
+    if q is not None and q_out is not None:
+        qp, ldq = _rows(q, "q")
+        qo, ldqo = _rows(q_out, "q_out")
+        Hq = q.numel() // (n * cache.Dh) if n else 0
+        if q.shape[0] != n or q_out.shape[0] != n or q_out.numel() != q.numel() or Hq * cache.Dh * n != q.numel():
+            raise ValueError("q and q_out must have k's rows of Hq * Dh")
+    elif q is not None or q_out is not None:
+        raise ValueError("q and q_out are given together")
+    if v.shape[0] != n or k.numel() != n * w or v.numel() != n * w:
+        raise ValueError("k and v must be rows of Hkv * Dh")
+    rc = _lib().mtp_cache_append(cache, rope, B, Hq, n, rs, cl, qp, ldq, kp, ldk, vp, ldv, qo, ldqo, _ptr(ws, "ws"),
+                                 ws.numel() * ws.element_size(), _stream(stream))
+    if rc != 0:
+        raise MtpError(rc, "mtp_cache_append")
+
+
+def paged_attn_workspace_size(B, n_rows, max_rows, Hq, Hkv, Dh):
+    return int(_lib().mtp_paged_attn_workspace_size(int(B), int(n_rows), int(max_rows), int(Hq), int(Hkv), int(Dh)))
+
+
+def mtp_paged_attn(cache, row_start, ctx_len, q, out, lse, ws, scale=0.0, window=0, sinks=0, max_rows=0, stream=None):
+    """Attention of the new rows q [rows, Hq, Dh] over the pages of cache, into out
+    (bf16, the same shape) and, if given, lse [rows, Hq] fp32."""
+    B, rs, cl = _row_args(cache, row_start, ctx_len)
+    qp, ldq = _rows(q, "q")
+    op, ldo = _rows(out, "out")
+    n = q.shape[0]
+    Hq = q.numel() // (n * cache.Dh) if n else 0
+    if out.shape[0] != n or out.numel() != q.numel() or Hq * cache.Dh * n != q.numel():
+        raise ValueError("q and out must have the same rows of Hq * Dh")
+    rc = _lib().mtp_paged_attn(cache, B, Hq, n, int(max_rows), rs, cl, qp, ldq, float(scale), int(window), int(sinks),
+                               op, ldo, _ptr(lse, "lse", torch.float32, n * Hq), _ptr(ws, "ws"),
+                               ws.numel() * ws.element_size(), _stream(stream))
+    if rc != 0:
+        raise MtpError(rc, "mtp_paged_attn")
+
+
+def make_logit_rules(history=None, prompt_len=None, hist_len=None, rep=None, freq=None, pres=None, bias_tok=None,
+                     bias_val=None, bias_len=None, mask=None):
+    """MtpLogitRules from CUDA tensors: history [B, cap] and bias_tok [B, cap]
+    int32, bias_val fp32, the lengths [B] int32, rep / freq / pres [B] fp32 and
+    mask [B, k+1, ceil(V/32)] int32.  The struct keeps them alive."""
+    def width(t, name):
+        if t is None:
+            return 0
+        if t.dim() != 2:
+            raise ValueError("%s must be [B, cap]" % name)
+        return t.shape[1]
+    if bias_tok is not None and bias_val is not None and bias_val.shape != bias_tok.shape:
+        raise ValueError("bias_val must have bias_tok's shape")
+    i32, f32 = torch.int32, torch.float32
+    r = MtpLogitRules(_ptr(history, "history", i32), _ptr(prompt_len, "prompt_len", i32), _ptr(hist_len, "hist_len", i32),
+                      width(history, "history"), _ptr(rep, "rep", f32), _ptr(freq, "freq", f32), _ptr(pres, "pres", f32),
+                      _ptr(bias_tok, "bias_tok", i32), _ptr(bias_val, "bias_val", f32), _ptr(bias_len, "bias_len", i32),
+                      width(bias_tok, "bias_tok"), _ptr(mask, "mask", i32))
+    r.tensors = (history, prompt_len, hist_len, rep, freq, pres, bias_tok, bias_val, bias_len, mask)
+    sizes = [t.shape[0] for t in r.tensors if t is not None]
+    r.B = min(sizes) if sizes else None
+    return r
+
+
+def spec_adjust_logits(B, k, V, rules, logits, draft_tok, out, stream=None):
+    """Apply rules (make_logit_rules) to the target logits [B, k+1, V] fp32 into
+    out (logits itself: in place); draft_tok [B, k] int32."""
+    if rules.B is not None and rules.B < B:
+        raise ValueError("the rules hold %d sequences, B is %d" % (rules.B, B))
+    mask = rules.tensors[-1]
+    if mask is not None and mask.numel() < B * (k + 1) * ((V + 31) // 32):
+        raise ValueError("mask must be [B, k+1, ceil(V/32)]")
+    n = B * (k + 1) * V
+    rc = _lib().spec_adjust_logits(int(B), int(k), int(V), rules, _ptr(logits, "logits", torch.float32, n),
+                                   _ptr(draft_tok, "draft_tok", torch.int32, B * k) if k else None,
+                                   _ptr(out, "out", torch.float32, n), _stream(stream))
+    if rc != 0:
+        raise MtpError(rc, "spec_adjust_logits")
+
+
 def get_status(ws, stream=None):
     v = ctypes.c_int32(0)
     rc = _lib().mtp_get_status(_ptr(ws, "ws"), _stream(stream), ctypes.byref(v))
@@ -444,7 +637,8 @@ class MtpTraceEntry(ctypes.Structure):
 TRACE_KIND_NAMES = {0: "gemv input projection", 1: "gemv QKV", 2: "gemv output projection", 3: "gemv gate/up",
                     4: "gemv down", 5: "gemv LM head", 10: "attention", 11: "attention (tensor cores)",
                     20: "verify (cluster)", 21: "verify (ticketed)", 30: "tc GEMM", 31: "tc prologue/select",
-                    40: "fused verify GEMM", 41: "fused verify aux (stats, decisions, draws)", 50: "chain"}
+                    40: "fused verify GEMM", 41: "fused verify aux (stats, decisions, draws)", 50: "chain", 60: "paged attention (streaming)", 61: "paged attention (tensor cores)",
+                    62: "paged attention combine", 63: "cache append", 64: "logit rules"}
 
 
 def trace_read(max_entries=16384):

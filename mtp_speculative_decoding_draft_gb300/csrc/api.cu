@@ -11,6 +11,8 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "internal.h"
+#include "logits.cuh"
+#include "paged.cuh"
 #include "mtpspec.h"
 
 namespace mtp {
@@ -76,6 +78,8 @@ int device_info(DevInfo *out) {
     if (verify_set_attributes() != cudaSuccess) return MTP_ERR_CUDA;
     if (tc_set_attributes() != cudaSuccess) return MTP_ERR_CUDA;
     if (fused_set_attributes() != cudaSuccess) return MTP_ERR_CUDA;
+    if (paged_set_attributes() != cudaSuccess) return MTP_ERR_CUDA;
+    if (logits_set_attributes() != cudaSuccess) return MTP_ERR_CUDA;
     di.ctx = context_id();  // set up (made current) by the calls above
     di.init = true;
   }
@@ -508,7 +512,9 @@ int static_scratch(void **out) {
 static_assert(kTkGemv == MTP_TK_GEMV && kTkAttn == MTP_TK_ATTN && kTkAttnTc == MTP_TK_ATTN_TC &&
                   kTkVerify == MTP_TK_VERIFY && kTkVerifySplit == MTP_TK_VERIFY_SPLIT && kTkTcGemm == MTP_TK_TC_GEMM &&
                   kTkTcAux == MTP_TK_TC_AUX && kTkFusedGemm == MTP_TK_FUSED_GEMM &&
-                  kTkFusedAux == MTP_TK_FUSED_AUX && kTkChain == MTP_TK_CHAIN,
+                  kTkFusedAux == MTP_TK_FUSED_AUX && kTkChain == MTP_TK_CHAIN && kTkPagedAttn == MTP_TK_PAGED_ATTN &&
+                  kTkPagedAttnTc == MTP_TK_PAGED_ATTN_TC && kTkPagedCombine == MTP_TK_PAGED_COMBINE &&
+                  kTkAppend == MTP_TK_CACHE_APPEND && kTkLogits == MTP_TK_LOGITS,
               "trace kinds match the header");
 
 // the launch-trace collectors of the kernel files (MTP_TRACE_COLLECTOR)
@@ -520,6 +526,9 @@ int trace_collect_tc(TraceRec *, int);
 int trace_collect_fused(TraceRec *, int);
 int trace_collect_chain(TraceRec *, int);
 int trace_collect_diag(TraceRec *, int);
+int trace_collect_paged_attn(TraceRec *, int);
+int trace_collect_cache_append(TraceRec *, int);
+int trace_collect_logits(TraceRec *, int);
 
 }  // namespace mtp
 
@@ -771,6 +780,195 @@ int spec_verify_fused(int B, int k, int V, int d, float T, int mode, const void 
   return cuda_rc(e);
 }
 
+}  // extern "C"
+
+namespace mtp {
+namespace {
+
+// The cache's description is sound (the table's entries are the device's to check).
+int check_cache(const MtpPagedCache *c) {
+  if (!c || c->Hkv < 1 || c->n_pages < 1 || c->max_pages < 1) return MTP_ERR_INVALID_ARG;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !aligned16(c->page_table)) return MTP_ERR_INVALID_ARG;
+  if (c->Dh != 32 && c->Dh != 64 && c->Dh != 128) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return MTP_ERR_UNSUPPORTED_SHAPE;
+  // rows of the pools are TMA coordinates, positions 32-bit
+  if ((long long)c->n_pages * c->Hkv * c->page >= (1ll << 31)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if ((long long)c->max_pages * c->page > (1ll << 30)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  return MTP_OK;
+}
+
+int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+int check_rows(const MtpPagedCache *c, int B, int Hq, int n_rows, const int32_t *row_start, const int32_t *ctx_len) {
+  if (B < 1 || n_rows < 1 || Hq < 1) return MTP_ERR_INVALID_ARG;
+  if (B > (1 << 20) || n_rows > (1 << 30)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if (Hq % c->Hkv || Hq / c->Hkv > kMaxGroup) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(row_start) || !aligned16(ctx_len)) return MTP_ERR_INVALID_ARG;
+  return MTP_OK;
+}
+
+bool row_stride_ok(int64_t ld, long long width) { return ld >= width && ld % 8 == 0; }
+
+}  // namespace
+}  // namespace mtp
+
+extern "C" {
+
+int mtp_rope_frequencies(int rot_dim, double base, int scaling, double factor, double low_turns, double high_turns,
+                         int original_len, double *inv_freq, float *scale) {
+  if (rot_dim < 2 || rot_dim % 2 || !(base > 1.0) || !inv_freq || !scale) return MTP_ERR_INVALID_ARG;
+  if (scaling < MTP_ROPE_SCALING_NONE || scaling > MTP_ROPE_SCALING_YARN) return MTP_ERR_INVALID_ARG;
+  if (scaling != MTP_ROPE_SCALING_NONE && !(factor >= 1.0 && factor < 1e12)) return MTP_ERR_INVALID_ARG;
+  if (scaling == MTP_ROPE_SCALING_YARN && (original_len < 1 || !(low_turns > 0.0) || !(high_turns > low_turns)))
+    return MTP_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925286766559;
+  for (int t = 0; t < rot_dim / 2; ++t) {
+    const double f = pow(base, -2.0 * t / rot_dim);
+    double g = f;
+    if (scaling == MTP_ROPE_SCALING_LINEAR) g = f / factor;
+    if (scaling == MTP_ROPE_SCALING_YARN) {
+      // turns over the original context: many keep their frequency, few are stretched
+      const double turns = original_len * f / two_pi;
+      const double keep = fmin(1.0, fmax(0.0, (turns - low_turns) / (high_turns - low_turns)));
+      g = f * keep + f / factor * (1.0 - keep);
+    }
+    inv_freq[t] = g;
+  }
+  *scale = scaling == MTP_ROPE_SCALING_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.f;
+  return MTP_OK;
+}
+
+int mtp_rope_turns(int n, const double *inv_freq, uint64_t *turns) {
+  if (n < 1 || !inv_freq || !turns) return MTP_ERR_INVALID_ARG;
+  // 1 / (2 pi) in two doubles: the product below carries over 100 bits
+  const double hi = 0.15915494309189535, lo = -9.839338337591243e-18, two64 = 18446744073709551616.0;
+  for (int t = 0; t < n; ++t) {
+    const double f = fabs(inv_freq[t]);
+    if (!(f < 1e9)) return MTP_ERR_INVALID_ARG;
+    const double p = f * hi, e = fma(f, hi, -p) + f * lo;
+    const double x = (p - floor(p)) * two64;  // whole turns drop out: positions are integers
+    const double whole = floor(x);
+    const uint64_t w = whole >= two64 ? 0u : (uint64_t)whole;
+    const uint64_t u = w + (uint64_t)(int64_t)llrint((x - whole) + e * two64);
+    turns[t] = inv_freq[t] < 0.0 ? 0u - u : u;
+  }
+  return MTP_OK;
+}
+
+int mtp_cache_append(const MtpPagedCache *cache, const MtpRope *rope, int B, int Hq, int n_rows,
+                     const int32_t *row_start, const int32_t *ctx_len, const void *q, int64_t ldq, const void *k,
+                     int64_t ldk, const void *v, int64_t ldv, void *q_out, int64_t ldqo, void *ws, size_t ws_bytes,
+                     mtp_stream_t stream) {
+  int rc = check_cache(cache);
+  if (!rc) rc = check_rows(cache, B, q ? Hq : cache->Hkv, n_rows, row_start, ctx_len);
+  if (rc) return rc;
+  const long long kvw = (long long)cache->Hkv * cache->Dh, qw = (long long)Hq * cache->Dh;
+  if (!aligned16(k) || !aligned16(v) || !row_stride_ok(ldk, kvw) || !row_stride_ok(ldv, kvw)) return MTP_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr)) return MTP_ERR_INVALID_ARG;
+  if (q && (!aligned16(q) || !aligned16(q_out) || !row_stride_ok(ldq, qw) || !row_stride_ok(ldqo, qw)))
+    return MTP_ERR_INVALID_ARG;
+  if (q == q_out && q && ldq != ldqo) return MTP_ERR_INVALID_ARG;
+  if (rope) {
+    if (rope->layout != MTP_ROPE_HALF && rope->layout != MTP_ROPE_INTERLEAVED) return MTP_ERR_INVALID_ARG;
+    if (!aligned16(rope->turns) || !(rope->scale > 0.f && rope->scale < 1e30f)) return MTP_ERR_INVALID_ARG;
+    if (rope->rot_dim < 8 || rope->rot_dim % 8 || rope->rot_dim > cache->Dh) return MTP_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (!aligned16(ws) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MTP_ERR_INVALID_ARG;
+  if (ws_bytes < kAlign) return MTP_ERR_WORKSPACE;
+  AppendArgs a{};
+  a.B = B; a.Hq = q ? Hq : 0; a.Hkv = cache->Hkv; a.Dh = cache->Dh;
+  a.page = cache->page; a.page_shift = page_shift(cache->page); a.n_pages = cache->n_pages;
+  a.max_pages = cache->max_pages; a.cap = cache->max_pages * cache->page; a.n_rows = n_rows;
+  a.rot = rope ? rope->rot_dim : 0;
+  a.layout = rope ? rope->layout : 0;
+  a.turns = rope ? reinterpret_cast<const unsigned long long *>(rope->turns) : nullptr;
+  a.scale = rope ? rope->scale : 1.f;
+  a.row_start = row_start; a.ctx_len = ctx_len; a.page_table = cache->page_table;
+  a.q = q; a.k = k; a.v = v; a.ldq = ldq; a.ldk = ldk; a.ldv = ldv; a.ldqo = ldqo; a.q_out = q_out;
+  a.k_pages = static_cast<uint16_t *>(cache->k_pages);
+  a.v_pages = static_cast<uint16_t *>(cache->v_pages);
+  a.status = static_cast<int *>(ws);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  NvtxRange r("mtp cache append");
+  cudaError_t e = launch_cache_append(a, s, use_pdl());
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return cuda_rc(e);
+}
+
+size_t mtp_paged_attn_workspace_size(int B, int n_rows, int max_rows, int Hq, int Hkv, int Dh) {
+  if (B < 1 || n_rows < 1 || max_rows < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv || Hq / Hkv > kMaxGroup) return 0;
+  if (Dh != 32 && Dh != 64 && Dh != 128) return 0;
+  return kAlign + paged_attn_scratch_bytes(n_rows, max_rows, Hq / Hkv, Dh);
+}
+
+int mtp_paged_attn(const MtpPagedCache *cache, int B, int Hq, int n_rows, int max_rows, const int32_t *row_start,
+                   const int32_t *ctx_len, const void *q, int64_t ldq, float scale, int window, int sinks, void *out,
+                   int64_t ldo, float *lse, void *ws, size_t ws_bytes, mtp_stream_t stream) {
+  int rc = check_cache(cache);
+  if (!rc) rc = check_rows(cache, B, Hq, n_rows, row_start, ctx_len);
+  if (rc) return rc;
+  const long long qw = (long long)Hq * cache->Dh;
+  if (max_rows < 0 || window < 0 || sinks < 0) return MTP_ERR_INVALID_ARG;
+  if (!(scale >= 0.f && scale < 1e30f)) return MTP_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !row_stride_ok(ldq, qw) || !row_stride_ok(ldo, qw)) return MTP_ERR_INVALID_ARG;
+  if (lse && !aligned16(lse)) return MTP_ERR_INVALID_ARG;
+  if (q == out) return MTP_ERR_INVALID_ARG;
+  if (!aligned16(ws) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MTP_ERR_INVALID_ARG;
+  if (ws_bytes < mtp_paged_attn_workspace_size(B, n_rows, max_rows, Hq, cache->Hkv, cache->Dh)) return MTP_ERR_WORKSPACE;
+  if (!tc_available()) return MTP_ERR_CUDA;
+  DevInfo di;
+  if ((rc = device_info(&di))) return rc;
+  PagedArgs a{};
+  a.B = B; a.Hq = Hq; a.Hkv = cache->Hkv; a.G = Hq / cache->Hkv; a.Dh = cache->Dh;
+  a.page = cache->page; a.page_shift = page_shift(cache->page); a.n_pages = cache->n_pages;
+  a.max_pages = cache->max_pages; a.cap = cache->max_pages * cache->page; a.n_rows = n_rows;
+  a.row_start = row_start; a.ctx_len = ctx_len; a.page_table = cache->page_table;
+  a.q = static_cast<const uint16_t *>(q); a.ldq = ldq; a.out = out; a.ldo = ldo; a.lse = lse;
+  a.scale_log2 = (scale > 0.f ? scale : 1.f / sqrtf((float)cache->Dh)) * kLog2e;
+  a.window = window; a.sinks = window ? sinks : 0;
+  a.status = static_cast<int *>(ws);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  NvtxRange r("mtp paged attention");
+  cudaError_t e = timed(MTP_KC_ATTN, s, [&] {
+    return launch_paged_attn(a, cache->k_pages, cache->v_pages, max_rows, static_cast<char *>(ws) + kAlign, di.sms, s,
+                             use_pdl());
+  });
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaErrorNotSupported ? MTP_ERR_CUDA : cuda_rc(e);
+}
+
+int spec_adjust_logits(int B, int k, int V, const MtpLogitRules *rules, const float *logits, const int32_t *draft_tok,
+                       float *out, mtp_stream_t stream) {
+  if (!rules || B < 1 || k < 0 || k > 8 || V < 1 || V > (1 << 30) || B > (1 << 20)) return MTP_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(out)) return MTP_ERR_INVALID_ARG;
+  if ((long long)B * ((V + 1023) / 1024) >= (1ll << 31)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  const void *opt[] = {draft_tok, rules->history, rules->prompt_len, rules->hist_len, rules->rep, rules->freq,
+                       rules->pres, rules->bias_tok, rules->bias_val, rules->bias_len, rules->mask};
+  for (const void *p : opt)
+    if (p && !aligned16(p)) return MTP_ERR_INVALID_ARG;
+  if (rules->history && (!rules->hist_len || rules->hist_cap < 1)) return MTP_ERR_INVALID_ARG;
+  if (rules->bias_tok && (!rules->bias_val || !rules->bias_len || rules->bias_cap < 1)) return MTP_ERR_INVALID_ARG;
+  const bool penal = rules->rep || rules->freq || rules->pres;
+  if (penal && k > 0 && !draft_tok) return MTP_ERR_INVALID_ARG;
+  DevInfo di;
+  int rc = device_info(&di);
+  if (rc) return rc;
+  LogitArgs a{};
+  a.B = B; a.k = k; a.V = V;
+  a.history = penal ? rules->history : nullptr;
+  a.hist_cap = rules->hist_cap; a.prompt_len = rules->prompt_len; a.hist_len = rules->hist_len;
+  a.rep = rules->rep; a.freq = rules->freq; a.pres = rules->pres;
+  a.bias_tok = rules->bias_tok; a.bias_val = rules->bias_val; a.bias_len = rules->bias_len; a.bias_cap = rules->bias_cap;
+  a.mask = reinterpret_cast<const uint32_t *>(rules->mask);
+  a.logits = logits; a.out = out;
+  a.draft_tok = penal ? draft_tok : nullptr;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  NvtxRange r("spec adjust logits");
+  cudaError_t e = launch_adjust_logits(a, di.sms, s, use_pdl());
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return cuda_rc(e);
+}
+
 int mtp_get_status(const void *ws, mtp_stream_t stream, int32_t *status) {
   if (!ws || !status) return MTP_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -836,7 +1034,8 @@ int mtp_trace_read(MtpTraceEntry *entries, int max_entries) {
                                          mtp::trace_collect_verify,
                                          mtp::trace_collect_verify_split, mtp::trace_collect_tc,
                                          mtp::trace_collect_fused, mtp::trace_collect_chain,
-                                         mtp::trace_collect_diag};
+                                         mtp::trace_collect_diag, mtp::trace_collect_paged_attn,
+                                         mtp::trace_collect_cache_append, mtp::trace_collect_logits};
   static mtp::TraceRec recs[mtp::kTraceSlots];
   int n = 0;
   for (Collector col : collectors) {

@@ -30,6 +30,7 @@
 #include "common.cuh"
 #include "draft_ops.cuh"
 #include "internal.h"
+#include "paged.cuh"
 #include "tcgen05.cuh"
 
 namespace mtp {
@@ -716,6 +717,20 @@ bool make_bf16_map(CUtensorMap *m, const void *base, uint64_t cols, uint64_t row
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 2-D map over a pool of K or V pages seen as [rows, Dh] bf16: boxes of box_rows
+// rows by at most 64 elements, 128-byte swizzle (64-byte for heads of 32).
+bool make_page_map(CUtensorMap *m, const void *base, int Dh, uint64_t rows, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)Dh, rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)Dh * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)(Dh < 64 ? Dh : 64), box_rows};
+  const cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, Dh < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 namespace {
