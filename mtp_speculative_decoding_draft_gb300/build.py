@@ -40,7 +40,7 @@ def library_path(variant=None):
         raise RuntimeError("unknown MTP_LIB_VARIANT %r (known: %s)" % (v, ", ".join(repr(k) for k in VARIANTS)))
     return VARIANTS[v][1]
 SOURCES = ("api.cu", "draft.cu", "verify.cu", "verify_split.cu", "tc.cu", "attn_tc.cu", "diag.cu", "fused.cu",
-           "chain.cu", "paged_attn.cu", "cache_append.cu", "logits.cu")
+           "chain.cu", "paged_attn.cu", "paged_attn_tc.cu", "cache_append.cu", "logits.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -527,6 +527,7 @@ int trace_collect_fused(TraceRec *, int);
 int trace_collect_chain(TraceRec *, int);
 int trace_collect_diag(TraceRec *, int);
 int trace_collect_paged_attn(TraceRec *, int);
+int trace_collect_paged_attn_tc(TraceRec *, int);
 int trace_collect_cache_append(TraceRec *, int);
 int trace_collect_logits(TraceRec *, int);
 
@@ -1035,6 +1036,7 @@ int mtp_trace_read(MtpTraceEntry *entries, int max_entries) {
                                          mtp::trace_collect_verify_split, mtp::trace_collect_tc,
                                          mtp::trace_collect_fused, mtp::trace_collect_chain,
                                          mtp::trace_collect_diag, mtp::trace_collect_paged_attn,
+                                         mtp::trace_collect_paged_attn_tc,
                                          mtp::trace_collect_cache_append, mtp::trace_collect_logits};
   static mtp::TraceRec recs[mtp::kTraceSlots];
   int n = 0;

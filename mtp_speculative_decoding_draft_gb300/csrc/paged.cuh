@@ -52,6 +52,10 @@ struct PagedArgs {
   int rows_above, rows_upto;
   int tpb;                // tokens per block
   int min_tiles;          // least tiles of a share
+  // Behind the tensor-core kernel, which starts dependents only after its own
+  // wait, the streaming kernel's inputs are ready at its start: it waits at its
+  // end instead, and runs on the SMs that the other kernel's tail leaves.
+  int late_wait;
   PagedDesc *desc;        // [CTAs]
   float *part_o;          // [CTAs][2][block rows][Dh]
   float *part_ml;         // [CTAs][2][block rows][2]

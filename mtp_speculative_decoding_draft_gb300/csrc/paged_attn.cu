@@ -20,7 +20,7 @@
 #include <stdlib.h>
 
 #include "internal.h"
-#include "paged.cuh"
+#include "paged_tc.cuh"
 
 namespace mtp {
 
@@ -113,12 +113,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
     fence_barrier_init();
   }
-  grid_dep_wait();
+  if (!p.late_wait) grid_dep_wait();
   trace_dep(kTkPagedAttn);
   grid_dep_launch();
   const PagedShare sh = paged_plan<kTK, kThreads>(p, scratch);  // its barriers publish the mbarriers
   if (tid == 0) p.desc[blockIdx.x].rows = 0;
   if (sh.start >= sh.end) {
+    grid_dep_wait();
     trace_end(kTkPagedAttn);
     return;
   }
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     if (!ok)  // let copies still in flight land before the CTA exits
       for (int i = max(0, issued - kStages); i < issued; ++i)
         if (!mbar_wait(&full[i % kStages], (uint32_t)(i / kStages) & 1u, p.status)) break;
+    grid_dep_wait();
     trace_end(kTkPagedAttn);
     return;
   }
@@ -396,22 +398,32 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
     named_sync(1, 32 * kCW);  // the buffer is the next block's queries
   }
+  grid_dep_wait();
   trace_end(kTkPagedAttn);
 }
 
-// Joins the segments of the item that starts in CTA blockIdx.x of the streaming
-// (or tensor-core) kernel and ends in a later one, in key order: a warp a row.
+// Joins the segments of the items that end in a later CTA than they start in, in
+// key order, a warp a row: block x takes the item that starts in CTA x of the
+// tensor-core kernel, then of the streaming kernel.
+struct CombineParams {
+  PagedArgs tc, st;
+  int tc_ctas, st_rows;
+};
+
 template <int DH>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedArgs p, int block_rows) {
+__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ CombineParams cp) {
   trace_start(kTkPagedCombine);
   grid_dep_wait();
   grid_dep_launch();
+  const bool tc = (int)blockIdx.x < cp.tc_ctas;
+  const PagedArgs &p = tc ? cp.tc : cp.st;
+  const int block_rows = tc ? kPagedTcRows : cp.st_rows, cta = (int)blockIdx.x - (tc ? 0 : cp.tc_ctas);
   constexpr int PER = DH / 32;
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const PagedDesc d = p.desc[blockIdx.x];
-  if (r < d.rows) {
-    const int nseg = d.last_cta - (int)blockIdx.x + 1;
-    auto seg = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * block_rows + r; };
+  const int lane = threadIdx.x & 31;
+  const PagedDesc d = p.desc[cta];
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < d.rows; r += 8 * gridDim.y) {
+    const int nseg = d.last_cta - cta + 1;
+    auto seg = [&](int i) { return ((size_t)(cta + i) * 2 + (i == 0 ? 1 : 0)) * block_rows + r; };
     float M = -INFINITY;
     for (int i = lane; i < nseg; i += 32) M = fmaxf(M, p.part_ml[seg(i) * 2]);
     M = warp_max(M);
@@ -498,15 +510,10 @@ cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t s, c
 
 template <int DH, int RG>
 cudaError_t launch_stream(const StreamParams &sp, int ctas, cudaStream_t s, bool pdl) {
-  using L = Lay<DH, RG>;
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = config(dim3(ctas), kThreads, L::SMEM, s, attr, pdl);
+  cudaLaunchConfig_t cfg = config(dim3(ctas), kThreads, Lay<DH, RG>::SMEM, s, attr, pdl);
   note_launch();
-  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<DH, RG>, sp);
-  if (e) return e;
-  cfg = config(dim3(ctas, (L::RB + 7) / 8), 256, 0, s, attr, pdl);
-  note_launch();
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<DH>, sp.a, (int)L::RB);
+  return cudaLaunchKernelEx(&cfg, paged_attn_kernel<DH, RG>, sp);
 }
 
 template <int DH>
@@ -536,39 +543,77 @@ cudaError_t paged_set_attributes() {
   cudaError_t e = set_head<32>();
   if (e == cudaSuccess) e = set_head<64>();
   if (e == cudaSuccess) e = set_head<128>();
+  if (e == cudaSuccess) e = paged_tc_set_attributes();
   return e;
 }
 
+// Packed rows of the largest sequence, as far as the host knows.
+static long long packed_rows(int n_rows, int max_rows, int G) {
+  return (long long)(max_rows > 0 && max_rows < n_rows ? max_rows : n_rows) * G;
+}
+
+// Sequences of more packed rows than a streaming block holds go to the tensor
+// cores (heads of 32 stay: their products are too thin for it).
+static bool wants_tc(long long packed, int Dh) { return packed > kStreamRows && Dh != 32; }
+
 size_t paged_attn_scratch_bytes(int n_rows, int max_rows, int G, int Dh) {
-  (void)n_rows;
-  (void)max_rows;
-  (void)G;
-  return region_bytes(2 * kMaxSms, kStreamRows, Dh);
+  return region_bytes(2 * kMaxSms, kStreamRows, Dh) +
+         (wants_tc(packed_rows(n_rows, max_rows, G), Dh) ? region_bytes(kMaxSms, kPagedTcRows, Dh) : 0);
 }
 
 cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const void *v_pages, int max_rows, void *scratch,
                               int sms, cudaStream_t s, bool pdl) {
+  const long long packed = packed_rows(args.n_rows, max_rows, args.G);
+  const bool tc = wants_tc(packed, args.Dh);
+  const uint64_t rows = (uint64_t)args.n_pages * args.Hkv * args.page;
+  const int n = sms < kMaxSms ? sms : kMaxSms;
+  char *base = static_cast<char *>(scratch);
+  CombineParams cp;
+  cp.tc_ctas = 0;
+  cp.tc = args;
+  cudaError_t e;
+  if (tc) {
+    PagedTcParams tp;
+    tp.a = args;
+    tp.a.rows_above = kStreamRows;
+    tp.a.rows_upto = 0x7fffffff;
+    tp.a.tpb = 2 * (128 / args.G);
+    tp.a.min_tiles = 2;
+    tp.a.late_wait = 0;
+    bind_region(tp.a, base + region_bytes(2 * kMaxSms, kStreamRows, args.Dh), n, kPagedTcRows);
+    if (!make_page_map(&tp.mk, k_pages, args.Dh, rows, args.page) ||
+        !make_page_map(&tp.mv, v_pages, args.Dh, rows, args.page) ||
+        !make_query_map(&tp.mq, args.q, args.Dh, args.Hq, args.n_rows, args.ldq, args.G, 128 / args.G))
+      return cudaErrorNotSupported;
+    if ((e = launch_paged_attn_tc(tp, n, s, pdl))) return e;
+    cp.tc = tp.a;
+    cp.tc_ctas = n;
+  }
   StreamParams sp;
   sp.a = args;
-  PagedArgs &a = sp.a;
-  const uint64_t rows = (uint64_t)a.n_pages * a.Hkv * a.page;
-  const uint32_t box = (uint32_t)(a.page < kTK ? a.page : kTK);
-  if (!make_page_map(&sp.mk, k_pages, a.Dh, rows, box) || !make_page_map(&sp.mv, v_pages, a.Dh, rows, box))
+  const int rb = packed <= 16 ? 16 : packed <= 32 ? 32 : 64, ctas = 2 * n;
+  sp.a.rows_above = 0;
+  sp.a.rows_upto = tc ? kStreamRows : 0x7fffffff;
+  sp.a.tpb = rb / args.G;
+  sp.a.min_tiles = 2;
+  sp.a.late_wait = tc && pdl;
+  if (const char *v = getenv("MTP_PAGED_MIN")) sp.a.min_tiles = atoi(v);
+  bind_region(sp.a, base, ctas, rb);
+  const uint32_t box = (uint32_t)(args.page < kTK ? args.page : kTK);
+  if (!make_page_map(&sp.mk, k_pages, args.Dh, rows, box) || !make_page_map(&sp.mv, v_pages, args.Dh, rows, box))
     return cudaErrorNotSupported;
-  const int pr = (max_rows > 0 && max_rows < a.n_rows ? max_rows : a.n_rows) <= kStreamRows
-                     ? (max_rows > 0 && max_rows < a.n_rows ? max_rows : a.n_rows) * a.G
-                     : kStreamRows + 1;
-  const int rb = pr <= 16 ? 16 : pr <= 32 ? 32 : 64;
-  const int ctas = 2 * (sms < kMaxSms ? sms : kMaxSms);
-  a.rows_above = 0;
-  a.rows_upto = 0x7fffffff;
-  a.tpb = rb / a.G;
-  a.min_tiles = 2;
-  if (const char *v = getenv("MTP_PAGED_MIN")) a.min_tiles = atoi(v);
-  bind_region(a, static_cast<char *>(scratch), ctas, rb);
-  if (a.Dh == 32) return launch_rows<32>(sp, rb, ctas, s, pdl);
-  if (a.Dh == 64) return launch_rows<64>(sp, rb, ctas, s, pdl);
-  return launch_rows<128>(sp, rb, ctas, s, pdl);
+  if (args.Dh == 32) e = launch_rows<32>(sp, rb, ctas, s, pdl);
+  else if (args.Dh == 64) e = launch_rows<64>(sp, rb, ctas, s, pdl);
+  else e = launch_rows<128>(sp, rb, ctas, s, pdl);
+  if (e) return e;
+  cp.st = sp.a;
+  cp.st_rows = rb;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config(dim3(cp.tc_ctas + ctas, tc ? 8 : (rb + 7) / 8), 256, 0, s, attr, pdl);
+  note_launch();
+  if (args.Dh == 32) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<32>, cp);
+  if (args.Dh == 64) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<64>, cp);
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<128>, cp);
 }
 
 MTP_TRACE_COLLECTOR(paged_attn)

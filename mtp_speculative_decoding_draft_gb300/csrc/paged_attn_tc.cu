@@ -1,0 +1,465 @@
+// Attention of a chunk of new tokens over a paged K/V cache: the tensor-core
+// kernel, for sequences with more packed rows (tokens x G) than the streaming
+// kernel's block.
+//
+// Bound by the two matrix products and by the exponentials between them.  A CTA
+// holds a block of two groups of 128 packed query rows of one K/V head; the
+// groups take turns on the tensor core, so that one group's softmax runs under
+// the other group's products:
+//   S_g = Q_g K_i^T     tcgen05.mma, both operands in shared memory by TMA
+//   P_g = 2^(S_g - m)   one thread a row: S from tensor memory, the maximum and
+//                       the sum in registers, P back over S as bf16
+//   O_g += P_g V_i      tcgen05.mma, P from tensor memory, V as it lies in its
+//                       pages (row-major keys: the MN-major form of operand B)
+// S_g i+1 is issued behind O_g += P_g V_i, so when a group's scores arrive its
+// accumulator is at rest, and the group's own threads rescale it: only when a
+// row's maximum grew by more than 2^8.
+//
+// Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1, 128 each; P_g lies in the
+// first half of S_g.  Warps 0-3 and 4-7 are the groups' softmax, warp 8 brings
+// pages by TMA into a ring of K and V tiles, warp 9 issues the products.
+#include "internal.h"
+#include "paged.cuh"
+#include "paged_tc.cuh"
+#include "tcgen05.cuh"
+
+namespace mtp {
+
+namespace {
+
+constexpr int kTK = 128;          // keys per tile
+constexpr int kThreads = 320;
+constexpr int kProducer = 8, kIssuer = 9;
+constexpr unsigned kFull = 0xffffffffu;
+
+template <int DH>
+struct Lay {
+  static constexpr int NB = DH / 64;               // 64-dim halves of a head
+  static constexpr int HALF = 128 * 128;           // bytes of a half: 128 rows of 128 bytes
+  static constexpr int TILE = NB * HALF;           // a K or V tile, or a group's queries
+  static constexpr int STAGES = DH == 128 ? 5 : 8;
+  static constexpr int RING = STAGES * TILE;
+  static constexpr size_t SMEM = (size_t)2 * TILE + RING + 512;
+  __host__ __device__ static constexpr uint32_t S(int g) { return 128u * g; }
+  __host__ __device__ static constexpr uint32_t O(int g) { return 256u + 128u * g; }
+};
+
+// D[tmem] (+)= A[tmem] * B[smem], issued by a single thread.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Descriptor of an operand whose rows (of 128 bytes, 128-byte swizzle) run along
+// K: 64 elements of N in a row, 8-row groups 1024 bytes apart (stride), the next
+// 64 of N one half further (leading).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t half_bytes) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(half_bytes >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+         ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+// 32 columns of this thread's lane, without the wait: the values are valid after
+// tmem_wait_ld() and pin32().
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Ties the registers of an asynchronous load to the wait before it: no use of
+// them is scheduled above this statement.
+__device__ __forceinline__ void pin32(uint32_t *r) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *m, int x, int y, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *m, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+}  // namespace
+
+template <int DH>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid_constant__ PagedTcParams sp) {
+  trace_start(kTkPagedAttnTc);
+  using L = Lay<DH>;
+  constexpr int NB = L::NB, ST = L::STAGES;
+  const PagedArgs &p = sp.a;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char *qbuf = smem;                      // [2 groups][halves][128][128 B]
+  unsigned char *ring = smem + 2 * L::TILE;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(ring + L::RING);
+  uint64_t *full = bars, *empty = bars + ST;       // ring
+  uint64_t *q_full = bars + 2 * ST, *q_empty = q_full + 1, *z_bar = q_full + 2, *drain = q_full + 3;
+  uint64_t *s_full = q_full + 4, *p_full = s_full + 2, *o_full = s_full + 4, *o_empty = s_full + 6;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 8);
+  long long *scratch = reinterpret_cast<long long *>(s_full + 9);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(z_bar, 1);
+    mbar_init(drain, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&s_full[g], 1);
+      mbar_init(&p_full[g], 4);
+      mbar_init(&o_full[g], 1);
+      mbar_init(&o_empty[g], 4);
+    }
+    fence_barrier_init();
+  }
+  grid_dep_wait();
+  trace_dep(kTkPagedAttnTc);
+  grid_dep_launch();
+  const PagedShare sh = paged_plan<kTK, kThreads>(p, scratch);
+  if (tid == 0) p.desc[blockIdx.x].rows = 0;
+  if (sh.start >= sh.end) {
+    trace_end(kTkPagedAttnTc);
+    return;
+  }
+  if (warp == kIssuer) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int tpg = 128 / p.G, rpg = tpg * p.G;      // tokens and packed rows of a group
+  bool ok = true;
+  PagedWalk<kTK> w(p, sh);
+
+  if (warp == kProducer) {
+    // ------------------------------------------------ pages into the ring
+    const int prow = min(p.page, kTK);             // rows of a piece: one page
+    const int npc = (kTK / prow) * NB;             // pieces of a tile (at most 16)
+    const int pc = lane / NB, hb = lane % NB;
+    int it = 0, seg = 0, zn = 0;
+    for (; w.valid() && ok; w.next(), ++seg) {
+      const int ng = w.t1() - w.t0 > tpg ? 2 : 1;
+      if (seg > 0) ok = mbar_wait(q_empty, (uint32_t)(seg - 1) & 1u, p.status);
+      ok = __all_sync(kFull, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full, (uint32_t)(ng * NB * rpg * 128));
+        for (int g = 0; g < ng; ++g)
+          for (int x = 0; x < NB; ++x)
+            tma_3d(qbuf + g * L::TILE + x * L::HALF, &sp.mq, 64 * x, w.h * p.G, w.s.row0 + w.t0 + g * tpg, q_full);
+      }
+      __syncwarp();
+      for (int i = w.i0; i < w.i1 && ok; ++i) {
+        const int t0 = w.r.tile(i) * kTK, k0 = t0 + pc * prow;
+        const bool need = lane < npc && w.r.any(k0, k0 + prow);
+        int y = 0;
+        if (need) y = (paged_page(p, w.b, k0) * p.Hkv + w.h) * p.page;
+        const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, need)) * prow * 128);
+        const bool whole = (t0 + kTK <= w.r.hi && t0 >= w.r.lo) || t0 + kTK <= w.r.sink_end;
+        for (int isv = 0; isv < 2 && ok; ++isv, ++it) {
+          const int s = it % ST;
+          if (it >= ST) ok = mbar_wait(&empty[s], (uint32_t)((it / ST) - 1) & 1u, p.status);
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          // Rows of V that no row sees (past the last key, before the window,
+          // never loaded) may hold anything, NaN too: in a tile that has such
+          // rows they are cleared before the tile is handed on.
+          const bool clear = isv && !whole;
+          uint64_t *bar = clear ? z_bar : &full[s];
+          unsigned char *dst = ring + (size_t)s * L::TILE;
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+          __syncwarp();
+          if (need) tma_2d(dst + hb * L::HALF + pc * prow * 128, isv ? &sp.mv : &sp.mk, 64 * hb, y, bar);
+          if (clear) {
+            ok = mbar_wait(z_bar, (uint32_t)(zn++) & 1u, p.status);
+            ok = __all_sync(kFull, ok);
+            for (int r = 0; r < kTK; ++r)
+              if (!w.r.sees(t0 + r) && lane < 8 * NB)
+                *reinterpret_cast<uint4 *>(dst + (lane >> 3) * L::HALF + r * 128 + (lane & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+          }
+        }
+      }
+    }
+    if (!ok)  // let copies still in flight land before the CTA exits
+      for (int i = max(0, it - ST); i < it; ++i)
+        if (!mbar_wait(&full[i % ST], (uint32_t)(i / ST) & 1u, p.status)) break;
+  } else if (warp == kIssuer) {
+    // ------------------------------------------------ matrix products
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16_f32(128, 128), id_o = idesc_bf16_f32(128, DH) | (1u << 16);
+      const uint32_t qa = smem_u32(qbuf), ra = smem_u32(ring);
+      int it = 0, seg = 0, np[2] = {0, 0}, no[2] = {0, 0};
+      auto scores = [&](int g, int stage) {
+#pragma unroll
+        for (int k = 0; k < DH / 16; ++k) {
+          const uint32_t off = (uint32_t)((k >> 2) * L::HALF + (k & 3) * 32);
+          mma_bf16(tmem + L::S(g), sw128_kmajor_desc(qa + g * L::TILE + off),
+                   sw128_kmajor_desc(ra + stage * L::TILE + off), id_s, k > 0);
+        }
+      };
+      auto output = [&](int g, int stage, bool first) {
+#pragma unroll
+        for (int k = 0; k < kTK / 16; ++k)
+          mma_ts(tmem + L::O(g), tmem + L::S(g) + 8 * k,
+                 sw128_mnmajor_desc(ra + stage * L::TILE + k * 2048, L::HALF), id_o, !first || k > 0);
+      };
+      for (; w.valid() && ok; w.next(), ++seg) {
+        const int ng = w.t1() - w.t0 > tpg ? 2 : 1, nt = w.i1 - w.i0;
+        ok = mbar_wait(q_full, (uint32_t)seg & 1u, p.status);
+        for (int i = 0; i <= nt && ok; ++i, it += 2) {
+          // tiles it (K_i) and it + 1 (V_i); V_{i-1} is it - 1
+          const int ks = it % ST, vs = (it + ST - 1) % ST;
+          if (i < nt) ok = mbar_wait(&full[ks], (uint32_t)(it / ST) & 1u, p.status);
+          if (ok && i > 0) ok = mbar_wait(&full[vs], (uint32_t)((it - 1) / ST) & 1u, p.status);
+          for (int g = 0; g < ng && ok; ++g) {
+            if (i > 0) {
+              ok = mbar_wait(&p_full[g], (uint32_t)(np[g]++) & 1u, p.status);
+              if (ok && i == 1) ok = mbar_wait(&o_empty[g], (uint32_t)((no[g]++) & 1) ^ 1u, p.status);
+              if (!ok) break;
+              tc_fence_after();
+              output(g, vs, i == 1);
+              if (i == nt) mma_commit(&o_full[g]);
+            }
+            if (i < nt) {
+              scores(g, ks);
+              mma_commit(&s_full[g]);
+            }
+          }
+          if (!ok) break;
+          if (i < nt) mma_commit(&empty[ks]);
+          if (i > 0) mma_commit(&empty[vs]);
+        }
+        it -= 2;  // the last round brought no K
+        if (ok) mma_commit(q_empty);
+      }
+      mma_commit(drain);  // nothing of this CTA is in flight when it frees its tensor memory
+      mbar_wait(drain, 0, p.status);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ softmax: a thread a row
+    const int g = warp >> 2, row = tid & 127;
+    const uint32_t lanebase = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanebase + L::S(g), to = tmem + lanebase + L::O(g);
+    int ns = 0, nseg = 0;
+    for (; w.valid() && ok; w.next()) {
+      const int ntok = w.t1() - w.t0;
+      if (g == 1 && ntok <= tpg) continue;
+      const int tg0 = w.t0 + g * tpg, tg1 = min(w.t1(), tg0 + tpg);  // the group's tokens
+      const int tok = min(tg0 + row / p.G, tg1 - 1);
+      const bool live = row < (tg1 - tg0) * p.G;
+      const int pos = w.s.ctx + tok;
+      const int rhi = min(pos + 1, p.cap), rlo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      const int all_hi = min(w.s.ctx + tg0 + 1, p.cap);
+      const int all_lo = p.window > 0 ? max(0, w.s.ctx + tg1 - 1 - p.window + 1) : 0;
+      float m = -INFINITY, l = 0.f;
+      for (int i = w.i0; i < w.i1; ++i) {
+        const int k0 = w.r.tile(i) * kTK;
+        const bool whole = k0 + kTK <= all_hi && (k0 >= all_lo || k0 + kTK <= min(p.sinks, all_hi));
+        ok = mbar_wait(&s_full[g], (uint32_t)(ns++) & 1u, p.status);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_async(ts + 32 * c, s + 32 * c);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) pin32(s + 32 * c);
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 128; ++e) {
+            const int j = k0 + e;
+            if (!(j < rhi && (j >= rlo || j < p.sinks))) s[e] = 0xff800000u;
+          }
+        }
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 128; ++e) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(s[e]));
+        const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
+        if (__any_sync(kFull, live && mx > m + 8.f)) {
+          const float n = fmaxf(m, mx);
+          const float f = n == m ? 1.f : exp2f(m - n);
+          m = n;
+          l *= f;
+          if (i > w.i0) {
+#pragma unroll
+            for (int c = 0; c < DH / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32_async(to + 32 * c, o);
+              tmem_wait_ld();
+              pin32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(to + 32 * c, o);
+            }
+          }
+        }
+        const float u = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float a = ex2_approx(fmaf(__uint_as_float(s[64 * c + 2 * e]), p.scale_log2, -u));
+            const float b = ex2_approx(fmaf(__uint_as_float(s[64 * c + 2 * e + 1]), p.scale_log2, -u));
+            sum[e & 3] += a + b;
+            pk[e] = pack2(a, b);
+          }
+          tmem_st32(ts + 32 * c, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[g]);
+      }
+      if (!ok) break;
+      // ---- the block's output, or this segment's state
+      ok = mbar_wait(&o_full[g], (uint32_t)(nseg++) & 1u, p.status);
+      ok = __all_sync(kFull, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole_item = w.starts() && w.ends();
+      const int slot = w.starts() ? 1 : 0;
+      const int qrow = w.s.row0 + tok, hq = w.h * p.G + row % p.G;
+      const bool mine = live && in_bounds(qrow < p.n_rows, p.status);
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const size_t pr = ((size_t)blockIdx.x * 2 + slot) * kPagedTcRows + g * rpg + row;
+#pragma unroll
+      for (int c = 0; c < DH / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32_async(to + 32 * c, o);
+        tmem_wait_ld();
+        pin32(o);
+        if (!mine) continue;
+        // O of a row without keys was multiplied by zero weights only: still zero
+        if (!whole_item || p.out_f32) {
+          float *d = whole_item ? static_cast<float *>(p.out) + (long long)qrow * p.ldo + hq * DH + 32 * c
+                                : p.part_o + pr * DH + 32 * c;
+          const float f = whole_item ? inv : 1.f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4 *>(d + e) =
+                make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f, __uint_as_float(o[e + 2]) * f,
+                            __uint_as_float(o[e + 3]) * f);
+        } else {
+          uint16_t *d = static_cast<uint16_t *>(p.out) + (long long)qrow * p.ldo + hq * DH + 32 * c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              v[j] = pack2(__uint_as_float(o[e + 2 * j]) * inv, __uint_as_float(o[e + 2 * j + 1]) * inv);
+            *reinterpret_cast<uint4 *>(d + e) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+      if (mine) {
+        if (!whole_item) {
+          p.part_ml[pr * 2] = m;
+          p.part_ml[pr * 2 + 1] = l;
+        } else if (p.lse) {
+          p.lse[(size_t)qrow * p.Hq + hq] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+      if (tid == 0 && w.starts() && !w.ends()) {
+        PagedDesc d;
+        d.row0 = w.s.row0 + w.t0;
+        d.rows = ntok * p.G;
+        d.h = w.h;
+        d.last_cta = (int)((w.pos + w.r.count - 1) / sh.per);
+        p.desc[blockIdx.x] = d;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_empty[g]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssuer) tmem_dealloc(tmem, 512);
+  trace_end(kTkPagedAttnTc);
+}
+
+// ---------------------------------------------------------------- host side
+
+cudaError_t paged_tc_set_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)Lay<128>::SMEM);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(paged_attn_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<64>::SMEM);
+  return e;
+}
+
+cudaError_t launch_paged_attn_tc(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sp.a.Dh == 128 ? Lay<128>::SMEM : Lay<64>::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  note_launch();
+  return sp.a.Dh == 128 ? cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<128>, sp)
+                        : cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<64>, sp);
+}
+
+MTP_TRACE_COLLECTOR(paged_attn_tc)
+
+}  // namespace mtp

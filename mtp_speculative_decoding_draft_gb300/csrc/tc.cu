@@ -30,7 +30,7 @@
 #include "common.cuh"
 #include "draft_ops.cuh"
 #include "internal.h"
-#include "paged.cuh"
+#include "paged_tc.cuh"
 #include "tcgen05.cuh"
 
 namespace mtp {
@@ -731,6 +731,18 @@ bool make_page_map(CUtensorMap *m, const void *base, int Dh, uint64_t rows, uint
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, Dh < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_query_map(CUtensorMap *m, const void *q, int Dh, int Hq, int n_rows, long long ldq, int G, int tokens) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)Dh, (cuuint64_t)Hq, (cuuint64_t)n_rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)Dh * 2, (cuuint64_t)ldq * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tokens};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 namespace {
