@@ -28,7 +28,7 @@ namespace mtp {
 namespace {
 
 constexpr int kTK = 128;          // keys per tile
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;   // three warpgroups: the registers move between whole ones
 constexpr int kProducer = 8, kIssuer = 9;
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -106,6 +106,44 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
 __device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *m, int x, int y, uint64_t *bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -136,9 +174,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
   uint64_t *bars = reinterpret_cast<uint64_t *>(ring + L::RING);
   uint64_t *full = bars, *empty = bars + ST;       // ring
   uint64_t *q_full = bars + 2 * ST, *q_empty = q_full + 1, *z_bar = q_full + 2, *drain = q_full + 3;
-  uint64_t *s_full = q_full + 4, *p_full = s_full + 2, *o_full = s_full + 4, *o_empty = s_full + 6;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 8);
-  long long *scratch = reinterpret_cast<long long *>(s_full + 9);
+  uint64_t *s_full = q_full + 4, *p_full = s_full + 2, *o_full = s_full + 4, *o_empty = s_full + 6,
+           *p_half = s_full + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 10);
+  long long *scratch = reinterpret_cast<long long *>(s_full + 11);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -153,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
     for (int g = 0; g < 2; ++g) {
       mbar_init(&s_full[g], 1);
       mbar_init(&p_full[g], 4);
+      mbar_init(&p_half[g], 4);
       mbar_init(&o_full[g], 1);
       mbar_init(&o_empty[g], 4);
     }
@@ -177,116 +217,146 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
   bool ok = true;
   PagedWalk<kTK> w(p, sh);
 
-  if (warp == kProducer) {
-    // ------------------------------------------------ pages into the ring
-    const int prow = min(p.page, kTK);             // rows of a piece: one page
-    const int npc = (kTK / prow) * NB;             // pieces of a tile (at most 16)
-    const int pc = lane / NB, hb = lane % NB;
-    int it = 0, seg = 0, zn = 0;
-    for (; w.valid() && ok; w.next(), ++seg) {
-      const int ng = w.t1() - w.t0 > tpg ? 2 : 1;
-      if (seg > 0) ok = mbar_wait(q_empty, (uint32_t)(seg - 1) & 1u, p.status);
-      ok = __all_sync(kFull, ok);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, (uint32_t)(ng * NB * rpg * 128));
-        for (int g = 0; g < ng; ++g)
-          for (int x = 0; x < NB; ++x)
-            tma_3d(qbuf + g * L::TILE + x * L::HALF, &sp.mq, 64 * x, w.h * p.G, w.s.row0 + w.t0 + g * tpg, q_full);
-      }
-      __syncwarp();
-      for (int i = w.i0; i < w.i1 && ok; ++i) {
-        const int t0 = w.r.tile(i) * kTK, k0 = t0 + pc * prow;
-        const bool need = lane < npc && w.r.any(k0, k0 + prow);
-        int y = 0;
-        if (need) y = (paged_page(p, w.b, k0) * p.Hkv + w.h) * p.page;
-        const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, need)) * prow * 128);
-        const bool whole = (t0 + kTK <= w.r.hi && t0 >= w.r.lo) || t0 + kTK <= w.r.sink_end;
-        for (int isv = 0; isv < 2 && ok; ++isv, ++it) {
-          const int s = it % ST;
-          if (it >= ST) ok = mbar_wait(&empty[s], (uint32_t)((it / ST) - 1) & 1u, p.status);
-          ok = __all_sync(kFull, ok);
-          if (!ok) break;
-          // Rows of V that no row sees (past the last key, before the window,
-          // never loaded) may hold anything, NaN too: in a tile that has such
-          // rows they are cleared before the tile is handed on.
-          const bool clear = isv && !whole;
-          uint64_t *bar = clear ? z_bar : &full[s];
-          unsigned char *dst = ring + (size_t)s * L::TILE;
-          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-          __syncwarp();
-          if (need) tma_2d(dst + hb * L::HALF + pc * prow * 128, isv ? &sp.mv : &sp.mk, 64 * hb, y, bar);
-          if (clear) {
-            ok = mbar_wait(z_bar, (uint32_t)(zn++) & 1u, p.status);
+  // The launch gives every thread 168 registers, 384 x 168 = 64512 in all; the
+  // third warpgroup needs few, a softmax row in registers needs more:
+  // 256 x 216 + 128 x 72 = 64512.
+  if (warp >= kProducer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kProducer) {
+      // ------------------------------------------------ pages into the ring
+      const int prow = min(p.page, kTK);             // rows of a piece: one page
+      const int npc = (kTK / prow) * NB;             // pieces of a tile (at most 16)
+      const int pc = lane / NB, hb = lane % NB;
+      int it = 0, seg = 0, zn = 0;
+      for (; w.valid() && ok; w.next(), ++seg) {
+        const int ng = w.t1() - w.t0 > tpg ? 2 : 1;
+        if (seg > 0) ok = mbar_wait(q_empty, (uint32_t)(seg - 1) & 1u, p.status);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full, (uint32_t)(ng * NB * rpg * 128));
+          for (int g = 0; g < ng; ++g)
+            for (int x = 0; x < NB; ++x)
+              tma_3d(qbuf + g * L::TILE + x * L::HALF, &sp.mq, 64 * x, w.h * p.G, w.s.row0 + w.t0 + g * tpg, q_full);
+        }
+        __syncwarp();
+        for (int i = w.i0; i < w.i1 && ok; ++i) {
+          const int t0 = w.r.tile(i) * kTK, k0 = t0 + pc * prow;
+          const bool need = lane < npc && w.r.any(k0, k0 + prow);
+          int y = 0;
+          if (need) y = (paged_page(p, w.b, k0) * p.Hkv + w.h) * p.page;
+          const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, need)) * prow * 128);
+          const bool whole = (t0 + kTK <= w.r.hi && t0 >= w.r.lo) || t0 + kTK <= w.r.sink_end;
+          for (int isv = 0; isv < 2 && ok; ++isv, ++it) {
+            const int s = it % ST;
+            if (it >= ST) ok = mbar_wait(&empty[s], (uint32_t)((it / ST) - 1) & 1u, p.status);
             ok = __all_sync(kFull, ok);
-            for (int r = 0; r < kTK; ++r)
-              if (!w.r.sees(t0 + r) && lane < 8 * NB)
-                *reinterpret_cast<uint4 *>(dst + (lane >> 3) * L::HALF + r * 128 + (lane & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
+            if (!ok) break;
+            // Rows of V that no row sees (past the last key, before the window,
+            // never loaded) may hold anything, NaN too: in a tile that has such
+            // rows they are cleared before the tile is handed on.
+            const bool clear = isv && !whole;
+            uint64_t *bar = clear ? z_bar : &full[s];
+            unsigned char *dst = ring + (size_t)s * L::TILE;
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[s]);
+            if (need) tma_2d(dst + hb * L::HALF + pc * prow * 128, isv ? &sp.mv : &sp.mk, 64 * hb, y, bar);
+            if (clear) {
+              ok = mbar_wait(z_bar, (uint32_t)(zn++) & 1u, p.status);
+              ok = __all_sync(kFull, ok);
+              for (int r = 0; r < kTK; ++r)
+                if (!w.r.sees(t0 + r) && lane < 8 * NB)
+                  *reinterpret_cast<uint4 *>(dst + (lane >> 3) * L::HALF + r * 128 + (lane & 7) * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&full[s]);
+            }
           }
         }
       }
-    }
-    if (!ok)  // let copies still in flight land before the CTA exits
-      for (int i = max(0, it - ST); i < it; ++i)
-        if (!mbar_wait(&full[i % ST], (uint32_t)(i / ST) & 1u, p.status)) break;
-  } else if (warp == kIssuer) {
-    // ------------------------------------------------ matrix products
-    if (lane == 0) {
+      if (!ok)  // let copies still in flight land before the CTA exits
+        for (int i = max(0, it - ST); i < it; ++i)
+          if (!mbar_wait(&full[i % ST], (uint32_t)(i / ST) & 1u, p.status)) break;
+    } else if (warp == kIssuer) {
+      // ------------------------------------------------ matrix products
+      // The whole warp walks and waits, one elected lane issues.  Loop bounds,
+      // addresses and the tensor-memory base are warp-uniform by construction
+      // (shuffles and votes), so that the operands sit in uniform registers: an
+      // issue loop under `lane == 0` took about 125 cycles an instruction, twice
+      // what the instruction itself takes.
       constexpr uint32_t id_s = idesc_bf16_f32(128, 128), id_o = idesc_bf16_f32(128, DH) | (1u << 16);
-      const uint32_t qa = smem_u32(qbuf), ra = smem_u32(ring);
+      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+      const uint64_t qd = sw128_kmajor_desc(smem_u32(qbuf)), kd = sw128_kmajor_desc(smem_u32(ring)),
+                     vd = sw128_mnmajor_desc(smem_u32(ring), L::HALF);
+      const bool leader = elect_one();
       int it = 0, seg = 0, np[2] = {0, 0}, no[2] = {0, 0};
-      auto scores = [&](int g, int stage) {
-#pragma unroll
-        for (int k = 0; k < DH / 16; ++k) {
-          const uint32_t off = (uint32_t)((k >> 2) * L::HALF + (k & 3) * 32);
-          mma_bf16(tmem + L::S(g), sw128_kmajor_desc(qa + g * L::TILE + off),
-                   sw128_kmajor_desc(ra + stage * L::TILE + off), id_s, k > 0);
-        }
-      };
-      auto output = [&](int g, int stage, bool first) {
-#pragma unroll
-        for (int k = 0; k < kTK / 16; ++k)
-          mma_ts(tmem + L::O(g), tmem + L::S(g) + 8 * k,
-                 sw128_mnmajor_desc(ra + stage * L::TILE + k * 2048, L::HALF), id_o, !first || k > 0);
-      };
-      for (; w.valid() && ok; w.next(), ++seg) {
-        const int ng = w.t1() - w.t0 > tpg ? 2 : 1, nt = w.i1 - w.i0;
-        ok = mbar_wait(q_full, (uint32_t)seg & 1u, p.status);
+      for (; __shfl_sync(kFull, w.valid() && ok, 0); w.next(), ++seg) {
+        const int ng = __shfl_sync(kFull, w.t1() - w.t0 > tpg ? 2 : 1, 0), nt = __shfl_sync(kFull, w.i1 - w.i0, 0);
+        ok = __all_sync(kFull, mbar_wait(q_full, (uint32_t)seg & 1u, p.status));
         for (int i = 0; i <= nt && ok; ++i, it += 2) {
           // tiles it (K_i) and it + 1 (V_i); V_{i-1} is it - 1
           const int ks = it % ST, vs = (it + ST - 1) % ST;
-          if (i < nt) ok = mbar_wait(&full[ks], (uint32_t)(it / ST) & 1u, p.status);
-          if (ok && i > 0) ok = mbar_wait(&full[vs], (uint32_t)((it - 1) / ST) & 1u, p.status);
-          for (int g = 0; g < ng && ok; ++g) {
+          if (i > 0) ok = __all_sync(kFull, mbar_wait(&full[vs], (uint32_t)((it - 1) / ST) & 1u, p.status));
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (g >= ng || !ok) break;
             if (i > 0) {
-              ok = mbar_wait(&p_full[g], (uint32_t)(np[g]++) & 1u, p.status);
+              ok = mbar_wait(&p_half[g], (uint32_t)np[g] & 1u, p.status);
               if (ok && i == 1) ok = mbar_wait(&o_empty[g], (uint32_t)((no[g]++) & 1) ^ 1u, p.status);
+              ok = __all_sync(kFull, ok);
               if (!ok) break;
               tc_fence_after();
-              output(g, vs, i == 1);
-              if (i == nt) mma_commit(&o_full[g]);
+              if (leader) {
+                const uint64_t v = vd + (uint64_t)(vs * (L::TILE >> 4));
+#pragma unroll
+                for (int k = 0; k < kTK / 32; ++k)
+                  mma_ts(tm + L::O(g), tm + L::S(g) + 8 * k, v + (uint64_t)(k * (2048 >> 4)), id_o, k > 0 || i > 1);
+              }
+              __syncwarp();
+              ok = __all_sync(kFull, mbar_wait(&p_full[g], (uint32_t)(np[g]++) & 1u, p.status));
+              if (!ok) break;
+              tc_fence_after();
+              if (leader) {
+                const uint64_t v = vd + (uint64_t)(vs * (L::TILE >> 4));
+#pragma unroll
+                for (int k = kTK / 32; k < kTK / 16; ++k)
+                  mma_ts(tm + L::O(g), tm + L::S(g) + 8 * k, v + (uint64_t)(k * (2048 >> 4)), id_o, 1u);
+                if (i == nt) mma_commit(&o_full[g]);
+              }
             }
-            if (i < nt) {
-              scores(g, ks);
+            if (i < nt && g == 0) {
+              ok = __all_sync(kFull, mbar_wait(&full[ks], (uint32_t)(it / ST) & 1u, p.status));
+              if (!ok) break;
+            }
+            if (i < nt && leader) {
+              const uint64_t q = qd + (uint64_t)(g * (L::TILE >> 4)), kk = kd + (uint64_t)(ks * (L::TILE >> 4));
+#pragma unroll
+              for (int k = 0; k < DH / 16; ++k) {
+                const uint64_t off = (uint64_t)(((k >> 2) * L::HALF + (k & 3) * 32) >> 4);
+                mma_bf16(tm + L::S(g), q + off, kk + off, id_s, k > 0);
+              }
               mma_commit(&s_full[g]);
             }
+            __syncwarp();
           }
           if (!ok) break;
-          if (i < nt) mma_commit(&empty[ks]);
-          if (i > 0) mma_commit(&empty[vs]);
+          if (leader) {
+            if (i < nt) mma_commit(&empty[ks]);
+            if (i > 0) mma_commit(&empty[vs]);
+          }
+          __syncwarp();
         }
         it -= 2;  // the last round brought no K
-        if (ok) mma_commit(q_empty);
+        if (ok && leader) mma_commit(q_empty);
+        __syncwarp();
       }
-      mma_commit(drain);  // nothing of this CTA is in flight when it frees its tensor memory
+      if (leader) mma_commit(drain);  // nothing of this CTA is in flight when it frees its tensor memory
+      __syncwarp();
       mbar_wait(drain, 0, p.status);
     }
-    __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ------------------------------------------------ softmax: a thread a row
     const int g = warp >> 2, row = tid & 127;
     const uint32_t lanebase = (uint32_t)((warp & 3) * 32) << 16;
@@ -325,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         }
         float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 128; ++e) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(s[e]));
+        for (int e = 0; e < 128; e += 2) x[(e >> 1) & 3] = max3(x[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
         if (__any_sync(kFull, live && mx > m + 8.f)) {
           const float n = fmaxf(m, mx);
@@ -346,24 +416,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
           }
         }
         const float u = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nu2 = make_float2(-u, -u);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float a = ex2_approx(fmaf(__uint_as_float(s[64 * c + 2 * e]), p.scale_log2, -u));
-            const float b = ex2_approx(fmaf(__uint_as_float(s[64 * c + 2 * e + 1]), p.scale_log2, -u));
-            sum[e & 3] += a + b;
-            pk[e] = pack2(a, b);
+            float2 y = fma2(make_float2(__uint_as_float(s[64 * c + 2 * e]), __uint_as_float(s[64 * c + 2 * e + 1])), sc2, nu2);
+            y.x = ex2_approx(y.x);
+            y.y = ex2_approx(y.y);
+            sum[e & 1] = add2(sum[e & 1], y);
+            pk[e] = pack2(y.x, y.y);
           }
           tmem_st32(ts + 32 * c, pk);
+          // the product over the first half of the keys starts under the second half's exponentials
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(c == 0 ? &p_half[g] : &p_full[g]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[g]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
       // ---- the block's output, or this segment's state
