@@ -12,11 +12,14 @@
 // exactly to pos * 2^-65 turns: one 64-bit integer product, no wide floating
 // point.  sincospif of that fraction is accurate to fp32.
 //
-// The kernel is bound by its bytes (each row read and written once).  A CTA
-// takes one row at a time: every thread first issues the loads of its items
-// (pairs of VEC elements that rotate together), then rot/2 threads compute the
-// row's sines and cosines once for all heads, and after a barrier the items are
-// rotated and stored.
+// The kernel is bound by its bytes (each row read and written once).  A warp
+// takes one unit, a run of 32 x U items of one row (an item: the two vectors of
+// VEC elements that rotate together), with no barrier between warps: it issues
+// its items' loads first, finds the row's sequence and position under them,
+// computes the row's rot/2 sines and cosines two a lane into its own corner of
+// shared memory, then rotates and stores.  Recomputing the sines for the four
+// units of a row costs less than a block-wide barrier a row: 8190 rows of 40 + 16
+// heads of 128 took 96 us with a block a row.
 #include "internal.h"
 #include "paged.cuh"
 
@@ -24,8 +27,8 @@ namespace mtp {
 
 namespace {
 
-constexpr int kAppThreads = 384;
-constexpr int kAppItems = 2;  // items a thread holds at a time
+constexpr int kAppWarps = 8;
+constexpr unsigned kFull = 0xffffffffu;
 
 template <int VEC>
 struct Bf;
@@ -62,168 +65,164 @@ __device__ __forceinline__ typename Bf<VEC>::T pack(const float (&x)[VEC]) {
 
 }  // namespace
 
-template <int VEC>
-__global__ void __launch_bounds__(kAppThreads) cache_append_kernel(const __grid_constant__ AppendArgs p) {
+// How many of the B sequences start at or before `row` (32 probes a round).
+__device__ __forceinline__ int starts_upto(const int *row_start, int B, int row, int lane) {
+  int lo = 0, n = B;
+  while (n > 0) {
+    const int step = (n + 31) / 32, i = lane * step;
+    const int c = __popc(__ballot_sync(kFull, i < n && __ldcg(&row_start[lo + i]) <= row));
+    if (c == 0) break;
+    lo += (c - 1) * step + 1;
+    n = min(step - 1, n - ((c - 1) * step + 1));
+  }
+  return lo;
+}
+
+template <int VEC, int U>
+__global__ void __launch_bounds__(32 * kAppWarps) cache_append_kernel(const __grid_constant__ AppendArgs p) {
   trace_start(kTkAppend);
   using T = typename Bf<VEC>::T;
-  __shared__ float2 cs[64];  // rot / 2 <= 64
-  const int tid = threadIdx.x;
-  grid_dep_wait();
-  trace_dep(kTkAppend);
-  grid_dep_launch();
+  __shared__ float2 cs_all[kAppWarps][64];  // rot / 2 <= 64
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float2 *cs = cs_all[warp];
   const int iph = p.Dh / (2 * VEC);                 // items of a head
   const int rph = p.rot / (2 * VEC);                // of them, rotated
   const int q_items = p.q ? p.Hq * iph : 0, kv_items = p.Hkv * iph;
-  const int items = q_items + 2 * kv_items;
+  const int items = q_items + 2 * kv_items, upr = (items + 32 * U - 1) / (32 * U);
+  const long long unit = (long long)blockIdx.x * kAppWarps + warp;
+  const int row = (int)(unit / upr), first = (int)(unit % upr) * 32 * U;
   const bool half = p.layout == 0;
-
-  for (int row = blockIdx.x; row < p.n_rows; row += gridDim.x) {
-    // ---- the first items' loads need no position
-    T a[kAppItems], c[kAppItems];
-    auto locate = [&](int it, const uint16_t *&src, int &which, int &head, int &e0, int &e1, bool &rot) {
-      which = it < q_items ? 0 : it < q_items + kv_items ? 1 : 2;
-      const int i = which == 0 ? it : which == 1 ? it - q_items : it - q_items - kv_items;
-      head = i / iph;
-      const int u = i - head * iph;
-      rot = which < 2 && u < rph;
-      if (rot && half) {
-        e0 = u * VEC;
-        e1 = e0 + p.rot / 2;
-      } else {
-        e0 = 2 * u * VEC;
-        e1 = e0 + VEC;
-      }
-      const void *base = which == 0 ? p.q : which == 1 ? p.k : p.v;
-      const long long ld = which == 0 ? p.ldq : which == 1 ? p.ldk : p.ldv;
-      src = static_cast<const uint16_t *>(base) + (long long)row * ld + head * p.Dh;
-    };
-    auto load = [&](int it0) {
-#pragma unroll
-      for (int n = 0; n < kAppItems; ++n) {
-        const int it = it0 + n * kAppThreads;
-        if (it < items) {
-          const uint16_t *src;
-          int which, head, e0, e1;
-          bool rot;
-          locate(it, src, which, head, e0, e1, rot);
-          a[n] = __ldcg(reinterpret_cast<const T *>(src + e0));
-          c[n] = __ldcg(reinterpret_cast<const T *>(src + e1));
-        }
-      }
-    };
-    const bool f32q = p.q_f32 != 0;
-    if (!f32q) load(tid);
-
-    // ---- the row's sequence: the last one that starts at or before the row
-    int below = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kAppThreads) {
-      const int b = b0 + tid;
-      below += __syncthreads_count(b < p.B && __ldcg(&p.row_start[b]) <= row);
+  grid_dep_wait();
+  trace_dep(kTkAppend);
+  grid_dep_launch();
+  if (blockIdx.x == 0) {  // once per call: are the row starts in order and inside the rows?
+    bool bad = false;
+    for (int i = threadIdx.x; i < p.B; i += 32 * kAppWarps) {
+      const int x = __ldcg(&p.row_start[i]), y = __ldcg(&p.row_start[i + 1]);
+      bad |= x < 0 || y < x || y > p.n_rows;
     }
-    // sequences that start at the same row are empty but the last of them
-    const int b = below - 1;
-    int pos = 0, page = -1;
-    bool real = b >= 0 && row < __ldcg(&p.row_start[b + 1]);
+    if (bad) set_status(p.status, kStatusBadRows);
+  }
+  if (row >= p.n_rows) {
+    trace_end(kTkAppend);
+    return;
+  }
+
+  // ---- the items' loads need no position
+  T a[U], c[U];
+  int which[U], head[U], e0[U], e1[U];
+  bool rot[U];
+#pragma unroll
+  for (int n = 0; n < U; ++n) {
+    const int it = first + n * 32 + lane;
+    which[n] = it >= items ? -1 : it < q_items ? 0 : it < q_items + kv_items ? 1 : 2;
+    const int i = which[n] == 1 ? it - q_items : which[n] == 2 ? it - q_items - kv_items : it;
+    head[n] = i / iph;
+    const int u = i - head[n] * iph;
+    rot[n] = which[n] < 2 && u < rph;
+    e0[n] = rot[n] && half ? u * VEC : 2 * u * VEC;
+    e1[n] = rot[n] && half ? e0[n] + p.rot / 2 : e0[n] + VEC;
+    if (which[n] >= 0 && !(p.q_f32 && which[n] == 0)) {
+      const void *base = which[n] == 0 ? p.q : which[n] == 1 ? p.k : p.v;
+      const long long ld = which[n] == 0 ? p.ldq : which[n] == 1 ? p.ldk : p.ldv;
+      const uint16_t *src = static_cast<const uint16_t *>(base) + (long long)row * ld + head[n] * p.Dh;
+      a[n] = __ldcs(reinterpret_cast<const T *>(src + e0[n]));
+      c[n] = __ldcs(reinterpret_cast<const T *>(src + e1[n]));
+    }
+  }
+
+  // ---- the row's sequence: the last one that starts at or before it (those that
+  // start at the same row are empty but the last of them)
+  const int b = starts_upto(p.row_start, p.B, row, lane) - 1;
+  bool real = false;
+  int pos = 0, page = -1;
+  if (b >= 0) {
+    const int s0 = __ldcg(&p.row_start[b]), s1 = __ldcg(&p.row_start[b + 1]), c0 = __ldcg(&p.ctx_len[b]);
+    const int ctx = min(max(c0, 0), p.cap);
+    real = row < s1 && s0 >= 0 && row >= s0;
+    pos = ctx + row - s0;
     if (real) {
-      const int s0 = __ldcg(&p.row_start[b]), c0 = __ldcg(&p.ctx_len[b]);
-      const int ctx = min(max(c0, 0), p.cap);
-      real = s0 >= 0;
-      pos = ctx + row - s0;
-      if (tid == 0 && (c0 != ctx || pos >= p.cap)) set_status(p.status, kStatusBadCtx);
+      if (lane == 0 && (c0 != ctx || pos >= p.cap)) set_status(p.status, kStatusBadCtx);
       if (pos < p.cap) {
         page = __ldg(&p.page_table[(size_t)b * p.max_pages + (pos >> p.page_shift)]);
         if (page < 0 || page >= p.n_pages) {
-          if (tid == 0) set_status(p.status, kStatusBadPage);
+          if (lane == 0) set_status(p.status, kStatusBadPage);
           page = -1;
         }
       }
     }
-    if (row == blockIdx.x && blockIdx.x == 0) {  // once per call: are the row starts in order and inside the rows?
-      bool bad = false;
-      for (int i = tid; i < p.B; i += kAppThreads) {
-        const int x = __ldcg(&p.row_start[i]), y = __ldcg(&p.row_start[i + 1]);
-        bad |= x < 0 || y < x || y > p.n_rows;
-      }
-      if (bad) set_status(p.status, kStatusBadRows);
-    }
-    if (real && tid < p.rot / 2) {
-      const unsigned long long t = (unsigned long long)(unsigned)pos * p.turns[tid];
+  }
+  if (!real) {
+    trace_end(kTkAppend);
+    return;
+  }
+  if (first < q_items + kv_items) {  // not values only
+    for (int t = lane; t < p.rot / 2; t += 32) {
+      const unsigned long long f = (unsigned long long)(unsigned)pos * __ldg(&p.turns[t]);
       // the top 32 bits as a signed fraction of a half turn: [-1, 1)
-      const float x = (float)((long long)t >> 32) * 4.656612873077393e-10f;
+      const float x = (float)(int)(f >> 32) * 4.656612873077393e-10f;
       float sn, co;
       sincospif(x, &sn, &co);
-      cs[tid] = make_float2(co * p.scale, sn * p.scale);
+      cs[t] = make_float2(co * p.scale, sn * p.scale);
     }
-    __syncthreads();
-    if (real) {
-      for (int it0 = tid; it0 < items; it0 += kAppItems * kAppThreads) {
-        if (it0 != tid && !f32q) load(it0);
+    __syncwarp();
+  }
 #pragma unroll
-        for (int n = 0; n < kAppItems; ++n) {
-          const int it = it0 + n * kAppThreads;
-          if (it >= items) continue;
-          const uint16_t *src;
-          int which, head, e0, e1;
-          bool rot;
-          locate(it, src, which, head, e0, e1, rot);
-          float x[VEC], y[VEC];
-          if (f32q && which == 0) {  // fp32 queries, rounded once after the rotation
-            const float *qs = static_cast<const float *>(p.q) + (long long)row * p.ldq + head * p.Dh;
+  for (int n = 0; n < U; ++n) {
+    if (which[n] < 0) continue;
+    float x[VEC], y[VEC];
+    if (p.q_f32 && which[n] == 0) {  // fp32 queries, rounded once, after the rotation
+      const float *qs = static_cast<const float *>(p.q) + (long long)row * p.ldq + head[n] * p.Dh;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              x[i] = __ldcg(qs + e0 + i);
-              y[i] = __ldcg(qs + e1 + i);
-            }
-          } else {
-            if (f32q) {
-              a[n] = __ldcg(reinterpret_cast<const T *>(src + e0));
-              c[n] = __ldcg(reinterpret_cast<const T *>(src + e1));
-            }
-            unpack<VEC>(a[n], x);
-            unpack<VEC>(c[n], y);
-          }
-          if (rot && half) {
+      for (int i = 0; i < VEC; ++i) {
+        x[i] = __ldcg(qs + e0[n] + i);
+        y[i] = __ldcg(qs + e1[n] + i);
+      }
+    } else {
+      unpack<VEC>(a[n], x);
+      unpack<VEC>(c[n], y);
+    }
+    if (rot[n] && half) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              const float2 f = cs[e0 + i];
-              const float x0 = x[i], x1 = y[i];
-              x[i] = x0 * f.x - x1 * f.y;
-              y[i] = x1 * f.x + x0 * f.y;
-            }
-          } else if (rot) {
+      for (int i = 0; i < VEC; ++i) {
+        const float2 f = cs[e0[n] + i];
+        const float x0 = x[i], x1 = y[i];
+        x[i] = x0 * f.x - x1 * f.y;
+        y[i] = x1 * f.x + x0 * f.y;
+      }
+    } else if (rot[n]) {
 #pragma unroll
-            for (int i = 0; i < VEC / 2; ++i) {
-              const float2 f = cs[e0 / 2 + i], g = cs[e1 / 2 + i];
-              const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
-              x[2 * i] = x0 * f.x - x1 * f.y;
-              x[2 * i + 1] = x1 * f.x + x0 * f.y;
-              y[2 * i] = y0 * g.x - y1 * g.y;
-              y[2 * i + 1] = y1 * g.x + y0 * g.y;
-            }
-          }
-          uint16_t *dst;
-          if (which == 0) {
-            dst = static_cast<uint16_t *>(p.q_out) + (long long)row * p.ldqo + head * p.Dh;
-          } else {
-            if (page < 0) continue;
-            dst = (which == 1 ? p.k_pages : p.v_pages) +
-                  (((size_t)page * p.Hkv + head) * p.page + (pos & (p.page - 1))) * p.Dh;
-          }
-          *reinterpret_cast<T *>(dst + e0) = pack<VEC>(x);
-          *reinterpret_cast<T *>(dst + e1) = pack<VEC>(y);
-        }
+      for (int i = 0; i < VEC / 2; ++i) {
+        const float2 f = cs[e0[n] / 2 + i], g = cs[e1[n] / 2 + i];
+        const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
+        x[2 * i] = x0 * f.x - x1 * f.y;
+        x[2 * i + 1] = x1 * f.x + x0 * f.y;
+        y[2 * i] = y0 * g.x - y1 * g.y;
+        y[2 * i + 1] = y1 * g.x + y0 * g.y;
       }
     }
-    __syncthreads();  // the sines are the next row's
+    uint16_t *dst;
+    if (which[n] == 0) {
+      dst = static_cast<uint16_t *>(p.q_out) + (long long)row * p.ldqo + head[n] * p.Dh;
+    } else {
+      if (page < 0) continue;
+      dst = (which[n] == 1 ? p.k_pages : p.v_pages) +
+            (((size_t)page * p.Hkv + head[n]) * p.page + (pos & (p.page - 1))) * p.Dh;
+    }
+    *reinterpret_cast<T *>(dst + e0[n]) = pack<VEC>(x);
+    *reinterpret_cast<T *>(dst + e1[n]) = pack<VEC>(y);
   }
   trace_end(kTkAppend);
 }
 
-cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t s, bool pdl) {
+namespace {
+
+template <int VEC, int U>
+cudaError_t launch_append(const AppendArgs &a, int items, cudaStream_t s, bool pdl) {
+  const long long units = (long long)a.n_rows * ((items + 32 * U - 1) / (32 * U));
   cudaLaunchConfig_t cfg{};
-  const int grid = a.n_rows < 152 * 40 ? a.n_rows : 152 * 40;
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kAppThreads);
+  cfg.gridDim = dim3((unsigned)((units + kAppWarps - 1) / kAppWarps));
+  cfg.blockDim = dim3(32 * kAppWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -231,9 +230,19 @@ cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t s, bool pdl) {
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   note_launch();
+  return cudaLaunchKernelEx(&cfg, cache_append_kernel<VEC, U>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t s, bool pdl) {
   // 16-byte accesses need the pairs' halves in whole vectors
-  if (a.rot % 16 == 0) return cudaLaunchKernelEx(&cfg, cache_append_kernel<8>, a);
-  return cudaLaunchKernelEx(&cfg, cache_append_kernel<4>, a);
+  const bool wide = a.rot % 16 == 0;
+  const int items = (a.Hq + 2 * a.Hkv) * a.Dh / (wide ? 16 : 8);
+  // few rows: an item a lane, more warps, the shortest chain
+  if ((long long)a.n_rows * items < 152ll * 2048)
+    return wide ? launch_append<8, 1>(a, items, s, pdl) : launch_append<4, 1>(a, items, s, pdl);
+  return wide ? launch_append<8, 4>(a, items, s, pdl) : launch_append<4, 4>(a, items, s, pdl);
 }
 
 MTP_TRACE_COLLECTOR(cache_append)

@@ -135,12 +135,18 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     const int pc = lane / (2 * NB), hb = (lane % (2 * NB)) % NB, isv = (lane % (2 * NB)) / NB;
     int issued = 0;
     for (; w.valid() && ok; w.next()) {
-      for (int i = w.i0; i < w.i1 && ok; ++i, ++it) {
-        const int s = it % kStages;
+      // the piece of this lane in tile i: whether a row sees it, and its row of the pool
+      auto locate = [&](int i, bool &need, int &y) {
         const int k0 = w.r.tile(i) * kTK + pc * prow;
-        const bool need = lane < npc && w.r.any(k0, k0 + prow);
-        int y = 0;
-        if (need) y = (paged_page(p, w.b, k0) * p.Hkv + w.h) * p.page + (k0 & (p.page - 1));
+        need = lane < npc && w.r.any(k0, k0 + prow);
+        y = need ? (paged_page(p, w.b, k0) * p.Hkv + w.h) * p.page + (k0 & (p.page - 1)) : 0;
+      };
+      bool need, need_next = false;
+      int y, y_next = 0;
+      locate(w.i0, need, y);
+      for (int i = w.i0; i < w.i1 && ok; ++i, ++it, need = need_next, y = y_next) {
+        const int s = it % kStages;
+        if (i + 1 < w.i1) locate(i + 1, need_next, y_next);  // its table entry loads under this tile's wait
         if (it >= kStages) ok = mbar_wait(&empty[s], (uint32_t)((it / kStages) - 1) & 1u, p.status);
         ok = __all_sync(kFull, ok);
         if (!ok) break;
@@ -595,9 +601,8 @@ cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const 
   sp.a.rows_above = 0;
   sp.a.rows_upto = tc ? kStreamRows : 0x7fffffff;
   sp.a.tpb = rb / args.G;
-  sp.a.min_tiles = 2;
+  sp.a.min_tiles = 4;
   sp.a.late_wait = tc && pdl;
-  if (const char *v = getenv("MTP_PAGED_MIN")) sp.a.min_tiles = atoi(v);
   bind_region(sp.a, base, ctas, rb);
   const uint32_t box = (uint32_t)(args.page < kTK ? args.page : kTK);
   if (!make_page_map(&sp.mk, k_pages, args.Dh, rows, box) || !make_page_map(&sp.mv, v_pages, args.Dh, rows, box))

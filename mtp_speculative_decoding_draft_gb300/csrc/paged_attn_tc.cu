@@ -17,7 +17,8 @@
 //
 // Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1, 128 each; P_g lies in the
 // first half of S_g.  Warps 0-3 and 4-7 are the groups' softmax, warp 8 brings
-// pages by TMA into a ring of K and V tiles, warp 9 issues the products.
+// pages by TMA into a ring of K and V tiles, warp 9 issues the products, warp 10
+// brings the next block's queries as soon as the last scores are done.
 #include "internal.h"
 #include "paged.cuh"
 #include "paged_tc.cuh"
@@ -29,7 +30,7 @@ namespace {
 
 constexpr int kTK = 128;          // keys per tile
 constexpr int kThreads = 384;   // three warpgroups: the registers move between whole ones
-constexpr int kProducer = 8, kIssuer = 9;
+constexpr int kProducer = 8, kIssuer = 9, kQuery = 10;
 constexpr unsigned kFull = 0xffffffffu;
 
 template <int DH>
@@ -227,24 +228,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       const int prow = min(p.page, kTK);             // rows of a piece: one page
       const int npc = (kTK / prow) * NB;             // pieces of a tile (at most 16)
       const int pc = lane / NB, hb = lane % NB;
-      int it = 0, seg = 0, zn = 0;
-      for (; w.valid() && ok; w.next(), ++seg) {
-        const int ng = w.t1() - w.t0 > tpg ? 2 : 1;
-        if (seg > 0) ok = mbar_wait(q_empty, (uint32_t)(seg - 1) & 1u, p.status);
-        ok = __all_sync(kFull, ok);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(q_full, (uint32_t)(ng * NB * rpg * 128));
-          for (int g = 0; g < ng; ++g)
-            for (int x = 0; x < NB; ++x)
-              tma_3d(qbuf + g * L::TILE + x * L::HALF, &sp.mq, 64 * x, w.h * p.G, w.s.row0 + w.t0 + g * tpg, q_full);
-        }
-        __syncwarp();
-        for (int i = w.i0; i < w.i1 && ok; ++i) {
-          const int t0 = w.r.tile(i) * kTK, k0 = t0 + pc * prow;
-          const bool need = lane < npc && w.r.any(k0, k0 + prow);
-          int y = 0;
-          if (need) y = (paged_page(p, w.b, k0) * p.Hkv + w.h) * p.page;
+      int it = 0, zn = 0;
+      for (; w.valid() && ok; w.next()) {
+        // the piece of this lane in tile i: whether a row sees it, and its row of the pool
+        auto locate = [&](int i, bool &need, int &y) {
+          const int k0 = w.r.tile(i) * kTK + pc * prow;
+          need = lane < npc && w.r.any(k0, k0 + prow);
+          y = need ? (paged_page(p, w.b, k0) * p.Hkv + w.h) * p.page : 0;
+        };
+        bool need, need_next = false;
+        int y, y_next = 0;
+        locate(w.i0, need, y);
+        for (int i = w.i0; i < w.i1 && ok; ++i, need = need_next, y = y_next) {
+          const int t0 = w.r.tile(i) * kTK;
+          if (i + 1 < w.i1) locate(i + 1, need_next, y_next);  // its table entry loads under this tile's waits
           const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, need)) * prow * 128);
           const bool whole = (t0 + kTK <= w.r.hi && t0 >= w.r.lo) || t0 + kTK <= w.r.sink_end;
           for (int isv = 0; isv < 2 && ok; ++isv, ++it) {
@@ -278,6 +275,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       if (!ok)  // let copies still in flight land before the CTA exits
         for (int i = max(0, it - ST); i < it; ++i)
           if (!mbar_wait(&full[i % ST], (uint32_t)(i / ST) & 1u, p.status)) break;
+    } else if (warp == kQuery) {
+      // ------------------------------------------------ the blocks' queries
+      if (lane == 0) {
+        for (int seg = 0; w.valid(); w.next(), ++seg) {
+          const int ng = w.t1() - w.t0 > tpg ? 2 : 1;
+          if (seg > 0 && !mbar_wait(q_empty, (uint32_t)(seg - 1) & 1u, p.status)) break;
+          mbar_arrive_expect_tx(q_full, (uint32_t)(ng * NB * rpg * 128));
+          for (int g = 0; g < ng; ++g)
+            for (int x = 0; x < NB; ++x)
+              tma_3d(qbuf + g * L::TILE + x * L::HALF, &sp.mq, 64 * x, w.h * p.G, w.s.row0 + w.t0 + g * tpg, q_full);
+        }
+      }
+      __syncwarp();
     } else if (warp == kIssuer) {
       // ------------------------------------------------ matrix products
       // The whole warp walks and waits, one elected lane issues.  Loop bounds,
@@ -342,14 +352,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
           }
           if (!ok) break;
           if (leader) {
+            if (i == nt - 1) mma_commit(q_empty);  // the block's last scores
             if (i < nt) mma_commit(&empty[ks]);
             if (i > 0) mma_commit(&empty[vs]);
           }
           __syncwarp();
         }
         it -= 2;  // the last round brought no K
-        if (ok && leader) mma_commit(q_empty);
-        __syncwarp();
       }
       if (leader) mma_commit(drain);  // nothing of this CTA is in flight when it frees its tensor memory
       __syncwarp();
