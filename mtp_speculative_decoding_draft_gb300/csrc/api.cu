@@ -948,6 +948,7 @@ int spec_adjust_logits(int B, int k, int V, const MtpLogitRules *rules, const fl
   for (const void *p : opt)
     if (p && !aligned16(p)) return MTP_ERR_INVALID_ARG;
   if (rules->history && (!rules->hist_len || rules->hist_cap < 1)) return MTP_ERR_INVALID_ARG;
+  if (rules->history && rules->hist_cap >= (1 << 28)) return MTP_ERR_UNSUPPORTED_SHAPE;  // counters of 29 bits
   if (rules->bias_tok && (!rules->bias_val || !rules->bias_len || rules->bias_cap < 1)) return MTP_ERR_INVALID_ARG;
   const bool penal = rules->rep || rules->freq || rules->pres;
   if (penal && k > 0 && !draft_tok) return MTP_ERR_INVALID_ARG;

@@ -7,16 +7,18 @@
 //   x = l(v);  seen: x = x > 0 ? x / rep : x * rep
 //   x -= freq * c;  c > 0: x -= pres;  x += bias(v);  v masked: x = -inf
 //
-// Bound by the logits' bytes.  A CTA owns one range of the vocabulary for all
-// k + 1 rows of a sequence: it scans the sequence's history once (4 bytes a
-// token, from L2 after the first CTA) into counters in shared memory, adds the
-// biases of its range, then streams its part of each row, adding draft j's
-// count between rows j and j + 1.  So the counters never go to memory, no
-// state is kept from step to step, and no global atomics are needed.  A bit a
-// token says which have a count or a bias, so that all others pay for the mask
-// alone.  In place, only what a rule changes is read and written.
-#include <stdlib.h>
-
+// Bound by the logits' bytes.  Few tokens have a count or a bias, so a CTA, which
+// owns one range of the vocabulary for all k + 1 rows of a sequence, scans the
+// sequence's history once (4 bytes a token, from L2 after the first CTA) into
+// counters in shared memory and keeps a list of the tokens it touched.  Each
+// row's part comes in and goes out by bulk copies through a ring in shared
+// memory, the first ones under the scan; there the masked logits are overwritten
+// and the listed ones recomputed.  The counters never go to memory, no state is
+// kept from step to step, and no global atomics are needed.  At 256 sequences of
+// 6 rows of 151936: looking every token up in the counters while streaming
+// through registers took 515 us (38 instructions a logit), rewriting the listed
+// tokens in global memory behind the stream 450 us.  In place, only what a rule
+// changes is read and written.
 #include "common.cuh"
 #include "internal.h"
 #include "logits.cuh"
@@ -25,191 +27,316 @@ namespace mtp {
 
 namespace {
 
-constexpr uint32_t kPrompt = 0x80000000u;  // the token occurs in the prompt; the low bits count
+// a counter's word: occurrences in the low bits, and why else the token is listed
+constexpr uint32_t kPrompt = 1u << 31, kBias = 1u << 30, kDraft = 1u << 29, kCount = kDraft - 1u;
 constexpr unsigned kFull = 0xffffffffu;
+
+// Six CTAs an SM: ranges of 4096 (three CTAs) and rings of four rows measured
+// slower at 256 sequences of 6 rows of 151936 (446 and 444 us against 344),
+// ranges of 1024 scan the history too often (494 us).
+constexpr int NT = 256;           // threads
+constexpr int VPT = 2;            // vectors of four logits a thread looks at per row
+constexpr int CH = VPT * 4 * NT;  // tokens of a range
+constexpr int kRing = 2;          // rows in shared memory at a time
 
 }  // namespace
 
-// VPT: vectors of four logits a thread holds per row; the range is VPT * 4 * NT tokens.
-template <int NT, int VPT, bool IN_PLACE>
+namespace {
+
+// One range of one sequence: counters, the list of touched tokens, biases.
+struct Range {
+  uint32_t *cnt;    // [CH]
+  uint16_t *list;   // [CH] offsets of the touched tokens
+  float *bias;      // [CH] (only with biases)
+  int *drafts;      // [8]
+  int *listed;
+  int b, c0, c1;
+  float rep, freq, pres;
+
+  // Executed by all NT threads; ends with a barrier.
+  __device__ __forceinline__ void build(const LogitArgs &p) {
+    const int tid = threadIdx.x;
+    for (int i = tid; i < CH / 4; i += NT) {
+      reinterpret_cast<uint4 *>(cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.bias_tok) reinterpret_cast<float4 *>(bias)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (tid == 0) *listed = 0;
+    rep = p.rep ? __ldcg(&p.rep[b]) : 1.f;
+    freq = p.freq ? __ldcg(&p.freq[b]) : 0.f;
+    pres = p.pres ? __ldcg(&p.pres[b]) : 0.f;
+    __syncthreads();
+    // the first to touch a counter puts the token on the list
+    auto touched = [&](uint32_t old, int o) {
+      if (old == 0u) list[atomicAdd(listed, 1)] = (uint16_t)o;
+    };
+    if (p.history) {
+      const int n = min(max(__ldcg(&p.hist_len[b]), 0), p.hist_cap);
+      const int np = p.prompt_len ? min(max(__ldcg(&p.prompt_len[b]), 0), n) : 0;
+      const int *h = p.history + (size_t)b * p.hist_cap;
+      auto occurs = [&](int i, int t) {
+        if (t >= c0 && t < c1) {
+          uint32_t *c = &cnt[t - c0];
+          touched(i < np ? atomicOr(c, kPrompt) : atomicAdd(c, 1u), t - c0);
+        }
+      };
+      const int n4 = p.hist_cap % 4 == 0 ? n / 4 : 0;  // rows that start on 16 bytes are read in vectors
+      for (int i0 = tid; i0 < n4; i0 += 4 * NT) {
+        int4 t[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          t[u] = i0 + u * NT < n4 ? __ldcg(reinterpret_cast<const int4 *>(h) + i0 + u * NT) : make_int4(-1, -1, -1, -1);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = 4 * (i0 + u * NT);
+          occurs(i, t[u].x);
+          occurs(i + 1, t[u].y);
+          occurs(i + 2, t[u].z);
+          occurs(i + 3, t[u].w);
+        }
+      }
+      for (int i = 4 * n4 + tid; i < n; i += NT) occurs(i, __ldcg(&h[i]));
+    }
+    if (tid < p.k && p.draft_tok) {
+      const int t = __ldcg(&p.draft_tok[b * p.k + tid]);
+      drafts[tid] = t;
+      if (t >= c0 && t < c1) touched(atomicOr(&cnt[t - c0], kDraft), t - c0);
+    }
+    if (p.bias_tok && tid >= NT - 32) {
+      // one warp, in list order: a token that is listed twice gets the sum, always alike
+      const int lane = tid & 31, n = min(max(__ldcg(&p.bias_len[b]), 0), p.bias_cap);
+      const int *tk = p.bias_tok + (size_t)b * p.bias_cap;
+      const float *tv = p.bias_val + (size_t)b * p.bias_cap;
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        const int t = i < n ? __ldcg(&tk[i]) : -1;
+        const float v = i < n ? __ldcg(&tv[i]) : 0.f;
+        const bool mine = t >= c0 && t < c1;
+        const unsigned peers = __match_any_sync(kFull, mine ? t : -1 - lane);
+        const int lead = __ffs(peers) - 1;
+        float sum = mine && lane == lead ? bias[t - c0] + v : 0.f;
+        if (__any_sync(kFull, lane != lead)) {
+#pragma unroll 1
+          for (int l = 1; l < 32; ++l) {
+            const float x = __shfl_sync(kFull, v, l);
+            if (lane == lead && l != lead && (peers >> l & 1u)) sum += x;
+          }
+        }
+        if (mine && lane == lead) {
+          bias[t - c0] = sum;
+          touched(atomicOr(&cnt[t - c0], kBias), t - c0);
+        }
+        __syncwarp();
+      }
+    }
+    __syncthreads();
+  }
+
+  // Penalties and bias of the touched token at offset o, at position j.
+  __device__ __forceinline__ float rule(float x, int o, int j) const {
+    const uint32_t c = cnt[o];
+    uint32_t n = c & kCount;
+    if (c & kDraft)
+      for (int d = 0; d < j; ++d) n += drafts[d] == c0 + o;
+    if (n || (c & kPrompt)) x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
+    if (n) x = x - freq * (float)n - pres;
+    if (c & kBias) x += bias[o];
+    return x;
+  }
+};
+
+// The mask's bits of tokens t .. t + 3 (bits 0 .. 3).
+__device__ __forceinline__ uint32_t mask4(const uint32_t *mask, int t) {
+  uint32_t m = __ldg(&mask[t >> 5]) >> (t & 31);
+  if ((t & 31) > 28) m |= __ldg(&mask[(t >> 5) + 1]) << (32 - (t & 31));
+  return m & 0xfu;
+}
+
+__device__ __forceinline__ bool mask1(const uint32_t *mask, int t) { return __ldg(&mask[t >> 5]) >> (t & 31) & 1u; }
+
+// -inf into the masked ones of four logits.
+__device__ __forceinline__ void cover(float *x, uint32_t m) {
+  if (m == 0xfu) return;
+  if (m == 0u) {
+    *reinterpret_cast<float4 *>(x) = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (!(m >> e & 1u)) x[e] = -INFINITY;
+}
+
+
+// Bulk copy shared memory -> global; 16-byte aligned, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+constexpr int range_bytes(bool bias) { return CH * (bias ? 10 : 6); }
+
+}  // namespace
+
 __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant__ LogitArgs p) {
   trace_start(kTkLogits);
-  constexpr int CH = VPT * 4 * NT;
-  extern __shared__ __align__(16) unsigned char smem[];
-  uint32_t *dirty = reinterpret_cast<uint32_t *>(smem);       // [CH / 32 + 1] tokens with a count or a bias
-  uint32_t *cnt = dirty + CH / 32 + 4;                        // [CH]
-  float *bias = reinterpret_cast<float *>(cnt + CH);          // [CH]
-  const int tid = threadIdx.x, ranges = (p.V + CH - 1) / CH, b = blockIdx.x / ranges;
-  const int c0 = (blockIdx.x % ranges) * CH, c1 = min(p.V, c0 + CH);
+  extern __shared__ __align__(128) unsigned char smem[];
+  float *ring = reinterpret_cast<float *>(smem);  // [kRing][CH]
+  __shared__ int listed, drafts[8];
+  __shared__ __align__(8) uint64_t full[kRing];
+  const int tid = threadIdx.x, ranges = (p.V + CH - 1) / CH, words = (p.V + 31) / 32;
+  Range r;
+  r.cnt = reinterpret_cast<uint32_t *>(ring + kRing * CH);
+  r.bias = reinterpret_cast<float *>(r.cnt + CH);
+  r.list = reinterpret_cast<uint16_t *>(r.cnt + CH + (p.bias_tok ? CH : 0));
+  r.drafts = drafts;
+  r.listed = &listed;
+  r.b = blockIdx.x / ranges;
+  r.c0 = (blockIdx.x % ranges) * CH;
+  r.c1 = min(p.V, r.c0 + CH);
+  const int n = r.c1 - r.c0;
+  // rows of V % 4 != 0 start off a 16-byte boundary: the copies start at the first
+  // aligned token and take whole vectors, the few tokens beside them go one by one
+  auto row_base = [&](int j) { return ((size_t)r.b * (p.k + 1) + j) * p.V + r.c0; };
+  auto row_lead = [&](int j) { return min(n, (int)((4 - (row_base(j) & 3)) & 3)); };
+  if (tid == 0) {
+    for (int s = 0; s < kRing; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+  }
   grid_dep_wait();
   trace_dep(kTkLogits);
   grid_dep_launch();
-
-  // rows of V % 4 != 0 start off a 16-byte boundary: the vectors start at the
-  // first aligned token, the few tokens beside them go one by one
-  const int words = (p.V + 31) / 32;
-  auto row_base = [&](int j) { return ((size_t)b * (p.k + 1) + j) * p.V; };
-  auto row_lead = [&](size_t base) { return min(c1 - c0, (int)((4 - ((base + c0) & 3)) & 3)); };
-  auto row_mask = [&](int j) { return p.mask + ((size_t)b * (p.k + 1) + j) * words; };
-  auto allowed4 = [&](const uint32_t *mask, int t) {  // the bits of tokens t .. t + 3
-    uint32_t m = __ldg(&mask[t >> 5]) >> (t & 31);
-    if ((t & 31) > 28) m |= __ldg(&mask[(t >> 5) + 1]) << (32 - (t & 31));
-    return m & 0xfu;
+  const int j0 = blockIdx.y * p.rows, j1 = min(p.k + 1, j0 + p.rows);  // the CTA's rows
+  auto bring = [&](int j) {  // thread 0
+    const int lead = row_lead(j), nv = (n - lead) / 4;
+    const int s = (j - j0) % kRing;
+    mbar_arrive_expect_tx(&full[s], (uint32_t)nv * 16u);
+    if (nv) bulk_g2s(ring + s * CH, p.logits + row_base(j) + lead, (uint32_t)nv * 16u, &full[s]);
   };
-  float4 nx[VPT];
-  uint32_t nm[VPT];
-  auto fetch = [&](int j) {
-    const size_t base = row_base(j);
-    const int lead = row_lead(base), nv = (c1 - c0 - lead) / 4;
-    const float4 *s4 = reinterpret_cast<const float4 *>(p.logits + base + c0 + lead);
+  if (tid == 0)
+    for (int j = j0; j < j1 && j < j0 + kRing; ++j) bring(j);
+  uint32_t next_mask[VPT];
+  auto fetch_mask = [&](int j) {
+    const int lead = row_lead(j), nv = (n - lead) / 4;
+    const uint32_t *mask = p.mask + ((size_t)r.b * (p.k + 1) + j) * words;
 #pragma unroll
-    for (int u = 0; u < VPT; ++u) {
-      const int i = tid + u * NT;
-      nm[u] = 0xfu;
-      if (i < nv) {
-        if (!IN_PLACE) nx[u] = __ldcs(s4 + i);
-        if (p.mask) nm[u] = allowed4(row_mask(j), c0 + lead + 4 * i);
-      }
-    }
+    for (int u = 0; u < VPT; ++u) next_mask[u] = tid + u * NT < nv ? mask4(mask, r.c0 + lead + 4 * (tid + u * NT)) : 0xfu;
   };
-  fetch(0);  // under the history's scan
+  if (p.mask) fetch_mask(j0);
+  r.build(p);
 
-  // ---- counters and biases of the range
-  for (int i = tid; i < CH / 4; i += NT) {
-    reinterpret_cast<uint4 *>(cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (p.bias_tok) reinterpret_cast<float4 *>(bias)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  for (int i = tid; i < CH / 32 + 4; i += NT) dirty[i] = 0u;
-  __syncthreads();
-  auto mark = [&](int o) { atomicOr(&dirty[o >> 5], 1u << (o & 31)); };
-  if (p.history) {
-    const int n = min(max(__ldcg(&p.hist_len[b]), 0), p.hist_cap);
-    const int np = p.prompt_len ? min(max(__ldcg(&p.prompt_len[b]), 0), n) : 0;
-    const int *h = p.history + (size_t)b * p.hist_cap;
-    for (int i0 = tid; i0 < n; i0 += 8 * NT) {
-      int t[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) t[u] = i0 + u * NT < n ? __ldcg(&h[i0 + u * NT]) : -1;
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (t[u] >= c0 && t[u] < c1) {
-          if (i0 + u * NT < np) atomicOr(&cnt[t[u] - c0], kPrompt);
-          else atomicAdd(&cnt[t[u] - c0], 1u);
-          mark(t[u] - c0);
-        }
-    }
-  }
-  if (p.bias_tok && tid < 32) {
-    // one warp, in list order: a token that is listed twice gets the sum, always alike
-    const int n = min(max(__ldcg(&p.bias_len[b]), 0), p.bias_cap);
-    const int *tk = p.bias_tok + (size_t)b * p.bias_cap;
-    const float *tv = p.bias_val + (size_t)b * p.bias_cap;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + tid;
-      const int t = i < n ? __ldcg(&tk[i]) : -1;
-      const float v = i < n ? __ldcg(&tv[i]) : 0.f;
-      const bool mine = t >= c0 && t < c1;
-      const unsigned peers = __match_any_sync(kFull, mine ? t : -1 - tid);
-      const int lead = __ffs(peers) - 1;
-      float sum = mine && tid == lead ? bias[t - c0] + v : 0.f;
-      if (__any_sync(kFull, tid != lead)) {
-#pragma unroll 1
-        for (int l = 1; l < 32; ++l) {
-          const float x = __shfl_sync(kFull, v, l);
-          if (tid == lead && l != lead && (peers >> l & 1u)) sum += x;
-        }
-      }
-      if (mine && tid == lead) {
-        bias[t - c0] = sum;
-        mark(t - c0);
-      }
-      __syncwarp();
-    }
-  }
-  const float rep = p.rep ? __ldcg(&p.rep[b]) : 1.f, freq = p.freq ? __ldcg(&p.freq[b]) : 0.f,
-              pres = p.pres ? __ldcg(&p.pres[b]) : 0.f;
-  __syncthreads();
-
-  // penalties and bias of the token at offset o of the range
-  auto rule = [&](float x, int o) {
-    const uint32_t c = cnt[o];
-    if (c) {
-      x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
-      const uint32_t n = c & ~kPrompt;
-      if (n) x = x - freq * (float)n - pres;
-    }
-    if (p.bias_tok) x += bias[o];
-    return x;
-  };
-
-  for (int j = 0; j <= p.k; ++j) {
-    const size_t base = row_base(j);
-    const float *src = p.logits + base;
-    float *dst = p.out + base;
-    const int lead = row_lead(base), nv = (c1 - c0 - lead) / 4;
-    float4 x[VPT];
+  const int n_list = listed;
+  bool ok = true;
+  for (int j = j0; j < j1; ++j) {
+    const int lead = row_lead(j), nv = (n - lead) / 4, s = (j - j0) % kRing;
+    float *row = ring + s * CH;
+    const uint32_t *mask = p.mask ? p.mask + ((size_t)r.b * (p.k + 1) + j) * words : nullptr;
     uint32_t m[VPT];
 #pragma unroll
-    for (int u = 0; u < VPT; ++u) {
-      x[u] = nx[u];
-      m[u] = nm[u];
+    for (int u = 0; u < VPT; ++u) m[u] = next_mask[u];
+    if (p.mask && j + 1 < j1) fetch_mask(j + 1);
+    if (ok) ok = mbar_wait(&full[s], (uint32_t)((j - j0) / kRing) & 1u, nullptr);
+    for (int i = tid; i < n_list; i += NT) {
+      const int o = r.list[i], at = o - lead;
+      if (at >= 0 && at < 4 * nv) row[at] = r.rule(row[at], o, j);
     }
-    if (j < p.k) fetch(j + 1);  // the next row's loads run under this row's rules and stores
+    if (p.mask) {  // the mask last: it wins over every other rule
+      if (n_list) __syncthreads();
 #pragma unroll
-    for (int u = 0; u < VPT; ++u) {
-      const int i = tid + u * NT;
-      if (i >= nv) continue;
-      const int o = lead + 4 * i;
-      uint32_t d = dirty[o >> 5] >> (o & 31);  // most tokens have no rule but the mask
-      if (lead && (o & 31) > 28) d |= dirty[(o >> 5) + 1] << (32 - (o & 31));
-      d &= 0xfu;
-      float4 *at = reinterpret_cast<float4 *>(dst + c0 + o);
-      if (IN_PLACE) {
-        if (m[u] == 0xfu && !d) continue;
-        x[u] = m[u] ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      if (d) {
-        if (d & 1u) x[u].x = rule(x[u].x, o);
-        if (d & 2u) x[u].y = rule(x[u].y, o + 1);
-        if (d & 4u) x[u].z = rule(x[u].z, o + 2);
-        if (d & 8u) x[u].w = rule(x[u].w, o + 3);
-      }
-      if (!(m[u] & 1u)) x[u].x = -INFINITY;
-      if (!(m[u] & 2u)) x[u].y = -INFINITY;
-      if (!(m[u] & 4u)) x[u].z = -INFINITY;
-      if (!(m[u] & 8u)) x[u].w = -INFINITY;
-      __stcs(at, x[u]);
+      for (int u = 0; u < VPT; ++u)
+        if (tid + u * NT < nv) cover(row + 4 * (tid + u * NT), m[u]);
     }
     // the tokens before the first vector and behind the last
-    const int tail = lead + 4 * nv, singles = lead + (c1 - c0 - tail);
+    const int tail = lead + 4 * nv, singles = lead + (n - tail);
     if (tid < singles) {
-      const int o = tid < lead ? tid : tail + tid - lead, t = c0 + o;
-      const bool allowed = !p.mask || (__ldg(&row_mask(j)[t >> 5]) >> (t & 31) & 1u);
-      const float y = rule(src[t], o);
-      dst[t] = allowed ? y : -INFINITY;
+      const int o = tid < lead ? tid : tail + tid - lead;
+      p.out[row_base(j) + o] =
+          !mask || mask1(mask, r.c0 + o) ? r.rule(__ldcg(p.logits + row_base(j) + o), o, j) : -INFINITY;
     }
-    if (j < p.k && p.draft_tok) {
-      const int t = __ldcg(&p.draft_tok[b * p.k + j]);
-      __syncthreads();  // every thread has read the counters of row j
-      if (tid == 0 && t >= c0 && t < c1) {
-        cnt[t - c0] += 1u;
-        mark(t - c0);
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      if (nv) bulk_s2g(p.out + row_base(j) + lead, row, (uint32_t)nv * 16u);
+      bulk_commit();
+      // the row kRing ahead takes this row's place once the copy out has read it
+      if (j + kRing < j1) {
+        bulk_wait_read();
+        bring(j + kRing);
       }
-      __syncthreads();
+    }
+  }
+  if (tid == 0) bulk_wait_all();
+  trace_end(kTkLogits);
+}
+
+// In place: the masked logits are overwritten, then the touched ones recomputed.
+__global__ void __launch_bounds__(NT) adjust_logits_in_place_kernel(const __grid_constant__ LogitArgs p) {
+  trace_start(kTkLogits);
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int listed, drafts[8];
+  const int tid = threadIdx.x, ranges = (p.V + CH - 1) / CH, words = (p.V + 31) / 32;
+  Range r;
+  r.cnt = reinterpret_cast<uint32_t *>(smem);
+  r.bias = reinterpret_cast<float *>(r.cnt + CH);
+  r.list = reinterpret_cast<uint16_t *>(r.cnt + CH + (p.bias_tok ? CH : 0));
+  r.drafts = drafts;
+  r.listed = &listed;
+  r.b = blockIdx.x / ranges;
+  r.c0 = (blockIdx.x % ranges) * CH;
+  r.c1 = min(p.V, r.c0 + CH);
+  const int n = r.c1 - r.c0;
+  grid_dep_wait();
+  trace_dep(kTkLogits);
+  grid_dep_launch();
+  r.build(p);
+  const int j0 = blockIdx.y * p.rows, j1 = min(p.k + 1, j0 + p.rows);
+  for (int j = j0; j < j1; ++j) {
+    const size_t base = ((size_t)r.b * (p.k + 1) + j) * p.V + r.c0;
+    const uint32_t *mask = p.mask ? p.mask + ((size_t)r.b * (p.k + 1) + j) * words : nullptr;
+    float *row = p.out + base;
+    if (mask) {
+      const int lead = min(n, (int)((4 - (base & 3)) & 3)), nv = (n - lead) / 4, tail = lead + 4 * nv;
+      uint32_t m[VPT];
+#pragma unroll
+      for (int u = 0; u < VPT; ++u) m[u] = tid + u * NT < nv ? mask4(mask, r.c0 + lead + 4 * (tid + u * NT)) : 0xfu;
+#pragma unroll
+      for (int u = 0; u < VPT; ++u)
+        if (tid + u * NT < nv) cover(row + lead + 4 * (tid + u * NT), m[u]);
+      if (tid < lead + (n - tail)) {
+        const int o = tid < lead ? tid : tail + tid - lead;
+        if (!mask1(mask, r.c0 + o)) row[o] = -INFINITY;
+      }
+    }
+    for (int i = tid; i < listed; i += NT) {
+      const int o = r.list[i];
+      if (mask && !mask1(mask, r.c0 + o)) continue;
+      row[o] = r.rule(row[o], o, j);
     }
   }
   trace_end(kTkLogits);
 }
 
-namespace {
+cudaError_t logits_set_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(adjust_logits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       range_bytes(true) + kRing * CH * 4);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(adjust_logits_in_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             range_bytes(true));
+  return e;
+}
 
-template <int NT, int VPT, bool IN_PLACE>
-cudaError_t launch_one(const LogitArgs &a, cudaStream_t s, bool pdl) {
-  constexpr int CH = VPT * 4 * NT;
+cudaError_t launch_adjust_logits(const LogitArgs &args, int sms, cudaStream_t s, bool pdl) {
+  LogitArgs a = args;
+  const bool in_place = a.logits == a.out;
+  const long long ranges = (long long)a.B * ((a.V + CH - 1) / CH);
+  // One scan of the history serves all rows of a range; with few ranges the rows
+  // go to CTAs of their own instead, each with its scan.
+  a.rows = ranges >= 2 * sms ? a.k + 1 : 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.V + CH - 1) / CH * (unsigned)a.B);
+  cfg.gridDim = dim3((unsigned)ranges, (unsigned)((a.k + a.rows) / a.rows));
   cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = (CH / 32 + 4 + CH * (a.bias_tok ? 2 : 1)) * 4;
+  cfg.dynamicSmemBytes = range_bytes(a.bias_tok != nullptr) + (in_place ? 0 : kRing * CH * 4);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -217,43 +344,8 @@ cudaError_t launch_one(const LogitArgs &a, cudaStream_t s, bool pdl) {
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   note_launch();
-  return cudaLaunchKernelEx(&cfg, adjust_logits_kernel<NT, VPT, IN_PLACE>, a);
-}
-
-template <int NT, int VPT>
-cudaError_t launch_width(const LogitArgs &a, cudaStream_t s, bool pdl) {
-  return a.logits == a.out ? launch_one<NT, VPT, true>(a, s, pdl) : launch_one<NT, VPT, false>(a, s, pdl);
-}
-
-template <int NT, int VPT>
-cudaError_t set_smem() {
-  constexpr int CH = VPT * 4 * NT, bytes = (CH / 32 + 4 + 2 * CH) * 4;
-  cudaError_t e = cudaFuncSetAttribute(adjust_logits_kernel<NT, VPT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(adjust_logits_kernel<NT, VPT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  return e;
-}
-
-}  // namespace
-
-cudaError_t logits_set_attributes() {
-  cudaError_t e = set_smem<256, 1>();
-  if (e == cudaSuccess) e = set_smem<512, 1>();
-  if (e == cudaSuccess) e = set_smem<512, 2>();
-  if (e == cudaSuccess) e = set_smem<512, 4>();
-  return e;
-}
-
-cudaError_t launch_adjust_logits(const LogitArgs &a, int sms, cudaStream_t s, bool pdl) {
-  // the widest range (fewest scans of the history) that still fills the GPU
-  // several times over; a single sequence takes the narrowest
-  auto ctas = [&](int ch) { return (long long)a.B * ((a.V + ch - 1) / ch); };
-  int width = 0;
-  if (const char *v = getenv("MTP_LG")) width = atoi(v);
-  if (width == 8192 || (!width && ctas(8192) >= 4 * sms)) return launch_width<512, 4>(a, s, pdl);
-  if (width == 4096 || (!width && ctas(4096) >= 4 * sms)) return launch_width<512, 2>(a, s, pdl);
-  if (width == 2048 || (!width && ctas(2048) >= 2 * sms)) return launch_width<512, 1>(a, s, pdl);
-  return launch_width<256, 1>(a, s, pdl);
+  return in_place ? cudaLaunchKernelEx(&cfg, adjust_logits_in_place_kernel, a)
+                  : cudaLaunchKernelEx(&cfg, adjust_logits_kernel, a);
 }
 
 MTP_TRACE_COLLECTOR(logits)

@@ -23,6 +23,7 @@ struct LogitArgs {
   const float *logits;    // [B, k + 1, V]
   float *out;             // the same, or logits itself
   const int *draft_tok;   // [B, k] or null
+  int rows;               // rows of a CTA (set by the launch)
 };
 cudaError_t logits_set_attributes();
 cudaError_t launch_adjust_logits(const LogitArgs &a, int sms, cudaStream_t s, bool pdl);
