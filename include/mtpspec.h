@@ -610,7 +610,8 @@ enum {
     MTP_TK_PAGED_ATTN_TC = 61, /* paged attention: tensor-core kernel */
     MTP_TK_PAGED_COMBINE = 62, /* paged attention: joins partial items */
     MTP_TK_CACHE_APPEND = 63,  /* mtp_cache_append */
-    MTP_TK_LOGITS = 64         /* spec_adjust_logits */
+    MTP_TK_LOGITS = 64,        /* spec_adjust_logits */
+    MTP_TK_PAGED_PLAN = 65     /* paged attention: the tensor-core kernel's plan */
 };
 typedef struct MtpTraceEntry {
     uint64_t launch;      /* the launch's grid id */

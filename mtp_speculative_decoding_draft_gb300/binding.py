@@ -639,7 +639,7 @@ TRACE_KIND_NAMES = {0: "gemv input projection", 1: "gemv QKV", 2: "gemv output p
                     4: "gemv down", 5: "gemv LM head", 10: "attention", 11: "attention (tensor cores)",
                     20: "verify (cluster)", 21: "verify (ticketed)", 30: "tc GEMM", 31: "tc prologue/select",
                     40: "fused verify GEMM", 41: "fused verify aux (stats, decisions, draws)", 50: "chain", 60: "paged attention (streaming)", 61: "paged attention (tensor cores)",
-                    62: "paged attention combine", 63: "cache append", 64: "logit rules"}
+                    62: "paged attention combine", 63: "cache append", 64: "logit rules", 65: "paged attention plan"}
 
 
 def trace_read(max_entries=16384):

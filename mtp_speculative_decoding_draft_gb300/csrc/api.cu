@@ -514,7 +514,7 @@ static_assert(kTkGemv == MTP_TK_GEMV && kTkAttn == MTP_TK_ATTN && kTkAttnTc == M
                   kTkTcAux == MTP_TK_TC_AUX && kTkFusedGemm == MTP_TK_FUSED_GEMM &&
                   kTkFusedAux == MTP_TK_FUSED_AUX && kTkChain == MTP_TK_CHAIN && kTkPagedAttn == MTP_TK_PAGED_ATTN &&
                   kTkPagedAttnTc == MTP_TK_PAGED_ATTN_TC && kTkPagedCombine == MTP_TK_PAGED_COMBINE &&
-                  kTkAppend == MTP_TK_CACHE_APPEND && kTkLogits == MTP_TK_LOGITS,
+                  kTkAppend == MTP_TK_CACHE_APPEND && kTkPagedPlan == MTP_TK_PAGED_PLAN && kTkLogits == MTP_TK_LOGITS,
               "trace kinds match the header");
 
 // the launch-trace collectors of the kernel files (MTP_TRACE_COLLECTOR)
@@ -899,7 +899,7 @@ int mtp_cache_append(const MtpPagedCache *cache, const MtpRope *rope, int B, int
 size_t mtp_paged_attn_workspace_size(int B, int n_rows, int max_rows, int Hq, int Hkv, int Dh) {
   if (B < 1 || n_rows < 1 || max_rows < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv || Hq / Hkv > kMaxGroup) return 0;
   if (Dh != 32 && Dh != 64 && Dh != 128) return 0;
-  return kAlign + paged_attn_scratch_bytes(n_rows, max_rows, Hq / Hkv, Dh);
+  return kAlign + paged_attn_scratch_bytes(B, Hkv, n_rows, max_rows, Hq / Hkv, Dh);
 }
 
 int mtp_paged_attn(const MtpPagedCache *cache, int B, int Hq, int n_rows, int max_rows, const int32_t *row_start,

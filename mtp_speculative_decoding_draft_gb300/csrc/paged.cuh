@@ -19,7 +19,7 @@
 namespace mtp {
 
 // trace kinds: the MTP_TK_* values of the public header
-constexpr int kTkPagedAttn = 60, kTkPagedAttnTc = 61, kTkPagedCombine = 62, kTkAppend = 63;
+constexpr int kTkPagedAttn = 60, kTkPagedAttnTc = 61, kTkPagedCombine = 62, kTkAppend = 63, kTkPagedPlan = 65;
 // status bits (mirror MTP_STATUS_*)
 constexpr int kStatusBadRows = 32;
 constexpr int kStatusBadPage = 64;
@@ -261,7 +261,7 @@ __device__ __forceinline__ int paged_page(const PagedArgs &p, int b, int j) {
 // A 2-D map over a pool of K or V pages as [rows, Dh] bf16, boxes of box_rows
 // rows by at most 64 elements (tc.cu); false if the driver cannot encode it.
 bool make_page_map(CUtensorMap *m, const void *base, int Dh, uint64_t rows, uint32_t box_rows);
-size_t paged_attn_scratch_bytes(int n_rows, int max_rows, int G, int Dh);
+size_t paged_attn_scratch_bytes(int B, int Hkv, int n_rows, int max_rows, int G, int Dh);
 cudaError_t paged_set_attributes();
 cudaError_t launch_paged_attn(const PagedArgs &a, const void *k_pages, const void *v_pages, int max_rows, void *scratch,
                               int sms, cudaStream_t s, bool pdl);

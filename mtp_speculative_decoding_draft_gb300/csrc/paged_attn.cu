@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
 
 namespace {
 
-constexpr int kMaxSms = 160;         // the workspace's CTA slots cover this many SMs
+constexpr int kMaxSms = kPagedMaxCtas;
 constexpr int kStreamRows = 64;      // block rows of the widest streaming variant
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -562,9 +562,10 @@ static long long packed_rows(int n_rows, int max_rows, int G) {
 // cores (heads of 32 stay: their products are too thin for it).
 static bool wants_tc(long long packed, int Dh) { return packed > kStreamRows && Dh != 32; }
 
-size_t paged_attn_scratch_bytes(int n_rows, int max_rows, int G, int Dh) {
-  return region_bytes(2 * kMaxSms, kStreamRows, Dh) +
-         (wants_tc(packed_rows(n_rows, max_rows, G), Dh) ? region_bytes(kMaxSms, kPagedTcRows, Dh) : 0);
+size_t paged_attn_scratch_bytes(int B, int Hkv, int n_rows, int max_rows, int G, int Dh) {
+  const size_t stream = region_bytes(2 * kMaxSms, kStreamRows, Dh);
+  if (!wants_tc(packed_rows(n_rows, max_rows, G), Dh)) return stream;
+  return stream + region_bytes(kMaxSms, kPagedTcRows, Dh) + paged_tc_plan_bytes(B, n_rows, G, Hkv);
 }
 
 cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const void *v_pages, int max_rows, void *scratch,
@@ -586,7 +587,9 @@ cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const 
     tp.a.tpb = 2 * (128 / args.G);
     tp.a.min_tiles = 2;
     tp.a.late_wait = 0;
-    bind_region(tp.a, base + region_bytes(2 * kMaxSms, kStreamRows, args.Dh), n, kPagedTcRows);
+    char *at = base + region_bytes(2 * kMaxSms, kStreamRows, args.Dh);
+    bind_region(tp.a, at, n, kPagedTcRows);
+    paged_tc_bind_plan(tp, at + region_bytes(kMaxSms, kPagedTcRows, args.Dh));
     if (!make_page_map(&tp.mk, k_pages, args.Dh, rows, args.page) ||
         !make_page_map(&tp.mv, v_pages, args.Dh, rows, args.page) ||
         !make_query_map(&tp.mq, args.q, args.Dh, args.Hq, args.n_rows, args.ldq, args.G, 128 / args.G))

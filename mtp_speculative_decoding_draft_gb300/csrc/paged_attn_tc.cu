@@ -24,6 +24,13 @@
 #include "paged_tc.cuh"
 #include "tcgen05.cuh"
 
+//
+// The order of the line (paged.cuh): with equal contiguous shares each CTA walks
+// the blocks of a few K/V heads one after another, and all heads of the batch are
+// read at the same time; past L2's size every block reads its keys from DRAM
+// again (24 ragged sequences of 315 MB of keys: 455 us).  The plan deals the items
+// out like cards instead, item t * CTAs + c to CTA c's t-th place, so that the
+// blocks of one K/V head run side by side.
 namespace mtp {
 
 namespace {
@@ -161,7 +168,149 @@ __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *m, int x, i
       : "memory");
 }
 
+constexpr int kPlanThreads = 1024;
+
+// Inclusive scan over the block's threads; returns the block's sum too.
+__device__ long long block_scan(long long v, long long *incl, long long *scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();  // scratch is free again
+  if (lane == 31) scratch[warp] = v;
+  __syncthreads();
+  long long before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    const long long u = scratch[w];
+    before += w < warp ? u : 0;
+    sum += u;
+  }
+  *incl = before + v;
+  return sum;
+}
+
+// Walks a share's items in the plan's order, one segment at a time; the interface
+// of PagedWalk.
+template <int TK>
+struct PlanWalk {
+  const PagedTcParams &sp;
+  const PagedArgs &p;
+  long long pos, end, per;
+  int i, b, h, t0;
+  PagedSeq s;
+  PagedRange r;
+  int i0, i1;
+
+  __device__ __forceinline__ explicit PlanWalk(const PagedTcParams &x) : sp(x), p(x.a), i0(0), i1(0) {
+    const long long total = __ldcg(&sp.plan->total);
+    per = __ldcg(&sp.plan->per);
+    pos = min(total, per * (long long)blockIdx.x);
+    end = min(total, pos + per);
+    if (pos >= end) return;
+    i = __ldcg(&sp.start[blockIdx.x]);
+    i0 = (int)(pos - load());
+    cut();
+  }
+  __device__ __forceinline__ long long load() {
+    const int4 x = __ldcg(reinterpret_cast<const int4 *>(&sp.items[i]));
+    b = x.x;
+    h = x.y;
+    t0 = x.z;
+    s = paged_seq(p, b, false);
+    r = paged_range<TK>(p, s, t0, t1());
+    return __ldcg(&sp.items[i].first);
+  }
+  __device__ __forceinline__ int t1() const { return min(s.n, t0 + p.tpb); }
+  __device__ __forceinline__ bool valid() const { return pos < end; }
+  __device__ __forceinline__ bool starts() const { return i0 == 0; }
+  __device__ __forceinline__ bool ends() const { return i1 == r.count; }
+  __device__ __forceinline__ void cut() {
+    const long long left = end - pos;
+    i1 = (long long)(r.count - i0) <= left ? r.count : i0 + (int)left;
+  }
+  __device__ __forceinline__ void next() {
+    pos += i1 - i0;
+    if (pos >= end) return;
+    do ++i;
+    while (__ldcg(&sp.items[i].count) == 0);  // pos < end: an item follows
+    load();
+    i0 = 0;
+    cut();
+  }
+};
+
 }  // namespace
+
+// One CTA: the items of the batch, their order, and where each share starts.
+__global__ void __launch_bounds__(kPlanThreads) paged_tc_plan_kernel(const __grid_constant__ PagedTcParams sp, int ctas) {
+  trace_start(kTkPagedPlan);
+  __shared__ long long scratch[kPlanThreads / 32];
+  const PagedArgs &p = sp.a;
+  const int tid = threadIdx.x;
+  grid_dep_wait();
+  trace_dep(kTkPagedPlan);
+  grid_dep_launch();
+  // ---- blocks of each sequence, and all tiles
+  long long nblk = 0, total = 0, incl;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    long long c = 0;
+    int nb = 0;
+    if (b < p.B) {
+      const PagedSeq s = paged_seq(p, b, true);
+      c = paged_cost<kTK>(p, s);
+      nb = c > 0 ? paged_blocks(p, s.n) : 0;
+    }
+    const long long sum = block_scan(nb, &incl, scratch);
+    if (b < p.B) sp.blocks[b] = (int)(nblk + incl - nb);
+    nblk += sum;
+    total += block_scan(c * p.Hkv, &incl, scratch);
+  }
+  if (tid == 0) sp.blocks[p.B] = (int)nblk;
+  const long long N = nblk * p.Hkv, q = (N + ctas - 1) / ctas;
+  const long long per = max((long long)p.min_tiles, (total + ctas - 1) / ctas);
+  if (tid == 0) {
+    sp.plan->total = total;
+    sp.plan->per = per;
+    sp.plan->n_items = (int)(q * ctas);
+  }
+  __syncthreads();  // the blocks are read below
+  // ---- items, dealt out: place i = c * q + t holds item t * CTAs + c
+  long long before = 0;
+  for (long long base = 0; base < q * ctas; base += kPlanThreads) {
+    const long long i = base + tid, m = i < q * ctas ? (i % q) * ctas + i / q : N;
+    PagedItem it;
+    it.b = it.h = it.t0 = it.count = 0;
+    if (m < N) {
+      // the sequence: the last whose first item is not past m
+      int lo = 0, hi = p.B;  // blocks[lo] * Hkv <= m < blocks[hi] * Hkv
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if ((long long)__ldcg(&sp.blocks[mid]) * p.Hkv <= m) lo = mid;
+        else hi = mid;
+      }
+      const PagedSeq s = paged_seq(p, lo, false);
+      const int nb = paged_blocks(p, s.n), off = (int)(m - (long long)__ldcg(&sp.blocks[lo]) * p.Hkv);
+      it.b = lo;
+      it.h = off / nb;
+      it.t0 = (off % nb) * p.tpb;
+      it.count = paged_range<kTK>(p, s, it.t0, min(s.n, it.t0 + p.tpb)).count;
+    }
+    const long long sum = block_scan(it.count, &incl, scratch);
+    it.first = before + incl - it.count;
+    before += sum;
+    if (i < q * ctas) {
+      sp.items[i] = it;
+      // the shares that start inside this item
+      for (long long c = (it.first + per - 1) / per; it.count > 0 && c * per < it.first + it.count; ++c)
+        if (c < ctas) sp.start[c] = (int)i;
+    }
+  }
+  trace_end(kTkPagedPlan);
+}
 
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid_constant__ PagedTcParams sp) {
@@ -178,7 +327,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
   uint64_t *s_full = q_full + 4, *p_full = s_full + 2, *o_full = s_full + 4, *o_empty = s_full + 6,
            *p_half = s_full + 8;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 10);
-  long long *scratch = reinterpret_cast<long long *>(s_full + 11);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -202,9 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
   grid_dep_wait();
   trace_dep(kTkPagedAttnTc);
   grid_dep_launch();
-  const PagedShare sh = paged_plan<kTK, kThreads>(p, scratch);
+  PlanWalk<kTK> w(sp);
   if (tid == 0) p.desc[blockIdx.x].rows = 0;
-  if (sh.start >= sh.end) {
+  if (!w.valid()) {  // the same for the whole CTA
     trace_end(kTkPagedAttnTc);
     return;
   }
@@ -216,7 +364,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
 
   const int tpg = 128 / p.G, rpg = tpg * p.G;      // tokens and packed rows of a group
   bool ok = true;
-  PagedWalk<kTK> w(p, sh);
 
   // The launch gives every thread 168 registers, 384 x 168 = 64512 in all; the
   // third warpgroup needs few, a softmax row in registers needs more:
@@ -501,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         d.row0 = w.s.row0 + w.t0;
         d.rows = ntok * p.G;
         d.h = w.h;
-        d.last_cta = (int)((w.pos + w.r.count - 1) / sh.per);
+        d.last_cta = (int)((w.pos + w.r.count - 1) / w.per);
         p.desc[blockIdx.x] = d;
       }
       tc_fence_before();
@@ -526,6 +673,29 @@ cudaError_t paged_tc_set_attributes() {
   return e;
 }
 
+// Items at most: one more block a sequence than its rows fill, a place's round of
+// CTAs for the gaps.
+static size_t plan_items(int B, int n_rows, int G, int Hkv) {
+  return ((size_t)n_rows / (2 * (128 / G)) + B) * Hkv + kPagedMaxCtas;
+}
+
+static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+size_t paged_tc_plan_bytes(int B, int n_rows, int G, int Hkv) {
+  return 256 + up256((size_t)kPagedMaxCtas * 4) + up256(((size_t)B + 1) * 4) +
+         up256(plan_items(B, n_rows, G, Hkv) * sizeof(PagedItem));
+}
+
+void paged_tc_bind_plan(PagedTcParams &sp, char *base) {
+  sp.plan = reinterpret_cast<PagedPlan *>(base);
+  base += 256;
+  sp.start = reinterpret_cast<int *>(base);
+  base += up256((size_t)kPagedMaxCtas * 4);
+  sp.blocks = reinterpret_cast<int *>(base);
+  base += up256(((size_t)sp.a.B + 1) * 4);
+  sp.items = reinterpret_cast<PagedItem *>(base);
+}
+
 cudaError_t launch_paged_attn_tc(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
@@ -537,6 +707,16 @@ cudaError_t launch_paged_attn_tc(const PagedTcParams &sp, int ctas, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
+  const int smem = cfg.dynamicSmemBytes;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = 0;
+  note_launch();
+  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_tc_plan_kernel, sp, ctas);
+  if (e) return e;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   note_launch();
   return sp.a.Dh == 128 ? cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<128>, sp)
                         : cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<64>, sp);
