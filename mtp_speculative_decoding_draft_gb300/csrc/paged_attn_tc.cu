@@ -18,7 +18,8 @@
 // Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1, 128 each; P_g lies in the
 // first half of S_g.  Warps 0-3 and 4-7 are the groups' softmax, warp 8 brings
 // pages by TMA into a ring of K and V tiles, warp 9 issues the products, warp 10
-// brings the next block's queries as soon as the last scores are done.
+// brings the next block's queries as soon as the last scores are done, warp 11
+// clears rows of V.
 #include "internal.h"
 #include "paged.cuh"
 #include "paged_tc.cuh"
@@ -37,7 +38,7 @@ namespace {
 
 constexpr int kTK = 128;          // keys per tile
 constexpr int kThreads = 384;   // three warpgroups: the registers move between whole ones
-constexpr int kProducer = 8, kIssuer = 9, kQuery = 10;
+constexpr int kProducer = 8, kIssuer = 9, kQuery = 10, kClear = 11;
 constexpr unsigned kFull = 0xffffffffu;
 
 template <int DH>
@@ -322,9 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
   unsigned char *qbuf = smem;                      // [2 groups][halves][128][128 B]
   unsigned char *ring = smem + 2 * L::TILE;
   uint64_t *bars = reinterpret_cast<uint64_t *>(ring + L::RING);
-  uint64_t *full = bars, *empty = bars + ST;       // ring
-  uint64_t *q_full = bars + 2 * ST, *q_empty = q_full + 1, *z_bar = q_full + 2, *drain = q_full + 3;
-  uint64_t *s_full = q_full + 4, *p_full = s_full + 2, *o_full = s_full + 4, *o_empty = s_full + 6,
+  uint64_t *full = bars, *empty = bars + ST, *zbar = bars + 2 * ST;  // ring
+  uint64_t *q_full = bars + 3 * ST, *q_empty = q_full + 1, *drain = q_full + 2;
+  uint64_t *s_full = q_full + 3, *p_full = s_full + 2, *o_full = s_full + 4, *o_empty = s_full + 6,
            *p_half = s_full + 8;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 10);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -333,10 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
     for (int s = 0; s < ST; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&zbar[s], 1);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    mbar_init(z_bar, 1);
     mbar_init(drain, 1);
     for (int g = 0; g < 2; ++g) {
       mbar_init(&s_full[g], 1);
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       const int prow = min(p.page, kTK);             // rows of a piece: one page
       const int npc = (kTK / prow) * NB;             // pieces of a tile (at most 16)
       const int pc = lane / NB, hb = lane % NB;
-      int it = 0, zn = 0;
+      int it = 0;
       for (; w.valid() && ok; w.next()) {
         // the piece of this lane in tile i: whether a row sees it, and its row of the pool
         auto locate = [&](int i, bool &need, int &y) {
@@ -396,32 +397,42 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
             if (it >= ST) ok = mbar_wait(&empty[s], (uint32_t)((it / ST) - 1) & 1u, p.status);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
-            // Rows of V that no row sees (past the last key, before the window,
-            // never loaded) may hold anything, NaN too: in a tile that has such
-            // rows they are cleared before the tile is handed on.
-            const bool clear = isv && !whole;
-            uint64_t *bar = clear ? z_bar : &full[s];
-            unsigned char *dst = ring + (size_t)s * L::TILE;
-            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-            __syncwarp();
-            if (need) tma_2d(dst + hb * L::HALF + pc * prow * 128, isv ? &sp.mv : &sp.mk, 64 * hb, y, bar);
-            if (clear) {
-              ok = mbar_wait(z_bar, (uint32_t)(zn++) & 1u, p.status);
-              ok = __all_sync(kFull, ok);
-              for (int r = 0; r < kTK; ++r)
-                if (!w.r.sees(t0 + r) && lane < 8 * NB)
-                  *reinterpret_cast<uint4 *>(dst + (lane >> 3) * L::HALF + r * 128 + (lane & 7) * 16) =
-                      make_uint4(0u, 0u, 0u, 0u);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&full[s]);
-            }
-          }
+            // a V tile with rows to clear goes to the clearing warp first
+          uint64_t *bar = isv && !whole ? &zbar[s] : &full[s];
+          unsigned char *dst = ring + (size_t)s * L::TILE;
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+          __syncwarp();
+          if (need) tma_2d(dst + hb * L::HALF + pc * prow * 128, isv ? &sp.mv : &sp.mk, 64 * hb, y, bar);
         }
       }
+    }
       if (!ok)  // let copies still in flight land before the CTA exits
         for (int i = max(0, it - ST); i < it; ++i)
           if (!mbar_wait(&full[i % ST], (uint32_t)(i / ST) & 1u, p.status)) break;
+    } else if (warp == kClear) {
+      // ------------------------------------------------ rows of V that no row sees
+      // (past the last key, before the window, never loaded) may hold anything,
+      // NaN too: in a tile that has such rows they are cleared before the tile is
+      // handed on
+      uint32_t phases = 0;  // a bit a stage
+      int it = 1;
+      for (; w.valid() && ok; w.next()) {
+        for (int i = w.i0; i < w.i1 && ok; ++i, it += 2) {
+          const int t0 = w.r.tile(i) * kTK, s = it % ST;
+          if ((t0 + kTK <= w.r.hi && t0 >= w.r.lo) || t0 + kTK <= w.r.sink_end) continue;
+          ok = __all_sync(kFull, mbar_wait(&zbar[s], phases >> s & 1u, p.status));
+          phases ^= 1u << s;
+          unsigned char *tile = ring + (size_t)s * L::TILE;
+          for (int x = lane; x < kTK * 8; x += 32)
+            if (!w.r.sees(t0 + (x >> 3)))
+#pragma unroll
+              for (int hb = 0; hb < NB; ++hb)
+                *reinterpret_cast<uint4 *>(tile + hb * L::HALF + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+        }
+      }
     } else if (warp == kQuery) {
       // ------------------------------------------------ the blocks' queries
       if (lane == 0) {
@@ -447,44 +458,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       const uint64_t qd = sw128_kmajor_desc(smem_u32(qbuf)), kd = sw128_kmajor_desc(smem_u32(ring)),
                      vd = sw128_mnmajor_desc(smem_u32(ring), L::HALF);
       const bool leader = elect_one();
-      int it = 0, seg = 0, np[2] = {0, 0}, no[2] = {0, 0};
-      for (; __shfl_sync(kFull, w.valid() && ok, 0); w.next(), ++seg) {
+      // A wait that gives up flags the status; the waits after it are skipped and
+      // the rest is issued on whatever is there, so that no barrier is left short.
+      auto await = [&](uint64_t *bar, uint32_t parity) {
+        if (ok) ok = mbar_wait(bar, parity, p.status);
+      };
+      int ks = 0, vs = 0, seg = 0;  // stages of K_i and V_{i-1}
+      uint32_t kph = 0, vph = 0, pph[2] = {0, 0}, oph[2] = {1, 1};
+      for (; __shfl_sync(kFull, w.valid(), 0); w.next(), ++seg) {
         const int ng = __shfl_sync(kFull, w.t1() - w.t0 > tpg ? 2 : 1, 0), nt = __shfl_sync(kFull, w.i1 - w.i0, 0);
-        ok = __all_sync(kFull, mbar_wait(q_full, (uint32_t)seg & 1u, p.status));
-        for (int i = 0; i <= nt && ok; ++i, it += 2) {
-          // tiles it (K_i) and it + 1 (V_i); V_{i-1} is it - 1
-          const int ks = it % ST, vs = (it + ST - 1) % ST;
-          if (i > 0) ok = __all_sync(kFull, mbar_wait(&full[vs], (uint32_t)((it - 1) / ST) & 1u, p.status));
+        await(q_full, (uint32_t)seg & 1u);
+        for (int i = 0; i <= nt; ++i) {
+          if (i < nt) await(&full[ks], kph);
+          if (i > 0) await(&full[vs], vph);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            if (g >= ng || !ok) break;
+            if (g >= ng) break;
             if (i > 0) {
-              ok = mbar_wait(&p_half[g], (uint32_t)np[g] & 1u, p.status);
-              if (ok && i == 1) ok = mbar_wait(&o_empty[g], (uint32_t)((no[g]++) & 1) ^ 1u, p.status);
-              ok = __all_sync(kFull, ok);
-              if (!ok) break;
+              const uint64_t v = vd + (uint64_t)(vs * (L::TILE >> 4));
+              if (i == 1) {
+                await(&o_empty[g], oph[g]);
+                oph[g] ^= 1u;
+              }
+              await(&p_half[g], pph[g]);
               tc_fence_after();
               if (leader) {
-                const uint64_t v = vd + (uint64_t)(vs * (L::TILE >> 4));
 #pragma unroll
                 for (int k = 0; k < kTK / 32; ++k)
                   mma_ts(tm + L::O(g), tm + L::S(g) + 8 * k, v + (uint64_t)(k * (2048 >> 4)), id_o, k > 0 || i > 1);
               }
-              __syncwarp();
-              ok = __all_sync(kFull, mbar_wait(&p_full[g], (uint32_t)(np[g]++) & 1u, p.status));
-              if (!ok) break;
+              await(&p_full[g], pph[g]);
+              pph[g] ^= 1u;
               tc_fence_after();
               if (leader) {
-                const uint64_t v = vd + (uint64_t)(vs * (L::TILE >> 4));
 #pragma unroll
                 for (int k = kTK / 32; k < kTK / 16; ++k)
                   mma_ts(tm + L::O(g), tm + L::S(g) + 8 * k, v + (uint64_t)(k * (2048 >> 4)), id_o, 1u);
                 if (i == nt) mma_commit(&o_full[g]);
               }
-            }
-            if (i < nt && g == 0) {
-              ok = __all_sync(kFull, mbar_wait(&full[ks], (uint32_t)(it / ST) & 1u, p.status));
-              if (!ok) break;
             }
             if (i < nt && leader) {
               const uint64_t q = qd + (uint64_t)(g * (L::TILE >> 4)), kk = kd + (uint64_t)(ks * (L::TILE >> 4));
@@ -495,17 +506,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
               }
               mma_commit(&s_full[g]);
             }
-            __syncwarp();
           }
-          if (!ok) break;
           if (leader) {
-            if (i == nt - 1) mma_commit(q_empty);  // the block's last scores
-            if (i < nt) mma_commit(&empty[ks]);
             if (i > 0) mma_commit(&empty[vs]);
+            if (i < nt) mma_commit(&empty[ks]);
+            if (i == nt - 1) mma_commit(q_empty);  // the block's last scores
           }
           __syncwarp();
+          // V_i lies behind K_i, K_{i+1} behind V_i
+          vs = ks + 1 == ST ? 0 : ks + 1;
+          vph = ks + 1 == ST ? kph ^ 1u : kph;
+          if (i < nt) {
+            ks += 2;
+            if (ks >= ST) {
+              ks -= ST;
+              kph ^= 1u;
+            }
+          }
         }
-        it -= 2;  // the last round brought no K
       }
       if (leader) mma_commit(drain);  // nothing of this CTA is in flight when it frees its tensor memory
       __syncwarp();
@@ -518,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
     const uint32_t lanebase = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanebase + L::S(g), to = tmem + lanebase + L::O(g);
     int ns = 0, nseg = 0;
-    for (; w.valid() && ok; w.next()) {
+    for (; w.valid(); w.next()) {
       const int ntok = w.t1() - w.t0;
       if (g == 1 && ntok <= tpg) continue;
       const int tg0 = w.t0 + g * tpg, tg1 = min(w.t1(), tg0 + tpg);  // the group's tokens
@@ -532,9 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       for (int i = w.i0; i < w.i1; ++i) {
         const int k0 = w.r.tile(i) * kTK;
         const bool whole = k0 + kTK <= all_hi && (k0 >= all_lo || k0 + kTK <= min(p.sinks, all_hi));
-        ok = mbar_wait(&s_full[g], (uint32_t)(ns++) & 1u, p.status);
-        ok = __all_sync(kFull, ok);
-        if (!ok) break;
+        if (ok) ok = mbar_wait(&s_full[g], (uint32_t)(ns++) & 1u, p.status);
+        __syncwarp();
         tc_fence_after();
         uint32_t s[128];
 #pragma unroll
@@ -594,11 +611,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
-      if (!ok) break;
       // ---- the block's output, or this segment's state
-      ok = mbar_wait(&o_full[g], (uint32_t)(nseg++) & 1u, p.status);
-      ok = __all_sync(kFull, ok);
-      if (!ok) break;
+      if (ok) ok = mbar_wait(&o_full[g], (uint32_t)(nseg++) & 1u, p.status);
+      __syncwarp();
       tc_fence_after();
       const bool whole_item = w.starts() && w.ends();
       const int slot = w.starts() ? 1 : 0;
