@@ -409,25 +409,28 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 }
 
 // Joins the segments of the items that end in a later CTA than they start in, in
-// key order, a warp a row: block x takes the item that starts in CTA x of the
-// tensor-core kernel, then of the streaming kernel.
+// key order, a warp a row: the blocks go over the rows of the items that start in
+// each CTA of the tensor-core kernel, then of the streaming kernel.
 struct CombineParams {
   PagedArgs tc, st;
-  int tc_ctas, st_rows;
+  int tc_blocks, st_rows;  // blocks of the tensor-core items, rows of a streaming block
 };
+constexpr int kCombineRows = 8;  // rows of a block: a warp each
 
 template <int DH>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ CombineParams cp) {
+__global__ void __launch_bounds__(32 * kCombineRows) paged_combine_kernel(const __grid_constant__ CombineParams cp) {
   trace_start(kTkPagedCombine);
   grid_dep_wait();
   grid_dep_launch();
-  const bool tc = (int)blockIdx.x < cp.tc_ctas;
+  const bool tc = (int)blockIdx.x < cp.tc_blocks;
   const PagedArgs &p = tc ? cp.tc : cp.st;
-  const int block_rows = tc ? kPagedTcRows : cp.st_rows, cta = (int)blockIdx.x - (tc ? 0 : cp.tc_ctas);
+  const int block_rows = tc ? kPagedTcRows : cp.st_rows, per = block_rows / kCombineRows;
+  const int blk = (int)blockIdx.x - (tc ? 0 : cp.tc_blocks), cta = blk / per;
   constexpr int PER = DH / 32;
   const int lane = threadIdx.x & 31;
   const PagedDesc d = p.desc[cta];
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < d.rows; r += 8 * gridDim.y) {
+  const int r = (blk % per) * kCombineRows + (threadIdx.x >> 5);
+  if (r < d.rows) {
     const int nseg = d.last_cta - cta + 1;
     auto seg = [&](int i) { return ((size_t)(cta + i) * 2 + (i == 0 ? 1 : 0)) * block_rows + r; };
     float M = -INFINITY;
@@ -576,7 +579,7 @@ cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const 
   const int n = sms < kMaxSms ? sms : kMaxSms;
   char *base = static_cast<char *>(scratch);
   CombineParams cp;
-  cp.tc_ctas = 0;
+  cp.tc_blocks = 0;
   cp.tc = args;
   cudaError_t e;
   if (tc) {
@@ -596,7 +599,7 @@ cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const 
       return cudaErrorNotSupported;
     if ((e = launch_paged_attn_tc(tp, n, s, pdl))) return e;
     cp.tc = tp.a;
-    cp.tc_ctas = n;
+    cp.tc_blocks = n * (kPagedTcRows / kCombineRows);
   }
   StreamParams sp;
   sp.a = args;
@@ -617,7 +620,7 @@ cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const 
   cp.st = sp.a;
   cp.st_rows = rb;
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = config(dim3(cp.tc_ctas + ctas, tc ? 8 : (rb + 7) / 8), 256, 0, s, attr, pdl);
+  cudaLaunchConfig_t cfg = config(dim3(cp.tc_blocks + ctas * (rb / kCombineRows)), 32 * kCombineRows, 0, s, attr, pdl);
   note_launch();
   if (args.Dh == 32) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<32>, cp);
   if (args.Dh == 64) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<64>, cp);
