@@ -538,6 +538,37 @@ typedef struct {
 int spec_adjust_logits(int B, int k, int V, const MtpLogitRules *rules, const float *logits,
                        const int32_t *draft_tok, float *out, mtp_stream_t stream);
 
+/*
+ * The draft over a paged cache.  mtp_draft / spec_step with the draft module's
+ * K/V in pages and, optionally, its queries and keys rotated and its attention
+ * under a window: depth j's row is written at position ctx_len[b] + j of the
+ * pages by mtp_cache_append's kernel and attended by mtp_paged_attn's.  The
+ * caller's page table covers positions 0 .. ctx_len[b] + k - 1.
+ *   dims   as for mtp_draft; Lmax is not used
+ *   cache  the draft module's own pools (its block has its own attention)
+ *   rope, window, sinks  as above (NULL, 0, 0: mtp_draft's block)
+ *   ws     mtp_paged_workspace_size(dims, k) bytes, zero before its first use
+ * Everything else is as for mtp_draft / spec_step.  Queries are rounded to bf16
+ * after the rotation, keys once more, and the softmax weights to bf16 (mtp_draft
+ * keeps fp32 there): its tolerance on the logits holds all the same.
+ */
+size_t mtp_paged_workspace_size(const MtpDims *dims, int k);
+
+int mtp_draft_paged(const MtpDims *dims, const MtpWeights *w, const MtpPagedCache *cache,
+                    const MtpRope *rope, int window, int sinks, const void *h,
+                    const int32_t *last_tok, const int32_t *ctx_len, int k, float T, int mode,
+                    const float *u_draft, int32_t *draft_tok, float *draft_logits,
+                    void *ws, size_t ws_bytes, mtp_stream_t stream);
+
+int spec_step_paged(const MtpDims *dims, const MtpWeights *w, const MtpPagedCache *cache,
+                    const MtpRope *rope, int window, int sinks, const void *h,
+                    const int32_t *last_tok, const int32_t *ctx_len, int k, float T, int mode,
+                    const float *u_draft, const float *target_logits,
+                    const float *u_accept, const float *u_final,
+                    int32_t *draft_tok, float *draft_logits,
+                    int32_t *out_tok, int32_t *accept_len, int32_t *num_accepted,
+                    void *ws, size_t ws_bytes, mtp_stream_t stream);
+
 /* Wait for the stream, then copy the workspace's status word (MTP_STATUS_* bits)
  * to *status.  Returns MTP_OK or MTP_ERR_*. */
 int mtp_get_status(const void *ws, mtp_stream_t stream, int32_t *status);

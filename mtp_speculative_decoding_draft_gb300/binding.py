@@ -138,6 +138,15 @@ def _lib():
         L.mtp_paged_attn.argtypes = [ctypes.POINTER(MtpPagedCache), I, I, I, I, P, P, P, L64, F, I, I, P, L64, P, P, Z,
                                      P]
         L.mtp_paged_attn.restype = I
+        L.mtp_paged_workspace_size.argtypes = [ctypes.POINTER(MtpDims), I]
+        L.mtp_paged_workspace_size.restype = Z
+        PC, PR = ctypes.POINTER(MtpPagedCache), ctypes.POINTER(MtpRope)
+        L.mtp_draft_paged.argtypes = [ctypes.POINTER(MtpDims), ctypes.POINTER(MtpWeights), PC, PR, I, I, P, P, P, I, F,
+                                      I, P, P, P, P, Z, P]
+        L.mtp_draft_paged.restype = I
+        L.spec_step_paged.argtypes = [ctypes.POINTER(MtpDims), ctypes.POINTER(MtpWeights), PC, PR, I, I, P, P, P, I, F,
+                                      I, P, P, P, P, P, P, P, P, P, P, Z, P]
+        L.spec_step_paged.restype = I
         L.spec_adjust_logits.argtypes = [I, I, I, ctypes.POINTER(MtpLogitRules), P, P, P, P]
         L.spec_adjust_logits.restype = I
         L.mtp_get_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
@@ -548,6 +557,51 @@ def mtp_paged_attn(cache, row_start, ctx_len, q, out, lse, ws, scale=0.0, window
                                ws.numel() * ws.element_size(), _stream(stream))
     if rc != 0:
         raise MtpError(rc, "mtp_paged_attn")
+
+
+def paged_workspace_size(dims, k):
+    return int(_lib().mtp_paged_workspace_size(ctypes.byref(dims), int(k)))
+
+
+def mtp_draft_paged(dims, weights, cache, rope, h, last_tok, ctx_len, k, T, mode, u_draft, draft_tok, draft_logits, ws,
+                    window=0, sinks=0, stream=None):
+    """mtp_draft with the module's K/V in the pages of cache (make_paged_cache),
+    rotated by rope (make_rope, or None)."""
+    B, V = dims.B, dims.V
+    if cache.B < B:
+        raise ValueError("page_table has %d sequences, dims.B is %d" % (cache.B, B))
+    rc = _lib().mtp_draft_paged(
+        ctypes.byref(dims), ctypes.byref(weights), cache, rope, int(window), int(sinks),
+        _ptr(h, "h", torch.bfloat16, B * dims.d), _ptr(last_tok, "last_tok", torch.int32, B),
+        _ptr(ctx_len, "ctx_len", torch.int32, B), int(k), float(T), int(mode),
+        _ptr(u_draft, "u_draft", torch.float32, B * k), _ptr(draft_tok, "draft_tok", torch.int32, B * k),
+        _ptr(draft_logits, "draft_logits", torch.float32, B * k * V),
+        _ptr(ws, "ws"), ws.numel() * ws.element_size(), _stream(stream))
+    if rc != 0:
+        raise MtpError(rc, "mtp_draft_paged")
+
+
+def spec_step_paged(dims, weights, cache, rope, h, last_tok, ctx_len, k, T, mode, u_draft, target_logits, u_accept,
+                    u_final, draft_tok, draft_logits, out_tok, accept_len, num_accepted, ws, window=0, sinks=0,
+                    stream=None):
+    """spec_step over a paged cache (see mtp_draft_paged)."""
+    B, V = dims.B, dims.V
+    if cache.B < B:
+        raise ValueError("page_table has %d sequences, dims.B is %d" % (cache.B, B))
+    rc = _lib().spec_step_paged(
+        ctypes.byref(dims), ctypes.byref(weights), cache, rope, int(window), int(sinks),
+        _ptr(h, "h", torch.bfloat16, B * dims.d), _ptr(last_tok, "last_tok", torch.int32, B),
+        _ptr(ctx_len, "ctx_len", torch.int32, B), int(k), float(T), int(mode),
+        _ptr(u_draft, "u_draft", torch.float32, B * k),
+        _ptr(target_logits, "target_logits", torch.float32, B * (k + 1) * V),
+        _ptr(u_accept, "u_accept", torch.float32, B * k), _ptr(u_final, "u_final", torch.float32, B),
+        _ptr(draft_tok, "draft_tok", torch.int32, B * k),
+        _ptr(draft_logits, "draft_logits", torch.float32, B * k * V),
+        _ptr(out_tok, "out_tok", torch.int32, B * (k + 1)), _ptr(accept_len, "accept_len", torch.int32, B),
+        _ptr(num_accepted, "num_accepted", torch.int32, B),
+        _ptr(ws, "ws"), ws.numel() * ws.element_size(), _stream(stream))
+    if rc != 0:
+        raise MtpError(rc, "spec_step_paged")
 
 
 def make_logit_rules(history=None, prompt_len=None, hist_len=None, rep=None, freq=None, pres=None, bias_tok=None,

@@ -194,6 +194,15 @@ struct Draft {
   TcBufs t;
   MtpModule mods[kMaxModules];
   int nmod;
+  // K/V in pages (paged set): the projections store their K/V rows in a small
+  // contiguous scratch cache of k + 1 positions, as if every context were empty
+  bool paged = false;
+  AppendArgs append;  // of depth 0
+  PagedArgs attn;
+  const void *k_pages = nullptr, *v_pages = nullptr;
+  void *attn_scratch = nullptr;
+  int *zero_ctx = nullptr;
+  int sms = 0;
 };
 
 // Point the context at module m's weights and K/V cache.
@@ -216,7 +225,71 @@ struct DraftOpts {
   const void *head = nullptr;     // [Vd, d] bf16
   const int32_t *vmap = nullptr;  // [Vd]
   int Vd = 0;
+  // the K/V cache in pages
+  const MtpPagedCache *cache = nullptr;
+  const MtpRope *rope = nullptr;
+  int window = 0, sinks = 0;
 };
+
+// Workspace of a paged draft behind draft_layout()'s: empty contexts, the
+// rotated queries, the scratch cache and the attention's partial states.
+struct PagedLayout {
+  size_t ctx, q, kv, attn, total;
+  size_t kv_bytes;  // of the scratch K cache (the V cache follows)
+};
+
+PagedLayout paged_layout(const MtpDims &d, int k, size_t base) {
+  PagedLayout L{};
+  size_t off = base;
+  L.ctx = off;
+  off += up((size_t)d.B * 4);
+  L.q = off;
+  off += up((size_t)d.B * d.Hq * d.Dh * 2);
+  L.kv = off;
+  L.kv_bytes = up((size_t)d.B * d.Hkv * (k + 1) * d.Dh * 2);
+  off += 2 * L.kv_bytes;
+  L.attn = off;
+  off += up(paged_attn_scratch_bytes(d.B, d.Hkv, d.B, 1, d.Hq / d.Hkv, d.Dh));
+  L.total = off;
+  return L;
+}
+
+// The dims a paged draft runs the projections with (its Lmax is not the caller's).
+MtpDims paged_dims(const MtpDims &d, int k) {
+  MtpDims p = d;
+  p.Lmax = k + 1;
+  return p;
+}
+
+// The cache's description is sound (the table's entries are the device's to check).
+int check_cache(const MtpPagedCache *c) {
+  if (!c || c->Hkv < 1 || c->n_pages < 1 || c->max_pages < 1) return MTP_ERR_INVALID_ARG;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !aligned16(c->page_table)) return MTP_ERR_INVALID_ARG;
+  if (c->Dh != 32 && c->Dh != 64 && c->Dh != 128) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return MTP_ERR_UNSUPPORTED_SHAPE;
+  // rows of the pools are TMA coordinates, positions 32-bit
+  if ((long long)c->n_pages * c->Hkv * c->page >= (1ll << 31)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if ((long long)c->max_pages * c->page > (1ll << 30)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  return MTP_OK;
+}
+
+int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+bool rope_ok(const MtpRope *rope, int Dh, int *rc) {
+  *rc = MTP_OK;
+  if (!rope) return true;
+  if (rope->layout != MTP_ROPE_HALF && rope->layout != MTP_ROPE_INTERLEAVED) *rc = MTP_ERR_INVALID_ARG;
+  else if (!aligned16(rope->turns) || !(rope->scale > 0.f && rope->scale < 1e30f)) *rc = MTP_ERR_INVALID_ARG;
+  else if (rope->rot_dim < 8 || rope->rot_dim % 8 || rope->rot_dim > Dh) *rc = MTP_ERR_UNSUPPORTED_SHAPE;
+  return *rc == MTP_OK;
+}
+
+void set_rope(AppendArgs &a, const MtpRope *rope) {
+  a.rot = rope ? rope->rot_dim : 0;
+  a.layout = rope ? rope->layout : 0;
+  a.turns = rope ? reinterpret_cast<const unsigned long long *>(rope->turns) : nullptr;
+  a.scale = rope ? rope->scale : 1.f;
+}
 
 int prepare_draft(const MtpDims *dims, const MtpModule *mods, int nmod, const void *h, const int32_t *last_tok,
                   const int32_t *ctx_len, int k, float T, int mode, const float *u_draft, int32_t *draft_tok,
@@ -246,7 +319,9 @@ int prepare_draft(const MtpDims *dims, const MtpModule *mods, int nmod, const vo
   if ((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MTP_ERR_INVALID_ARG;
   if (draft_only && logits_in_ws) return MTP_ERR_INVALID_ARG;
   const WsLayout L = draft_layout(*dims, k, draft_only);
-  if (ws_bytes < L.total) return MTP_ERR_WORKSPACE;
+  const PagedLayout P = paged_layout(*dims, k, L.total);
+  if (ws_bytes < (o.cache ? P.total : L.total)) return MTP_ERR_WORKSPACE;
+  if (o.cache && !tc_available()) return MTP_ERR_CUDA;
   DevInfo di;
   if ((rc = device_info(&di))) return rc;
 
@@ -298,7 +373,55 @@ int prepare_draft(const MtpDims *dims, const MtpModule *mods, int nmod, const vo
     c.seq_order = reinterpret_cast<int *>(base + L.order);
     out->t.part_floats = L.tz.part_floats;
   }
+  out->paged = o.cache != nullptr;
+  if (out->paged) {
+    const MtpPagedCache &pc = *o.cache;
+    out->zero_ctx = reinterpret_cast<int *>(base + P.ctx);
+    c.ctx_len = out->zero_ctx;
+    AppendArgs &a = out->append;
+    a = AppendArgs{};
+    a.B = d.B; a.Hq = d.Hq; a.Hkv = d.Hkv; a.Dh = d.Dh;
+    a.page = pc.page; a.page_shift = page_shift(pc.page); a.n_pages = pc.n_pages; a.max_pages = pc.max_pages;
+    a.cap = pc.max_pages * pc.page; a.n_rows = d.B;
+    set_rope(a, o.rope);
+    a.ctx_len = ctx_len; a.page_table = pc.page_table;
+    a.q = c.q; a.q_f32 = 1; a.ldq = a.ldqo = (long long)d.Hq * d.Dh;
+    a.k = out->mods[0].k_cache; a.v = out->mods[0].v_cache;
+    a.khs = a.vhs = (long long)d.Lmax * d.Dh;
+    a.ldk = a.ldv = a.khs * d.Hkv;
+    a.q_out = base + P.q;
+    a.k_pages = static_cast<uint16_t *>(pc.k_pages); a.v_pages = static_cast<uint16_t *>(pc.v_pages);
+    a.status = c.status;
+    PagedArgs &t = out->attn;
+    t = PagedArgs{};
+    t.B = d.B; t.Hq = d.Hq; t.Hkv = d.Hkv; t.G = d.Hq / d.Hkv; t.Dh = d.Dh;
+    t.page = a.page; t.page_shift = a.page_shift; t.n_pages = a.n_pages; t.max_pages = a.max_pages; t.cap = a.cap;
+    t.n_rows = d.B; t.ctx_len = ctx_len; t.page_table = pc.page_table;
+    t.q = static_cast<const uint16_t *>(a.q_out); t.ldq = t.ldo = a.ldq;
+    t.out = c.o; t.out_f32 = 1;
+    t.scale_log2 = 1.f / sqrtf((float)d.Dh) * 1.4426950408889634f;
+    t.window = o.window; t.sinks = o.window ? o.sinks : 0;
+    t.status = c.status;
+    out->k_pages = pc.k_pages; out->v_pages = pc.v_pages;
+    out->attn_scratch = base + P.attn;
+    out->sms = di.sms;
+  }
   return MTP_OK;
+}
+
+// Depth c.j's attention: over the contiguous cache, or the row's K/V written to
+// its page slot (and q, k rotated) and attended over the pages.
+cudaError_t run_attention(const Draft &D, const DraftCtx &c, cudaStream_t s, bool pdl) {
+  if (!D.paged) return launch_attention(c, D.attn_cluster, s, pdl);
+  AppendArgs a = D.append;
+  a.ctx_add = c.j;
+  a.k = static_cast<const uint16_t *>(a.k) + (size_t)c.j * c.Dh;
+  a.v = static_cast<const uint16_t *>(a.v) + (size_t)c.j * c.Dh;
+  cudaError_t e = launch_cache_append(a, s, pdl);
+  if (e) return e;
+  PagedArgs t = D.attn;
+  t.ctx_add = c.j;
+  return launch_paged_attn(t, D.k_pages, D.v_pages, 1, D.attn_scratch, D.sms, s, pdl);
 }
 
 // Programmatic dependent launch between the chained kernels (MTP_PDL=0 turns it
@@ -324,7 +447,7 @@ bool use_verify_split() {
 // measured faster (1077 against 911 steps/s).
 bool use_chain(const Draft &D) {
   const char *v = getenv("MTP_CHAIN");
-  if (!(v && v[0] == '1') || D.tc) return false;
+  if (!(v && v[0] == '1') || D.tc || D.paged) return false;
   const GemvPlan *ps[] = {&D.fc, &D.qkv, &D.wo, &D.gateup, &D.down, &D.lm};
   for (const GemvPlan *p : ps)
     if (!chain_op_ok(*p)) return false;
@@ -409,6 +532,7 @@ cudaError_t run_draft(Draft &D, cudaStream_t s) {
   const bool pdl = use_pdl();
   NvtxRange call_range("mtp_draft chain");
   if (use_chain(D)) return run_draft_chain(D, s, pdl);
+  if (D.paged && (e = cudaMemsetAsync(D.zero_ctx, 0, (size_t)D.c.B * 4, s))) return e;
   if (D.c.vmap && D.c.logits) {  // a reduced head writes only its ids: the rest of each row is -inf
     e = launch_fill(D.c.logits, (size_t)D.c.B * D.c.k * D.c.V, -INFINITY, s, pdl);
     if (e) return e;
@@ -424,14 +548,14 @@ cudaError_t run_draft(Draft &D, cudaStream_t s) {
     c.zero_counters = j == 0;
     if (D.tc) {  // tensor-core path
       if ((e = timed(MTP_KC_GEMV, s, [&] { return run_block_pre_tc(c, D.t, s, pdl); }))) break;
-      if ((e = timed(MTP_KC_ATTN, s, [&] { return launch_attention(c, D.attn_cluster, s, pdl); }))) break;
+      if ((e = timed(MTP_KC_ATTN, s, [&] { return run_attention(D, c, s, pdl); }))) break;
       if ((e = timed(MTP_KC_GEMV, s, [&] { return run_block_post_tc(c, D.t, s, pdl); }))) break;
       if ((e = timed(MTP_KC_LMHEAD, s, [&] { return run_lmhead_tc(c, D.t, s, pdl); }))) break;
       continue;
     }
     if ((e = timed(MTP_KC_GEMV, s, [&] { return launch_gemv(c, D.fc, s, pdl); }))) break;
     if ((e = timed(MTP_KC_GEMV, s, [&] { return launch_gemv(c, D.qkv, s, pdl); }))) break;
-    if ((e = timed(MTP_KC_ATTN, s, [&] { return launch_attention(c, D.attn_cluster, s, pdl); }))) break;
+    if ((e = timed(MTP_KC_ATTN, s, [&] { return run_attention(D, c, s, pdl); }))) break;
     if ((e = timed(MTP_KC_GEMV, s, [&] { return launch_gemv(c, D.wo, s, pdl); }))) break;
     if ((e = timed(MTP_KC_GEMV, s, [&] { return launch_gemv(c, D.gateup, s, pdl); }))) break;
     if ((e = timed(MTP_KC_GEMV, s, [&] { return launch_gemv(c, D.down, s, pdl); }))) break;
@@ -604,6 +728,53 @@ int mtp_draft_dynamic(const MtpDims *dims, const MtpWeights *w, const void *h, c
   return cuda_rc(e);
 }
 
+size_t mtp_paged_workspace_size(const MtpDims *dims, int k) {
+  if (!dims || k < 1 || k > 8) return 0;
+  const MtpDims d = paged_dims(*dims, k);
+  if (check_dims(&d, k) != MTP_OK) return 0;
+  return paged_layout(d, k, draft_layout(d, k).total).total;
+}
+
+// The arguments that only the paged calls have; *one: the module over the
+// workspace's scratch cache.
+static int paged_call(const MtpDims *dims, const MtpWeights *w, const MtpPagedCache *cache, const MtpRope *rope,
+                      int window, int sinks, int k, void *ws, MtpDims *d, MtpModule *one, DraftOpts *o) {
+  if (!dims || !w || !ws || k < 1 || k > 8) return MTP_ERR_INVALID_ARG;
+  *d = paged_dims(*dims, k);
+  int rc = check_dims(d, k);
+  if (!rc) rc = check_cache(cache);
+  if (rc) return rc;
+  if (cache->Hkv != dims->Hkv || cache->Dh != dims->Dh || window < 0 || sinks < 0) return MTP_ERR_INVALID_ARG;
+  if (!rope_ok(rope, dims->Dh, &rc)) return rc;
+  const PagedLayout P = paged_layout(*d, k, draft_layout(*d, k).total);
+  char *base = static_cast<char *>(ws);
+  *one = MtpModule{*w, base + P.kv, base + P.kv + P.kv_bytes};
+  o->cache = cache;
+  o->rope = rope;
+  o->window = window;
+  o->sinks = sinks;
+  return MTP_OK;
+}
+
+int mtp_draft_paged(const MtpDims *dims, const MtpWeights *w, const MtpPagedCache *cache, const MtpRope *rope,
+                    int window, int sinks, const void *h, const int32_t *last_tok, const int32_t *ctx_len, int k,
+                    float T, int mode, const float *u_draft, int32_t *draft_tok, float *draft_logits, void *ws,
+                    size_t ws_bytes, mtp_stream_t stream) {
+  MtpDims d;
+  MtpModule one;
+  DraftOpts o;
+  int rc = paged_call(dims, w, cache, rope, window, sinks, k, ws, &d, &one, &o);
+  if (rc) return rc;
+  Draft D;
+  rc = prepare_draft(&d, &one, 1, h, last_tok, ctx_len, k, T, mode, u_draft, draft_tok, draft_logits, ws, ws_bytes,
+                     false, o, &D);
+  if (rc) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = run_draft(D, s);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return cuda_rc(e);
+}
+
 int mtp_draft_noalloc(const MtpDims *dims, const MtpWeights *w, const void *h, const int32_t *last_tok,
                       void *k_cache, void *v_cache, const int32_t *ctx_len, int k, float T, int mode,
                       const float *u_draft, int32_t *draft_tok, float *draft_logits, int32_t *status,
@@ -741,6 +912,20 @@ int spec_step(const MtpDims *dims, const MtpWeights *w, const void *h, const int
                            u_final, draft_tok, draft_logits, out_tok, accept_len, num_accepted, ws, ws_bytes, stream);
 }
 
+int spec_step_paged(const MtpDims *dims, const MtpWeights *w, const MtpPagedCache *cache, const MtpRope *rope,
+                    int window, int sinks, const void *h, const int32_t *last_tok, const int32_t *ctx_len, int k,
+                    float T, int mode, const float *u_draft, const float *target_logits, const float *u_accept,
+                    const float *u_final, int32_t *draft_tok, float *draft_logits, int32_t *out_tok,
+                    int32_t *accept_len, int32_t *num_accepted, void *ws, size_t ws_bytes, mtp_stream_t stream) {
+  MtpDims d;
+  MtpModule one;
+  DraftOpts o;
+  int rc = paged_call(dims, w, cache, rope, window, sinks, k, ws, &d, &one, &o);
+  if (rc) return rc;
+  return step_call(&d, &one, 1, h, last_tok, ctx_len, k, T, mode, o, u_draft, target_logits, u_accept, u_final,
+                   draft_tok, draft_logits, out_tok, accept_len, num_accepted, ws, ws_bytes, stream);
+}
+
 size_t spec_verify_fused_workspace_size(int B, int k, int V, int d, int mode) {
   if (!fused_shape_ok(B, k, V, d) || (mode != MTP_GREEDY && mode != MTP_STOCHASTIC)) return 0;
   if (mode == MTP_STOCHASTIC && (long long)B * k * ((V + 255) / 256) >= (1ll << 31)) return 0;
@@ -785,20 +970,6 @@ int spec_verify_fused(int B, int k, int V, int d, float T, int mode, const void 
 
 namespace mtp {
 namespace {
-
-// The cache's description is sound (the table's entries are the device's to check).
-int check_cache(const MtpPagedCache *c) {
-  if (!c || c->Hkv < 1 || c->n_pages < 1 || c->max_pages < 1) return MTP_ERR_INVALID_ARG;
-  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !aligned16(c->page_table)) return MTP_ERR_INVALID_ARG;
-  if (c->Dh != 32 && c->Dh != 64 && c->Dh != 128) return MTP_ERR_UNSUPPORTED_SHAPE;
-  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return MTP_ERR_UNSUPPORTED_SHAPE;
-  // rows of the pools are TMA coordinates, positions 32-bit
-  if ((long long)c->n_pages * c->Hkv * c->page >= (1ll << 31)) return MTP_ERR_UNSUPPORTED_SHAPE;
-  if ((long long)c->max_pages * c->page > (1ll << 30)) return MTP_ERR_UNSUPPORTED_SHAPE;
-  return MTP_OK;
-}
-
-int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
 int check_rows(const MtpPagedCache *c, int B, int Hq, int n_rows, const int32_t *row_start, const int32_t *ctx_len) {
   if (B < 1 || n_rows < 1 || Hq < 1) return MTP_ERR_INVALID_ARG;
@@ -869,21 +1040,15 @@ int mtp_cache_append(const MtpPagedCache *cache, const MtpRope *rope, int B, int
   if (q && (!aligned16(q) || !aligned16(q_out) || !row_stride_ok(ldq, qw) || !row_stride_ok(ldqo, qw)))
     return MTP_ERR_INVALID_ARG;
   if (q == q_out && q && ldq != ldqo) return MTP_ERR_INVALID_ARG;
-  if (rope) {
-    if (rope->layout != MTP_ROPE_HALF && rope->layout != MTP_ROPE_INTERLEAVED) return MTP_ERR_INVALID_ARG;
-    if (!aligned16(rope->turns) || !(rope->scale > 0.f && rope->scale < 1e30f)) return MTP_ERR_INVALID_ARG;
-    if (rope->rot_dim < 8 || rope->rot_dim % 8 || rope->rot_dim > cache->Dh) return MTP_ERR_UNSUPPORTED_SHAPE;
-  }
+  if (!rope_ok(rope, cache->Dh, &rc)) return rc;
   if (!aligned16(ws) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MTP_ERR_INVALID_ARG;
   if (ws_bytes < kAlign) return MTP_ERR_WORKSPACE;
   AppendArgs a{};
   a.B = B; a.Hq = q ? Hq : 0; a.Hkv = cache->Hkv; a.Dh = cache->Dh;
   a.page = cache->page; a.page_shift = page_shift(cache->page); a.n_pages = cache->n_pages;
   a.max_pages = cache->max_pages; a.cap = cache->max_pages * cache->page; a.n_rows = n_rows;
-  a.rot = rope ? rope->rot_dim : 0;
-  a.layout = rope ? rope->layout : 0;
-  a.turns = rope ? reinterpret_cast<const unsigned long long *>(rope->turns) : nullptr;
-  a.scale = rope ? rope->scale : 1.f;
+  set_rope(a, rope);
+  a.khs = a.vhs = cache->Dh;
   a.row_start = row_start; a.ctx_len = ctx_len; a.page_table = cache->page_table;
   a.q = q; a.k = k; a.v = v; a.ldq = ldq; a.ldk = ldk; a.ldv = ldv; a.ldqo = ldqo; a.q_out = q_out;
   a.k_pages = static_cast<uint16_t *>(cache->k_pages);

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(32 * kAppWarps) cache_append_kernel(const __gr
   grid_dep_wait();
   trace_dep(kTkAppend);
   grid_dep_launch();
-  if (blockIdx.x == 0) {  // once per call: are the row starts in order and inside the rows?
+  if (blockIdx.x == 0 && p.row_start) {  // once per call: are the row starts in order and inside the rows?
     bool bad = false;
     for (int i = threadIdx.x; i < p.B; i += 32 * kAppWarps) {
       const int x = __ldcg(&p.row_start[i]), y = __ldcg(&p.row_start[i + 1]);
@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(32 * kAppWarps) cache_append_kernel(const __gr
     if (which[n] >= 0 && !(p.q_f32 && which[n] == 0)) {
       const void *base = which[n] == 0 ? p.q : which[n] == 1 ? p.k : p.v;
       const long long ld = which[n] == 0 ? p.ldq : which[n] == 1 ? p.ldk : p.ldv;
-      const uint16_t *src = static_cast<const uint16_t *>(base) + (long long)row * ld + head[n] * p.Dh;
+      const uint16_t *src = static_cast<const uint16_t *>(base) + (long long)row * ld +
+                            head[n] * (which[n] == 0 ? p.Dh : which[n] == 1 ? p.khs : p.vhs);
       a[n] = __ldcs(reinterpret_cast<const T *>(src + e0[n]));
       c[n] = __ldcs(reinterpret_cast<const T *>(src + e1[n]));
     }
@@ -133,11 +134,12 @@ __global__ void __launch_bounds__(32 * kAppWarps) cache_append_kernel(const __gr
 
   // ---- the row's sequence: the last one that starts at or before it (those that
   // start at the same row are empty but the last of them)
-  const int b = starts_upto(p.row_start, p.B, row, lane) - 1;
+  const int b = p.row_start ? starts_upto(p.row_start, p.B, row, lane) - 1 : row;
   bool real = false;
   int pos = 0, page = -1;
   if (b >= 0) {
-    const int s0 = __ldcg(&p.row_start[b]), s1 = __ldcg(&p.row_start[b + 1]), c0 = __ldcg(&p.ctx_len[b]);
+    const int s0 = p.row_start ? __ldcg(&p.row_start[b]) : row, s1 = p.row_start ? __ldcg(&p.row_start[b + 1]) : row + 1;
+    const int c0 = __ldcg(&p.ctx_len[b]) + p.ctx_add;
     const int ctx = min(max(c0, 0), p.cap);
     real = row < s1 && s0 >= 0 && row >= s0;
     pos = ctx + row - s0;

@@ -37,8 +37,9 @@ struct PagedArgs {
   int B, Hq, Hkv, G, Dh;
   int page, page_shift, n_pages, max_pages, cap;  // cap = max_pages * page
   int n_rows;
-  const int *row_start;   // [B + 1]
-  const int *ctx_len;     // [B]
+  const int *row_start;   // [B + 1]; null: one row a sequence
+  const int *ctx_len;     // [B], ctx_add more positions each
+  int ctx_add;
   const int *page_table;  // [B, max_pages]
   const uint16_t *q;      // bf16 rows of Hq * Dh, ldq elements apart
   long long ldq, ldo;
@@ -67,7 +68,8 @@ struct PagedSeq {
 
 // Sequence b's rows and context, clamped to the buffers; flags what was out of range.
 __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs &p, int b, bool flag) {
-  const int a = __ldcg(&p.row_start[b]), e = __ldcg(&p.row_start[b + 1]), c = __ldcg(&p.ctx_len[b]);
+  const int a = p.row_start ? __ldcg(&p.row_start[b]) : b, e = p.row_start ? __ldcg(&p.row_start[b + 1]) : b + 1;
+  const int c = __ldcg(&p.ctx_len[b]) + p.ctx_add;
   PagedSeq s;
   s.row0 = min(max(a, 0), p.n_rows);
   s.n = min(max(e, s.row0), p.n_rows) - s.row0;
@@ -271,9 +273,11 @@ struct AppendArgs {
   int rot, layout;              // rot 0: no rotation
   const unsigned long long *turns;  // [rot / 2] turns a position, 0.64 fixed point
   float scale;
-  const int *row_start, *ctx_len, *page_table;
-  const void *q, *k, *v;        // bf16 (q32: fp32 q)
+  const int *row_start, *ctx_len, *page_table;  // row_start null: one row a sequence
+  int ctx_add;                  // positions past ctx_len
+  const void *q, *k, *v;        // bf16
   long long ldq, ldk, ldv, ldqo;
+  long long khs, vhs;           // elements between heads of k and v
   void *q_out;
   uint16_t *k_pages, *v_pages;
   int *status;

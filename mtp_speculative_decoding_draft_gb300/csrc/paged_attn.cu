@@ -117,6 +117,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   trace_dep(kTkPagedAttn);
   grid_dep_launch();
   const PagedShare sh = paged_plan<kTK, kThreads>(p, scratch);  // its barriers publish the mbarriers
+  trace_mark(kTkPagedAttn, 0);  // share known
   if (tid == 0) p.desc[blockIdx.x].rows = 0;
   if (sh.start >= sh.end) {
     grid_dep_wait();
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       *reinterpret_cast<uint4 *>(ubuf + at<DH>(r, c, RB)) = v;
     }
     named_sync(1, 32 * kCW);
+    trace_mark(kTkPagedAttn, 1);  // queries staged
     uint32_t qf[KS][4];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) ldsm4(qb + at<DH>(rg * 16 + arow, 2 * ks + acol, RB), qf[ks]);
@@ -316,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       if (lane == 0) mbar_arrive(&empty[s]);
     }
 
+    trace_mark(kTkPagedAttn, 2);  // last tile done
     // ---- merge the key groups; write the output, or this segment's state
 #pragma unroll
     for (int e = 0; e < 2; ++e) {

@@ -140,3 +140,28 @@ def test_rope_frequencies(lib):
     import torch
     with pytest.raises(bd.MtpError):
         bd.rope_table(torch.tensor([math.nan], dtype=torch.float64))
+
+
+def test_paged_draft_refusals(lib):
+    dims = bd.make_dims(2, 64, 8, 2, 64, 128, 500, 0)      # Lmax is not used
+    weights = bd.MtpWeights(*[OK_PTR.value] * len(bd.WEIGHT_FIELDS))
+    good = cache(Hkv=2, Dh=64)
+    need = lib.mtp_paged_workspace_size(ctypes.byref(dims), 3)
+    assert need > lib.mtp_workspace_size(ctypes.byref(bd.make_dims(2, 64, 8, 2, 64, 128, 500, 4)), 3)
+    assert lib.mtp_paged_workspace_size(ctypes.byref(dims), 0) == 0 and lib.mtp_paged_workspace_size(None, 3) == 0
+
+    def call(c=good, r=None, k=3, window=0, sinks=0, d=dims, wt=weights, wsb=0, ws=OK_PTR):
+        draft = lib.mtp_draft_paged(d, wt, c, r, window, sinks, OK_PTR, OK_PTR, OK_PTR, k, 1.0, 0, None, OK_PTR, None, ws,
+                                    wsb, None)
+        step = lib.spec_step_paged(d, wt, c, r, window, sinks, OK_PTR, OK_PTR, OK_PTR, k, 1.0, 0, None, OK_PTR, None, None,
+                                   OK_PTR, None, OK_PTR, OK_PTR, OK_PTR, ws, wsb, None)
+        assert draft == step
+        return draft
+    assert call() == WORKSPACE and call(wsb=need - 1) == WORKSPACE
+    assert call(r=rope(rot=64), wsb=need - 1) == WORKSPACE
+    assert call(c=None) == INVALID and call(wt=None) == INVALID and call(ws=None) == INVALID and call(k=9) == INVALID
+    assert call(c=cache(Hkv=8, Dh=64)) == INVALID and call(c=cache(Hkv=2, Dh=128)) == INVALID   # not the dims' heads
+    assert call(c=cache(Hkv=2, Dh=64, page=40)) == SHAPE
+    assert call(r=rope(rot=128)) == SHAPE and call(r=rope(rot=64, layout=7)) == INVALID
+    assert call(window=-1) == INVALID and call(sinks=-1) == INVALID
+    assert call(d=bd.make_dims(2, 64, 8, 3, 64, 128, 500, 0)) == SHAPE
