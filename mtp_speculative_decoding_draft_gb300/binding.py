@@ -492,24 +492,29 @@ def make_rope(turns, rot_dim, layout=ROPE_HALF, scale=1.0):
     return r
 
 
-def _rows(t, name, dtype=torch.bfloat16):
-    """(pointer, row stride in elements) of [n, heads, Dh] or [n, heads * Dh] rows
-    that are contiguous inside and a stride apart."""
+_BF16 = torch.bfloat16
+
+
+def _rows(t, name, Dh):
+    """(pointer, row stride in elements, rows, elements of a row) of [n, heads, Dh]
+    or [n, heads * Dh] bf16 rows that are contiguous inside and a stride apart."""
     if not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.dtype is not _BF16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
     st, sh = t.stride(), t.shape
-    if st[-1] != 1 or (len(sh) == 3 and sh[1] > 1 and st[1] != sh[2]) or len(sh) not in (2, 3):
-        raise ValueError("%s must be [rows, heads, Dh] or [rows, heads * Dh], contiguous within a row" % name)
-    return t.data_ptr(), st[0]
+    if len(st) == 3 and st[2] == 1 and sh[2] == Dh and (st[1] == Dh or sh[1] == 1):
+        return t.data_ptr(), st[0], sh[0], sh[1] * Dh
+    if len(st) == 2 and st[1] == 1:
+        return t.data_ptr(), st[0], sh[0], sh[1]
+    raise ValueError("%s must be [rows, heads, Dh] or [rows, heads * Dh], contiguous within a row" % name)
 
 
 def _row_args(cache, row_start, ctx_len):
     B = ctx_len.numel()
     if B > cache.B:
         raise ValueError("page_table has %d sequences, ctx_len %d" % (cache.B, B))
-    return B, _ptr(row_start, "row_start", torch.int32, B + 1), _ptr(ctx_len, "ctx_len", torch.int32, B)
+    return B, _ptr(row_start, "row_start", torch.int32, B + 1), _ptr(ctx_len, "ctx_len", torch.int32)
 
 
 def mtp_cache_append(cache, rope, row_start, ctx_len, q, k, v, q_out, ws, stream=None):
@@ -517,23 +522,23 @@ def mtp_cache_append(cache, rope, row_start, ctx_len, q, k, v, q_out, ws, stream
     of cache (make_paged_cache).  q, k, v, q_out: bf16 [rows, heads, Dh], rows any
     multiple of 8 elements apart; q and q_out may be None together."""
     B, rs, cl = _row_args(cache, row_start, ctx_len)
-    n, w = k.shape[0], cache.Hkv * cache.Dh
-    kp, ldk = _rows(k, "k")
-    vp, ldv = _rows(v, "v")
+    Dh = cache.Dh
+    w = cache.Hkv * Dh
+    kp, ldk, n, kw = _rows(k, "k", Dh)
+    vp, ldv, nv, vw = _rows(v, "v", Dh)
+    if nv != n or kw != w or vw != w:
+        raise ValueError("k and v must be rows of Hkv * Dh")
     qp = qo = None
-    ldq = ldqo = Hq = 0
+    ldq = ldqo = qw = 0
     if q is not None and q_out is not None:
-        qp, ldq = _rows(q, "q")
-        qo, ldqo = _rows(q_out, "q_out")
-        Hq = q.numel() // (n * cache.Dh) if n else 0
-        if q.shape[0] != n or q_out.shape[0] != n or q_out.numel() != q.numel() or Hq * cache.Dh * n != q.numel():
+        qp, ldq, nq, qw = _rows(q, "q", Dh)
+        qo, ldqo, no, ow = _rows(q_out, "q_out", Dh)
+        if nq != n or no != n or ow != qw or qw % Dh:
             raise ValueError("q and q_out must have k's rows of Hq * Dh")
     elif q is not None or q_out is not None:
         raise ValueError("q and q_out are given together")
-    if v.shape[0] != n or k.numel() != n * w or v.numel() != n * w:
-        raise ValueError("k and v must be rows of Hkv * Dh")
-    rc = _lib().mtp_cache_append(cache, rope, B, Hq, n, rs, cl, qp, ldq, kp, ldk, vp, ldv, qo, ldqo, _ptr(ws, "ws"),
-                                 ws.numel() * ws.element_size(), _stream(stream))
+    rc = _lib().mtp_cache_append(cache, rope, B, qw // Dh, n, rs, cl, qp, ldq, kp, ldk, vp, ldv, qo, ldqo,
+                                 _ptr(ws, "ws"), ws.nbytes, _stream(stream))
     if rc != 0:
         raise MtpError(rc, "mtp_cache_append")
 
@@ -546,15 +551,14 @@ def mtp_paged_attn(cache, row_start, ctx_len, q, out, lse, ws, scale=0.0, window
     """Attention of the new rows q [rows, Hq, Dh] over the pages of cache, into out
     (bf16, the same shape) and, if given, lse [rows, Hq] fp32."""
     B, rs, cl = _row_args(cache, row_start, ctx_len)
-    qp, ldq = _rows(q, "q")
-    op, ldo = _rows(out, "out")
-    n = q.shape[0]
-    Hq = q.numel() // (n * cache.Dh) if n else 0
-    if out.shape[0] != n or out.numel() != q.numel() or Hq * cache.Dh * n != q.numel():
+    Dh = cache.Dh
+    qp, ldq, n, w = _rows(q, "q", Dh)
+    op, ldo, no, ow = _rows(out, "out", Dh)
+    if no != n or ow != w or w % Dh:
         raise ValueError("q and out must have the same rows of Hq * Dh")
-    rc = _lib().mtp_paged_attn(cache, B, Hq, n, int(max_rows), rs, cl, qp, ldq, float(scale), int(window), int(sinks),
-                               op, ldo, _ptr(lse, "lse", torch.float32, n * Hq), _ptr(ws, "ws"),
-                               ws.numel() * ws.element_size(), _stream(stream))
+    Hq = w // Dh
+    rc = _lib().mtp_paged_attn(cache, B, Hq, n, max_rows, rs, cl, qp, ldq, scale, window, sinks, op, ldo,
+                               _ptr(lse, "lse", torch.float32, n * Hq), _ptr(ws, "ws"), ws.nbytes, _stream(stream))
     if rc != 0:
         raise MtpError(rc, "mtp_paged_attn")
 

@@ -9,7 +9,7 @@
 // item order, form one line that is cut into equal shares, one per CTA: every
 // CTA streams the same number of tiles whatever the lengths are.  An item that
 // crosses a cut leaves fp32 partial states (running maximum, sum, output) in
-// the workspace, and a second kernel joins them in key order.
+// the workspace, which are joined in key order.
 #pragma once
 
 #include <cuda.h>
@@ -24,9 +24,9 @@ constexpr int kTkPagedAttn = 60, kTkPagedAttnTc = 61, kTkPagedCombine = 62, kTkA
 constexpr int kStatusBadRows = 32;
 constexpr int kStatusBadPage = 64;
 
-// What a CTA leaves for the combine kernel: the item that starts in it and does
+// What a CTA of the tensor-core kernel leaves for the combine kernel: the item that starts in it and does
 // not end in it (none: rows = 0).
-struct PagedDesc {
+struct alignas(16) PagedDesc {
   int row0;      // first query row (of q) of the block
   int rows;      // packed rows of the block (tokens x G)
   int h;         // kv head
@@ -52,7 +52,7 @@ struct PagedArgs {
   // sequences whose packed rows (n * G) are in (rows_above, rows_upto] are this kernel's
   int rows_above, rows_upto;
   int tpb;                // tokens per block
-  int min_tiles;          // least tiles of a share
+  int min_tiles;          // tiles of a run when items are cut one by one; least tiles of a share otherwise
   // Behind the tensor-core kernel, which starts dependents only after its own
   // wait, the streaming kernel's inputs are ready at its start: it waits at its
   // end instead, and runs on the SMs that the other kernel's tail leaves.
@@ -116,45 +116,74 @@ __device__ __forceinline__ PagedRange paged_range(const PagedArgs &p, const Page
 
 __device__ __forceinline__ int paged_blocks(const PagedArgs &p, int n) { return (n + p.tpb - 1) / p.tpb; }
 
-// Tiles of one kv head of a sequence (0 for a sequence of the other kernel).
+__device__ __forceinline__ int paged_units(const PagedArgs &p, int count) { return (count + p.min_tiles - 1) / p.min_tiles; }
+
+// Tiles of one kv head of a sequence (0 for a sequence of the other kernel), and
+// the CTAs they take when every item is cut by itself into runs of min_tiles.
 template <int TK>
-__device__ __forceinline__ long long paged_cost(const PagedArgs &p, const PagedSeq &s) {
+__device__ __forceinline__ long long paged_cost(const PagedArgs &p, const PagedSeq &s, long long *units) {
   const long long pr = (long long)s.n * p.G;
+  *units = 0;
   if (s.n <= 0 || pr <= p.rows_above || pr > p.rows_upto) return 0;
   long long c = 0;
-  for (int t0 = 0; t0 < s.n; t0 += p.tpb) c += paged_range<TK>(p, s, t0, min(s.n, t0 + p.tpb)).count;
+  for (int t0 = 0; t0 < s.n; t0 += p.tpb) {
+    const int n = paged_range<TK>(p, s, t0, min(s.n, t0 + p.tpb)).count;
+    c += n;
+    *units += paged_units(p, n);
+  }
   return c;
 }
 
-// This CTA's share of the line of tiles, and where on it the walk starts.
+// This CTA's share: tiles [start, end) of the line, found in sequence b behind
+// `off` of its tiles.  When the items cut one by one into runs of min_tiles fit
+// the CTAs (cut set), a share is one such run, number `off` of sequence b: a
+// small batch is not divided evenly for its own sake, and no CTA has the tail of
+// one item and the head of the next.
 struct PagedShare {
-  long long start, end, per;  // tiles [start, end) of the line, shares of `per`
-  int b;                      // sequence of tile `start`
-  long long off;              // tiles of the line before `start` inside sequence b
+  long long start, end, per, off;
+  int b;
+  bool cut;
 };
 
-// Executed by all NT threads of the CTA; scratch: NT / 32 + 2 long longs of shared memory.
+// Executed by all NT threads of the CTA; scratch: 2 NT / 32 + 2 long longs of shared memory.
 template <int TK, int NT>
 __device__ PagedShare paged_plan(const PagedArgs &p, long long *scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int NW = NT / 32;
-  long long *found = scratch + NW;
-  long long first = 0, mine = 0;
+  long long *found = scratch + 2 * NW;
+  long long first = 0, first_u = 0, mine = 0, mine_u = 0;
   for (int b = tid; b < p.B; b += NT) {
-    const long long c = paged_cost<TK>(p, paged_seq(p, b, blockIdx.x == 0)) * p.Hkv;
-    if (b < NT) first = c;
+    long long u;
+    const long long c = paged_cost<TK>(p, paged_seq(p, b, blockIdx.x == 0), &u) * p.Hkv;
+    u *= p.Hkv;
+    if (b < NT) {
+      first = c;
+      first_u = u;
+    }
     mine += c;
+    mine_u += u;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) scratch[warp] = mine;
+  for (int o = 16; o > 0; o >>= 1) {
+    mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    mine_u += __shfl_xor_sync(0xffffffffu, mine_u, o);
+  }
+  if (lane == 0) {
+    scratch[warp] = mine;
+    scratch[NW + warp] = mine_u;
+  }
   __syncthreads();
-  long long total = 0;
+  long long total = 0, units = 0;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) total += scratch[w];
+  for (int w = 0; w < NW; ++w) {
+    total += scratch[w];
+    units += scratch[NW + w];
+  }
   PagedShare sh;
   const long long nc = gridDim.x;
-  sh.per = max((long long)p.min_tiles, (total + nc - 1) / nc);
+  sh.cut = units <= nc;
+  if (sh.cut) total = units;
+  sh.per = sh.cut ? 1 : (total + nc - 1) / nc;
   sh.start = min(total, sh.per * (long long)blockIdx.x);
   sh.end = min(total, sh.start + sh.per);
   sh.b = 0;
@@ -163,7 +192,12 @@ __device__ PagedShare paged_plan(const PagedArgs &p, long long *scratch) {
   long long acc = 0;
   for (int base = 0; base < p.B; base += NT) {
     const int b = base + tid;
-    long long c = base == 0 ? first : (b < p.B ? paged_cost<TK>(p, paged_seq(p, b, false)) * p.Hkv : 0);
+    long long c = sh.cut ? first_u : first;
+    if (base > 0) {
+      long long u = 0;
+      c = b < p.B ? paged_cost<TK>(p, paged_seq(p, b, false), &u) : 0;
+      c = (sh.cut ? u : c) * p.Hkv;
+    }
     long long inc = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -198,27 +232,41 @@ __device__ PagedShare paged_plan(const PagedArgs &p, long long *scratch) {
 template <int TK>
 struct PagedWalk {
   const PagedArgs &p;
-  long long pos, end;
+  long long pos, end, per;
   int b, h, t0;
   PagedSeq s;
   PagedRange r;
   int i0, i1;
+  int first, last;  // the CTAs in which the item starts and ends
 
   __device__ __forceinline__ PagedWalk(const PagedArgs &pa, const PagedShare &sh)
-      : p(pa), pos(sh.start), end(sh.end), b(sh.b), h(0), t0(0), i0(0), i1(0) {
+      : p(pa), pos(sh.start), end(sh.end), per(sh.per), b(sh.b), h(0), t0(0), i0(0), i1(0), first(0), last(0) {
     if (pos >= end) return;
     s = paged_seq(p, b, false);
-    const long long c = paged_cost<TK>(p, s);
+    long long u;
+    long long c = paged_cost<TK>(p, s, &u);
+    if (sh.cut) c = u;
     h = (int)(sh.off / c);
     long long rem = sh.off % c;
     for (;;) {
       r = paged_range<TK>(p, s, t0, t1());
-      if (rem < r.count) break;
-      rem -= r.count;
+      const int n = sh.cut ? paged_units(p, r.count) : r.count;
+      if (rem < n) break;
+      rem -= n;
       t0 += p.tpb;
     }
-    i0 = (int)rem;
-    cut();
+    if (sh.cut) {
+      const int n = paged_units(p, r.count);  // the item's runs, alike to a tile
+      i0 = (int)((long long)rem * r.count / n);
+      i1 = (int)((long long)(rem + 1) * r.count / n);
+      first = (int)blockIdx.x - (int)rem;
+      last = first + n - 1;
+      pos = 0;
+      end = i1 - i0;
+    } else {
+      i0 = (int)rem;
+      cut();
+    }
   }
   __device__ __forceinline__ int t1() const { return min(s.n, t0 + p.tpb); }
   __device__ __forceinline__ bool valid() const { return pos < end; }
@@ -227,6 +275,8 @@ struct PagedWalk {
   __device__ __forceinline__ void cut() {
     const long long left = end - pos;
     i1 = (long long)(r.count - i0) <= left ? r.count : i0 + (int)left;
+    first = (int)((pos - i0) / per);
+    last = (int)((pos - i0 + r.count - 1) / per);
   }
   __device__ __forceinline__ void next() {
     pos += i1 - i0;
@@ -237,9 +287,10 @@ struct PagedWalk {
       t0 = 0;
       if (++h == p.Hkv) {
         h = 0;
+        long long u;
         do {
           s = paged_seq(p, ++b, false);
-        } while (b + 1 < p.B && paged_cost<TK>(p, s) == 0);
+        } while (b + 1 < p.B && paged_cost<TK>(p, s, &u) == 0);
       }
     }
     r = paged_range<TK>(p, s, t0, t1());

@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_tc_plan_kernel(const __gri
     int nb = 0;
     if (b < p.B) {
       const PagedSeq s = paged_seq(p, b, true);
-      c = paged_cost<kTK>(p, s);
+      long long u;
+      c = paged_cost<kTK>(p, s, &u);
       nb = c > 0 ? paged_blocks(p, s.n) : 0;
     }
     const long long sum = block_scan(nb, &incl, scratch);

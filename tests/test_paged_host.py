@@ -102,7 +102,7 @@ def test_binding_refusals():
     import torch
     x = torch.zeros(4, 8, 64, dtype=torch.bfloat16)
     with pytest.raises(TypeError):
-        bd._rows(x, "q")                                                     # not a CUDA tensor
+        bd._rows(x, "q", 64)                                                     # not a CUDA tensor
     with pytest.raises(ValueError):
         bd.make_paged_cache(x, x, x)
     with pytest.raises(TypeError):
