@@ -142,6 +142,43 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+// The n lowest bits.
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// N lanes that hold N quads of a row each exchange them: lane j of the N leaves
+// with quad j of every row, so that N lanes store one row's quads side by side.
+// (A lane a row, the stores touched 32 lines an instruction and an epilogue took
+// 6000 cycles.)
+template <int N>
+__device__ __forceinline__ void transpose_quads(uint4 (&q)[N], int lane) {
+#pragma unroll
+  for (int s = 1; s < N; s <<= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i & s) continue;
+      uint4 v = up ? q[i] : q[i | s];
+      v.x = __shfl_xor_sync(kFull, v.x, s);
+      v.y = __shfl_xor_sync(kFull, v.y, s);
+      v.z = __shfl_xor_sync(kFull, v.z, s);
+      v.w = __shfl_xor_sync(kFull, v.w, s);
+      if (up) q[i] = v;
+      else q[i | s] = v;
+    }
+  }
+}
+
+// Stores N quads of each lane's row at the lane's address (null: none).
+template <int N>
+__device__ __forceinline__ void store_quads(uint4 (&q)[N], void *at, int lane) {
+  transpose_quads<N>(q, lane);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const unsigned long long a = __shfl_sync(kFull, reinterpret_cast<unsigned long long>(at), (lane & ~(N - 1)) + i);
+    if (a) reinterpret_cast<uint4 *>(a)[lane & (N - 1)] = q[i];
+  }
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
@@ -562,9 +599,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         for (int c = 0; c < 4; ++c) pin32(s + 32 * c);
         if (!whole) {
 #pragma unroll
-          for (int e = 0; e < 128; ++e) {
-            const int j = k0 + e;
-            if (!(j < rhi && (j >= rlo || j < p.sinks))) s[e] = 0xff800000u;
+          for (int c = 0; c < 4; ++c) {
+            const int b = k0 + 32 * c;  // the row's view of 32 keys as bits
+            const uint32_t see = below(rhi - b) & (~below(rlo - b) | below(p.sinks - b));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(see >> e & 1u)) s[32 * c + e] = 0xff800000u;
           }
         }
         float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -628,27 +668,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         tmem_ld32_async(to + 32 * c, o);
         tmem_wait_ld();
         pin32(o);
-        if (!mine) continue;
         // O of a row without keys was multiplied by zero weights only: still zero
         if (!whole_item || p.out_f32) {
           float *d = whole_item ? static_cast<float *>(p.out) + (long long)qrow * p.ldo + hq * DH + 32 * c
                                 : p.part_o + pr * DH + 32 * c;
           const float f = whole_item ? inv : 1.f;
+          uint4 v[8];
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4 *>(d + e) =
-                make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f, __uint_as_float(o[e + 2]) * f,
-                            __uint_as_float(o[e + 3]) * f);
+          for (int e = 0; e < 8; ++e)
+            v[e] = make_uint4(__float_as_uint(__uint_as_float(o[4 * e]) * f), __float_as_uint(__uint_as_float(o[4 * e + 1]) * f),
+                              __float_as_uint(__uint_as_float(o[4 * e + 2]) * f), __float_as_uint(__uint_as_float(o[4 * e + 3]) * f));
+          store_quads<8>(v, mine ? d : nullptr, lane);
         } else {
           uint16_t *d = static_cast<uint16_t *>(p.out) + (long long)qrow * p.ldo + hq * DH + 32 * c;
+          uint4 v[4];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t v[4];
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              v[j] = pack2(__uint_as_float(o[e + 2 * j]) * inv, __uint_as_float(o[e + 2 * j + 1]) * inv);
-            *reinterpret_cast<uint4 *>(d + e) = make_uint4(v[0], v[1], v[2], v[3]);
+              w[j] = pack2(__uint_as_float(o[8 * e + 2 * j]) * inv, __uint_as_float(o[8 * e + 2 * j + 1]) * inv);
+            v[e] = make_uint4(w[0], w[1], w[2], w[3]);
           }
+          store_quads<4>(v, mine ? d : nullptr, lane);
         }
       }
       if (mine) {
