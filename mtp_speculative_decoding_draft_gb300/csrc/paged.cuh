@@ -49,14 +49,8 @@ struct PagedArgs {
   float scale_log2;       // softmax scale * log2(e)
   int window, sinks;      // window 0: every earlier key
   int *status;
-  // sequences whose packed rows (n * G) are in (rows_above, rows_upto] are this kernel's
-  int rows_above, rows_upto;
   int tpb;                // tokens per block
   int min_tiles;          // tiles of a run when items are cut one by one; least tiles of a share otherwise
-  // Behind the tensor-core kernel, which starts dependents only after its own
-  // wait, the streaming kernel's inputs are ready at its start: it waits at its
-  // end instead, and runs on the SMs that the other kernel's tail leaves.
-  int late_wait;
   PagedDesc *desc;        // [CTAs]
   float *part_o;          // [CTAs][2][block rows][Dh]
   float *part_ml;         // [CTAs][2][block rows][2]
@@ -118,13 +112,10 @@ __device__ __forceinline__ int paged_blocks(const PagedArgs &p, int n) { return 
 
 __device__ __forceinline__ int paged_units(const PagedArgs &p, int count) { return (count + p.min_tiles - 1) / p.min_tiles; }
 
-// Tiles of one kv head of a sequence (0 for a sequence of the other kernel), and
-// the CTAs they take when every item is cut by itself into runs of min_tiles.
+// Tiles of one kv head of a sequence, and the CTAs they take when every item is cut by itself into runs of min_tiles.
 template <int TK>
 __device__ __forceinline__ long long paged_cost(const PagedArgs &p, const PagedSeq &s, long long *units) {
-  const long long pr = (long long)s.n * p.G;
   *units = 0;
-  if (s.n <= 0 || pr <= p.rows_above || pr > p.rows_upto) return 0;
   long long c = 0;
   for (int t0 = 0; t0 < s.n; t0 += p.tpb) {
     const int n = paged_range<TK>(p, s, t0, min(s.n, t0 + p.tpb)).count;

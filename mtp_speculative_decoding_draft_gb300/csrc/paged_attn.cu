@@ -113,14 +113,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
     fence_barrier_init();
   }
-  if (!p.late_wait) grid_dep_wait();
+  grid_dep_wait();
   trace_dep(kTkPagedAttn);
   grid_dep_launch();
   const PagedShare sh = paged_plan<kTK, kThreads>(p, scratch);  // its barriers publish the mbarriers
   trace_mark(kTkPagedAttn, 0);  // share known
   if (tid == 0) p.desc[blockIdx.x].rows = 0;
   if (sh.start >= sh.end) {
-    grid_dep_wait();
     trace_end(kTkPagedAttn);
     return;
   }
@@ -169,7 +168,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     if (!ok)  // let copies still in flight land before the CTA exits
       for (int i = max(0, issued - kStages); i < issued; ++i)
         if (!mbar_wait(&full[i % kStages], (uint32_t)(i / kStages) & 1u, p.status)) break;
-    grid_dep_wait();
     trace_end(kTkPagedAttn);
     return;
   }
@@ -407,18 +405,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     }
     named_sync(1, 32 * kCW);  // the buffer is the next block's queries
   }
-  grid_dep_wait();
   trace_end(kTkPagedAttn);
 }
 
 // Joins the segments of the items that end in a later CTA than they start in, in
-// key order, a warp a row: the blocks go over the rows of the items that start in
-// each CTA of the tensor-core kernel, then of the streaming kernel.
-struct CombineParams {
-  PagedArgs tc, st;
-  int tc_blocks, st_rows;  // blocks of the tensor-core items, rows of a streaming block
-};
-constexpr int kCombineRows = 8;  // rows of a block: a warp each
+// key order: eight rows of the item that starts in a CTA a block, a warp a row.
+constexpr int kCombineRows = 8;
 
 template <int PER>
 struct Vec;
@@ -436,18 +428,15 @@ struct Vec<4> {
 };
 
 template <int DH>
-__global__ void __launch_bounds__(32 * kCombineRows) paged_combine_kernel(const __grid_constant__ CombineParams cp) {
+__global__ void __launch_bounds__(32 * kCombineRows) paged_combine_kernel(const __grid_constant__ PagedArgs p, int block_rows) {
   trace_start(kTkPagedCombine);
   grid_dep_wait();
   grid_dep_launch();
-  const bool tc = (int)blockIdx.x < cp.tc_blocks;
-  const PagedArgs &p = tc ? cp.tc : cp.st;
-  const int block_rows = tc ? kPagedTcRows : cp.st_rows, per = block_rows / kCombineRows;
-  const int blk = (int)blockIdx.x - (tc ? 0 : cp.tc_blocks), cta = blk / per;
+  const int per = block_rows / kCombineRows, cta = blockIdx.x / per;
   constexpr int PER = DH / 32;
   const int lane = threadIdx.x & 31;
   const PagedDesc d = p.desc[cta];
-  const int r = (blk % per) * kCombineRows + (threadIdx.x >> 5);
+  const int r = (blockIdx.x % per) * kCombineRows + (threadIdx.x >> 5);
   if (r < d.rows) {
     const int nseg = d.last_cta - cta + 1;
     auto seg = [&](int i) { return ((size_t)(cta + i) * 2 + (i == 0 ? 1 : 0)) * block_rows + r; };
@@ -554,6 +543,14 @@ cudaError_t launch_rows(const StreamParams &sp, int rb, int ctas, cudaStream_t s
   return launch_stream<DH, 4>(sp, ctas, s, pdl);
 }
 
+template <int DH>
+cudaError_t launch_combine(const PagedArgs &a, int ctas, int rows, cudaStream_t s, bool pdl) {
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config(dim3(ctas * (rows / kCombineRows)), 32 * kCombineRows, 0, s, attr, pdl);
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<DH>, a, rows);
+}
+
 template <int DH, int RG>
 cudaError_t set_smem() {
   return cudaFuncSetAttribute(paged_attn_kernel<DH, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -583,55 +580,45 @@ static long long packed_rows(int n_rows, int max_rows, int G) {
   return (long long)(max_rows > 0 && max_rows < n_rows ? max_rows : n_rows) * G;
 }
 
-// Sequences of more packed rows than a streaming block holds go to the tensor
-// cores (heads of 32 stay: their products are too thin for it).
+// A call with a sequence of more packed rows than a streaming block holds goes to
+// the tensor cores whole: there a few rows cost a tile about what its bytes cost
+// (2300 cycles of one query group against 2800 of DRAM time for 128 keys of 128),
+// and one kernel takes any mixture.  Heads of 32 stay: their products are too thin.
 static bool wants_tc(long long packed, int Dh) { return packed > kStreamRows && Dh != 32; }
 
 size_t paged_attn_scratch_bytes(int B, int Hkv, int n_rows, int max_rows, int G, int Dh) {
-  const size_t stream = region_bytes(2 * kMaxSms, kStreamRows, Dh);
-  if (!wants_tc(packed_rows(n_rows, max_rows, G), Dh)) return stream;
-  return stream + region_bytes(kMaxSms, kPagedTcRows, Dh) + paged_tc_plan_bytes(B, n_rows, G, Hkv);
+  if (!wants_tc(packed_rows(n_rows, max_rows, G), Dh)) return region_bytes(2 * kMaxSms, kStreamRows, Dh);
+  return region_bytes(kMaxSms, kPagedTcRows, Dh) + paged_tc_plan_bytes(B, n_rows, G, Hkv);
 }
 
 cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const void *v_pages, int max_rows, void *scratch,
                               int sms, cudaStream_t s, bool pdl) {
   const long long packed = packed_rows(args.n_rows, max_rows, args.G);
-  const bool tc = wants_tc(packed, args.Dh);
   const uint64_t rows = (uint64_t)args.n_pages * args.Hkv * args.page;
   const int n = sms < kMaxSms ? sms : kMaxSms;
   char *base = static_cast<char *>(scratch);
-  CombineParams cp;
-  cp.tc_blocks = 0;
-  cp.tc = args;
   cudaError_t e;
-  if (tc) {
+  if (wants_tc(packed, args.Dh)) {
     PagedTcParams tp;
     tp.a = args;
-    tp.a.rows_above = kStreamRows;
-    tp.a.rows_upto = 0x7fffffff;
     tp.a.tpb = 2 * (128 / args.G);
     tp.a.min_tiles = 2;
-    tp.a.late_wait = 0;
-    char *at = base + region_bytes(2 * kMaxSms, kStreamRows, args.Dh);
-    bind_region(tp.a, at, n, kPagedTcRows);
-    paged_tc_bind_plan(tp, at + region_bytes(kMaxSms, kPagedTcRows, args.Dh));
+    bind_region(tp.a, base, n, kPagedTcRows);
+    paged_tc_bind_plan(tp, base + region_bytes(kMaxSms, kPagedTcRows, args.Dh));
     if (!make_page_map(&tp.mk, k_pages, args.Dh, rows, args.page) ||
         !make_page_map(&tp.mv, v_pages, args.Dh, rows, args.page) ||
         !make_query_map(&tp.mq, args.q, args.Dh, args.Hq, args.n_rows, args.ldq, args.G, 128 / args.G))
       return cudaErrorNotSupported;
     if ((e = launch_paged_attn_tc(tp, n, s, pdl))) return e;
-    cp.tc = tp.a;
-    cp.tc_blocks = n * (kPagedTcRows / kCombineRows);
+    return args.Dh == 64 ? launch_combine<64>(tp.a, n, kPagedTcRows, s, pdl)
+                         : launch_combine<128>(tp.a, n, kPagedTcRows, s, pdl);
   }
   StreamParams sp;
   sp.a = args;
   const int rb = packed <= 16 ? 16 : packed <= 32 ? 32 : 64, ctas = 2 * n;
-  sp.a.rows_above = 0;
-  sp.a.rows_upto = tc ? kStreamRows : 0x7fffffff;
   sp.a.tpb = rb / args.G;
   // at 4096 keys of 8 heads: runs of 2 tiles 15.1 us a call, of 4 14.1, of 6 14.4
   sp.a.min_tiles = 4;
-  sp.a.late_wait = tc && pdl;
   bind_region(sp.a, base, ctas, rb);
   const uint32_t box = (uint32_t)(args.page < kTK ? args.page : kTK);
   if (!make_page_map(&sp.mk, k_pages, args.Dh, rows, box) || !make_page_map(&sp.mv, v_pages, args.Dh, rows, box))
@@ -640,14 +627,9 @@ cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const 
   else if (args.Dh == 64) e = launch_rows<64>(sp, rb, ctas, s, pdl);
   else e = launch_rows<128>(sp, rb, ctas, s, pdl);
   if (e) return e;
-  cp.st = sp.a;
-  cp.st_rows = rb;
-  cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = config(dim3(cp.tc_blocks + ctas * (rb / kCombineRows)), 32 * kCombineRows, 0, s, attr, pdl);
-  note_launch();
-  if (args.Dh == 32) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<32>, cp);
-  if (args.Dh == 64) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<64>, cp);
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<128>, cp);
+  if (args.Dh == 32) return launch_combine<32>(sp.a, ctas, rb, s, pdl);
+  if (args.Dh == 64) return launch_combine<64>(sp.a, ctas, rb, s, pdl);
+  return launch_combine<128>(sp.a, ctas, rb, s, pdl);
 }
 
 MTP_TRACE_COLLECTOR(paged_attn)

@@ -1,6 +1,6 @@
 // Attention of a chunk of new tokens over a paged K/V cache: the tensor-core
-// kernel, for sequences with more packed rows (tokens x G) than the streaming
-// kernel's block.
+// kernel, for calls with a sequence of more packed rows (tokens x G) than the
+// streaming kernel's block.
 //
 // Bound by the two matrix products and by the exponentials between them.  A CTA
 // holds a block of two groups of 128 packed query rows of one K/V head; the
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
           m = n;
           l *= f;
           if (i > w.i0) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DH / 32; ++c) {
               uint32_t o[32];
               tmem_ld32_async(to + 32 * c, o);
@@ -662,7 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       const bool mine = live && in_bounds(qrow < p.n_rows, p.status);
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const size_t pr = ((size_t)blockIdx.x * 2 + slot) * kPagedTcRows + g * rpg + row;
-#pragma unroll
+      // not unrolled: run once a segment, the code comes from memory each time
+#pragma unroll 1
       for (int c = 0; c < DH / 32; ++c) {
         uint32_t o[32];
         tmem_ld32_async(to + 32 * c, o);
