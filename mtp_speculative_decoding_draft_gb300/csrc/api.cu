@@ -1064,6 +1064,7 @@ int mtp_cache_append(const MtpPagedCache *cache, const MtpRope *rope, int B, int
 size_t mtp_paged_attn_workspace_size(int B, int n_rows, int max_rows, int Hq, int Hkv, int Dh) {
   if (B < 1 || n_rows < 1 || max_rows < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv || Hq / Hkv > kMaxGroup) return 0;
   if (Dh != 32 && Dh != 64 && Dh != 128) return 0;
+  if (!paged_attn_items_ok(B, Hkv, n_rows, Hq / Hkv)) return 0;
   return kAlign + paged_attn_scratch_bytes(B, Hkv, n_rows, max_rows, Hq / Hkv, Dh);
 }
 
@@ -1075,6 +1076,7 @@ int mtp_paged_attn(const MtpPagedCache *cache, int B, int Hq, int n_rows, int ma
   if (rc) return rc;
   const long long qw = (long long)Hq * cache->Dh;
   if (max_rows < 0 || window < 0 || sinks < 0) return MTP_ERR_INVALID_ARG;
+  if (!paged_attn_items_ok(B, cache->Hkv, n_rows, Hq / cache->Hkv)) return MTP_ERR_UNSUPPORTED_SHAPE;
   if (!(scale >= 0.f && scale < 1e30f)) return MTP_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !row_stride_ok(ldq, qw) || !row_stride_ok(ldo, qw)) return MTP_ERR_INVALID_ARG;
   if (lse && !aligned16(lse)) return MTP_ERR_INVALID_ARG;

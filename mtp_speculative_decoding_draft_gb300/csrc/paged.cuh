@@ -305,6 +305,7 @@ __device__ __forceinline__ int paged_page(const PagedArgs &p, int b, int j) {
 // A 2-D map over a pool of K or V pages as [rows, Dh] bf16, boxes of box_rows
 // rows by at most 64 elements (tc.cu); false if the driver cannot encode it.
 bool make_page_map(CUtensorMap *m, const void *base, int Dh, uint64_t rows, uint32_t box_rows);
+bool paged_attn_items_ok(int B, int Hkv, int n_rows, int G);
 size_t paged_attn_scratch_bytes(int B, int Hkv, int n_rows, int max_rows, int G, int Dh);
 cudaError_t paged_set_attributes();
 cudaError_t launch_paged_attn(const PagedArgs &a, const void *k_pages, const void *v_pages, int max_rows, void *scratch,

@@ -206,10 +206,10 @@ __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *m, int x, i
       : "memory");
 }
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
 
-// Inclusive scan over the block's threads; returns the block's sum too.
-__device__ long long block_scan(long long v, long long *incl, long long *scratch) {
+// Inclusive scan over the block's threads; returns the block's sum.
+__device__ __forceinline__ long long block_scan(long long v, long long *incl, long long *scratch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -219,15 +219,15 @@ __device__ long long block_scan(long long v, long long *incl, long long *scratch
   __syncthreads();  // scratch is free again
   if (lane == 31) scratch[warp] = v;
   __syncthreads();
-  long long before = 0, sum = 0;
+  long long w = lane < kPlanThreads / 32 ? scratch[lane] : 0;  // every warp scans the warps' sums
 #pragma unroll
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    const long long u = scratch[w];
-    before += w < warp ? u : 0;
-    sum += u;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(kFull, w, o);
+    if (lane >= o) w += u;
   }
-  *incl = before + v;
-  return sum;
+  const long long before = __shfl_sync(kFull, w, (warp + 31) & 31);
+  *incl = v + (warp > 0 ? before : 0);
+  return __shfl_sync(kFull, w, 31);
 }
 
 // Walks a share's items in the plan's order, one segment at a time; the interface
@@ -243,23 +243,27 @@ struct PlanWalk {
   int i0, i1;
 
   __device__ __forceinline__ explicit PlanWalk(const PagedTcParams &x) : sp(x), p(x.a), i0(0), i1(0) {
-    const long long total = __ldcg(&sp.plan->total);
-    per = __ldcg(&sp.plan->per);
-    pos = min(total, per * (long long)blockIdx.x);
-    end = min(total, pos + per);
+    const PagedStart *st = &sp.start[blockIdx.x];
+    const longlong2 e = __ldcg(reinterpret_cast<const longlong2 *>(&st->end));
+    i = __ldcg(&st->i);
+    const long long before = load(&st->item);
+    end = e.x;
+    per = e.y;
+    pos = per * (long long)blockIdx.x;
     if (pos >= end) return;
-    i = __ldcg(&sp.start[blockIdx.x]);
-    i0 = (int)(pos - load());
+    i0 = (int)(pos - before);
     cut();
   }
-  __device__ __forceinline__ long long load() {
-    const int4 x = __ldcg(reinterpret_cast<const int4 *>(&sp.items[i]));
+  __device__ __forceinline__ long long load(const PagedItem *it) {
+    const int4 x = __ldcg(reinterpret_cast<const int4 *>(&it->b)), y = __ldcg(reinterpret_cast<const int4 *>(&it->row0));
     b = x.x;
     h = x.y;
     t0 = x.z;
-    s = paged_seq(p, b, false);
+    s.row0 = y.x;
+    s.n = y.y;
+    s.ctx = y.z;
     r = paged_range<TK>(p, s, t0, t1());
-    return __ldcg(&sp.items[i].first);
+    return __ldcg(&it->first);
   }
   __device__ __forceinline__ int t1() const { return min(s.n, t0 + p.tpb); }
   __device__ __forceinline__ bool valid() const { return pos < end; }
@@ -274,7 +278,7 @@ struct PlanWalk {
     if (pos >= end) return;
     do ++i;
     while (__ldcg(&sp.items[i].count) == 0);  // pos < end: an item follows
-    load();
+    load(&sp.items[i]);
     i0 = 0;
     cut();
   }
@@ -285,9 +289,12 @@ struct PlanWalk {
 // One CTA: the items of the batch, their order, and where each share starts.
 __global__ void __launch_bounds__(kPlanThreads) paged_tc_plan_kernel(const __grid_constant__ PagedTcParams sp, int ctas) {
   trace_start(kTkPagedPlan);
+  constexpr int kNear = 1024;  // sequences whose blocks are kept in shared memory
   __shared__ long long scratch[kPlanThreads / 32];
+  __shared__ int near_blocks[kNear + 1];
   const PagedArgs &p = sp.a;
   const int tid = threadIdx.x;
+  const bool near = p.B <= kNear;
   grid_dep_wait();
   trace_dep(kTkPagedPlan);
   grid_dep_launch();
@@ -295,57 +302,75 @@ __global__ void __launch_bounds__(kPlanThreads) paged_tc_plan_kernel(const __gri
   long long nblk = 0, total = 0, incl;
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    long long c = 0;
+    long long c = 0, u;
     int nb = 0;
     if (b < p.B) {
       const PagedSeq s = paged_seq(p, b, true);
-      long long u;
       c = paged_cost<kTK>(p, s, &u);
-      nb = c > 0 ? paged_blocks(p, s.n) : 0;
+      nb = paged_blocks(p, s.n);
     }
     const long long sum = block_scan(nb, &incl, scratch);
-    if (b < p.B) sp.blocks[b] = (int)(nblk + incl - nb);
+    if (b < p.B) {
+      const int before = (int)(nblk + incl - nb);
+      if (near) near_blocks[b] = before;
+      else sp.blocks[b] = before;
+    }
     nblk += sum;
     total += block_scan(c * p.Hkv, &incl, scratch);
   }
-  if (tid == 0) sp.blocks[p.B] = (int)nblk;
-  const long long N = nblk * p.Hkv, q = (N + ctas - 1) / ctas;
-  const long long per = max((long long)p.min_tiles, (total + ctas - 1) / ctas);
   if (tid == 0) {
-    sp.plan->total = total;
-    sp.plan->per = per;
-    sp.plan->n_items = (int)(q * ctas);
+    if (near) near_blocks[p.B] = (int)nblk;
+    else sp.blocks[p.B] = (int)nblk;
   }
+  // items fit 31 bits (the host checks), so that places and sequences divide in 32
+  const unsigned N = (unsigned)(nblk * p.Hkv), q = (N + ctas - 1) / ctas, places = q * ctas;
+  const long long per = max((long long)p.min_tiles, (total + ctas - 1) / ctas);
+  // shares without tiles
+  for (int c = tid; c < ctas; c += kPlanThreads)
+    if (c * per >= total) {
+      sp.start[c].end = 0;
+      sp.start[c].per = per;
+    }
   __syncthreads();  // the blocks are read below
+  auto first_item = [&](int b) { return (unsigned)(near ? near_blocks[b] : __ldcg(&sp.blocks[b])) * p.Hkv; };
   // ---- items, dealt out: place i = c * q + t holds item t * CTAs + c
   long long before = 0;
-  for (long long base = 0; base < q * ctas; base += kPlanThreads) {
-    const long long i = base + tid, m = i < q * ctas ? (i % q) * ctas + i / q : N;
-    PagedItem it;
-    it.b = it.h = it.t0 = it.count = 0;
+  for (unsigned base = 0; base < places; base += kPlanThreads) {
+    const unsigned i = base + tid, m = i < places ? (i % q) * ctas + i / q : N;
+    PagedItem it{};
     if (m < N) {
       // the sequence: the last whose first item is not past m
-      int lo = 0, hi = p.B;  // blocks[lo] * Hkv <= m < blocks[hi] * Hkv
+      int lo = 0, hi = p.B;  // first_item(lo) <= m < first_item(hi)
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if ((long long)__ldcg(&sp.blocks[mid]) * p.Hkv <= m) lo = mid;
+        if (first_item(mid) <= m) lo = mid;
         else hi = mid;
       }
       const PagedSeq s = paged_seq(p, lo, false);
-      const int nb = paged_blocks(p, s.n), off = (int)(m - (long long)__ldcg(&sp.blocks[lo]) * p.Hkv);
+      const int nb = paged_blocks(p, s.n), off = (int)(m - first_item(lo));
       it.b = lo;
       it.h = off / nb;
       it.t0 = (off % nb) * p.tpb;
       it.count = paged_range<kTK>(p, s, it.t0, min(s.n, it.t0 + p.tpb)).count;
+      it.row0 = s.row0;
+      it.n = s.n;
+      it.ctx = s.ctx;
     }
     const long long sum = block_scan(it.count, &incl, scratch);
     it.first = before + incl - it.count;
     before += sum;
-    if (i < q * ctas) {
+    if (i < places) {
       sp.items[i] = it;
       // the shares that start inside this item
-      for (long long c = (it.first + per - 1) / per; it.count > 0 && c * per < it.first + it.count; ++c)
-        if (c < ctas) sp.start[c] = (int)i;
+      if (it.count > 0)
+        for (long long c = (it.first + per - 1) / per; c * per < it.first + it.count && c < ctas; ++c) {
+          PagedStart st{};
+          st.item = it;
+          st.end = min(total, (c + 1) * per);
+          st.per = per;
+          st.i = (int)i;
+          sp.start[c] = st;
+        }
     }
   }
   trace_end(kTkPagedPlan);
@@ -738,18 +763,18 @@ static size_t plan_items(int B, int n_rows, int G, int Hkv) {
   return ((size_t)n_rows / (2 * (128 / G)) + B) * Hkv + kPagedMaxCtas;
 }
 
+bool paged_tc_items_ok(int B, int n_rows, int G, int Hkv) { return plan_items(B, n_rows, G, Hkv) < (1ull << 31) - (1 << 20); }
+
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t paged_tc_plan_bytes(int B, int n_rows, int G, int Hkv) {
-  return 256 + up256((size_t)kPagedMaxCtas * 4) + up256(((size_t)B + 1) * 4) +
+  return up256((size_t)kPagedMaxCtas * sizeof(PagedStart)) + up256(((size_t)B + 1) * 4) +
          up256(plan_items(B, n_rows, G, Hkv) * sizeof(PagedItem));
 }
 
 void paged_tc_bind_plan(PagedTcParams &sp, char *base) {
-  sp.plan = reinterpret_cast<PagedPlan *>(base);
-  base += 256;
-  sp.start = reinterpret_cast<int *>(base);
-  base += up256((size_t)kPagedMaxCtas * 4);
+  sp.start = reinterpret_cast<PagedStart *>(base);
+  base += up256((size_t)kPagedMaxCtas * sizeof(PagedStart));
   sp.blocks = reinterpret_cast<int *>(base);
   base += up256(((size_t)sp.a.B + 1) * 4);
   sp.items = reinterpret_cast<PagedItem *>(base);
