@@ -414,7 +414,7 @@ int spec_verify_fused(int B, int k, int V, int d, float T, int mode,
  *              that a row sees (or is written to) are read: the others, of
  *              pages not yet given or, under a window, already given back, may
  *              hold anything.  Sequences may share pages that none appends to.
- * n_pages * Hkv * page < 2^31 and max_pages * page <= 2^30.
+ * n_pages * Hkv * page < 2^31, max_pages * page <= 2^30, n_rows <= 2^29.
  */
 typedef struct {
     int32_t Hkv, Dh, page, n_pages, max_pages;

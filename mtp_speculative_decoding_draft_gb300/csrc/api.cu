@@ -973,7 +973,8 @@ namespace {
 
 int check_rows(const MtpPagedCache *c, int B, int Hq, int n_rows, const int32_t *row_start, const int32_t *ctx_len) {
   if (B < 1 || n_rows < 1 || Hq < 1) return MTP_ERR_INVALID_ARG;
-  if (B > (1 << 20) || n_rows > (1 << 30)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  // positions (a context and the rows behind it) stay below 2^31
+  if (B > (1 << 20) || n_rows > (1 << 29)) return MTP_ERR_UNSUPPORTED_SHAPE;
   if (Hq % c->Hkv || Hq / c->Hkv > kMaxGroup) return MTP_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(row_start) || !aligned16(ctx_len)) return MTP_ERR_INVALID_ARG;
   return MTP_OK;
@@ -1042,6 +1043,7 @@ int mtp_cache_append(const MtpPagedCache *cache, const MtpRope *rope, int B, int
   if (q == q_out && q && ldq != ldqo) return MTP_ERR_INVALID_ARG;
   if (!rope_ok(rope, cache->Dh, &rc)) return rc;
   if (!aligned16(ws) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MTP_ERR_INVALID_ARG;
+  if ((long long)n_rows * (qw + 2 * kvw) / 8 >= (1ll << 36)) return MTP_ERR_UNSUPPORTED_SHAPE;  // warps of the launch
   if (ws_bytes < kAlign) return MTP_ERR_WORKSPACE;
   AppendArgs a{};
   a.B = B; a.Hq = q ? Hq : 0; a.Hkv = cache->Hkv; a.Dh = cache->Dh;

@@ -17,9 +17,10 @@
 // VEC elements that rotate together), with no barrier between warps: it issues
 // its items' loads first, finds the row's sequence and position under them,
 // computes the row's rot/2 sines and cosines two a lane into its own corner of
-// shared memory, then rotates and stores.  Recomputing the sines for the four
-// units of a row costs less than a block-wide barrier a row: 8190 rows of 40 + 16
-// heads of 128 took 96 us with a block a row.
+// shared memory, then rotates and stores.  Recomputing the sines for each unit of
+// a row costs less than a block-wide barrier a row: 8190 rows of 40 + 16 heads of
+// 128 took 96 us with a block a row, 45 us this way (5.2 TB/s, 77% of the copy
+// rate; what is left is the chain position -> page -> store of each warp).
 #include "internal.h"
 #include "paged.cuh"
 
@@ -79,7 +80,7 @@ __device__ __forceinline__ int starts_upto(const int *row_start, int B, int row,
 }
 
 template <int VEC, int U>
-__global__ void __launch_bounds__(32 * kAppWarps) cache_append_kernel(const __grid_constant__ AppendArgs p) {
+__global__ void __launch_bounds__(32 * kAppWarps, U == 1 ? 1 : 5) cache_append_kernel(const __grid_constant__ AppendArgs p) {
   trace_start(kTkAppend);
   using T = typename Bf<VEC>::T;
   __shared__ float2 cs_all[kAppWarps][64];  // rot / 2 <= 64
@@ -133,13 +134,29 @@ __global__ void __launch_bounds__(32 * kAppWarps) cache_append_kernel(const __gr
   }
 
   // ---- the row's sequence: the last one that starts at or before it (those that
-  // start at the same row are empty but the last of them)
-  const int b = p.row_start ? starts_upto(p.row_start, p.B, row, lane) - 1 : row;
+  // start at the same row are empty but the last of them).  For up to 32 sequences
+  // a lane has one's numbers in hand, and the search costs no second round trip.
   bool real = false;
-  int pos = 0, page = -1;
+  int b, s0 = row, s1 = row + 1, c0 = 0, pos = 0, page = -1;
+  if (!p.row_start) {
+    b = row;
+    c0 = __ldcg(&p.ctx_len[b]) + p.ctx_add;
+  } else if (p.B <= 32) {
+    const int mine = min(lane, p.B - 1);
+    const int x0 = __ldcg(&p.row_start[mine]), x1 = __ldcg(&p.row_start[mine + 1]), x2 = __ldcg(&p.ctx_len[mine]);
+    b = __popc(__ballot_sync(kFull, lane < p.B && x0 <= row)) - 1;
+    s0 = __shfl_sync(kFull, x0, max(b, 0));
+    s1 = __shfl_sync(kFull, x1, max(b, 0));
+    c0 = __shfl_sync(kFull, x2, max(b, 0)) + p.ctx_add;
+  } else {
+    b = starts_upto(p.row_start, p.B, row, lane) - 1;
+    if (b >= 0) {
+      s0 = __ldcg(&p.row_start[b]);
+      s1 = __ldcg(&p.row_start[b + 1]);
+      c0 = __ldcg(&p.ctx_len[b]) + p.ctx_add;
+    }
+  }
   if (b >= 0) {
-    const int s0 = p.row_start ? __ldcg(&p.row_start[b]) : row, s1 = p.row_start ? __ldcg(&p.row_start[b + 1]) : row + 1;
-    const int c0 = __ldcg(&p.ctx_len[b]) + p.ctx_add;
     const int ctx = min(max(c0, 0), p.cap);
     real = row < s1 && s0 >= 0 && row >= s0;
     pos = ctx + row - s0;
@@ -244,7 +261,9 @@ cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t s, bool pdl) {
   // few rows: an item a lane, more warps, the shortest chain
   if ((long long)a.n_rows * items < 152ll * 2048)
     return wide ? launch_append<8, 1>(a, items, s, pdl) : launch_append<4, 1>(a, items, s, pdl);
-  return wide ? launch_append<8, 4>(a, items, s, pdl) : launch_append<4, 4>(a, items, s, pdl);
+  // many rows: two items a lane at five blocks an SM (8190 rows of 40 + 16 heads of
+  // 128: 45 us; one item 64, four items at three blocks 46, at five, spilling, 60)
+  return wide ? launch_append<8, 2>(a, items, s, pdl) : launch_append<4, 2>(a, items, s, pdl);
 }
 
 MTP_TRACE_COLLECTOR(cache_append)

@@ -121,3 +121,19 @@ def test_a_graph_replays_on_new_inputs():
     torch.cuda.synchronize()
     ref, mag = logits_reference(logits, drafts, 2000, **r)
     check_logits(out, ref, mag)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_more_logits_than_32_bits_count(in_place):
+    from mtp_speculative_decoding_draft_gb300 import binding as bd
+    B, k, V = 1010, 8, 256001 - 18000
+    assert B * (k + 1) * V > 2 ** 31
+    logits = torch.zeros(B, k + 1, V, device="cuda")
+    logits[-1].normal_()
+    _, drafts, r = rules_case(B, k, 5, hist=3, mask=False, bias=2, seed=4)
+    last = logits[-1:].clone()
+    out = logits if in_place else torch.empty_like(logits)
+    bd.spec_adjust_logits(B, k, V, bd.make_logit_rules(**r), logits, drafts, out)
+    sub = {n: None if t is None else t[-1:] for n, t in r.items()}
+    ref, mag = logits_reference(last, drafts[-1:], V, **sub)
+    check_logits(out[-1:], ref, mag)

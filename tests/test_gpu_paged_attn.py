@@ -163,3 +163,63 @@ def test_a_row_that_sees_nothing_is_zero(rows):
     out, lse, st = attend(d)
     assert st & 4
     assert (out[:rows] == 0).all() and torch.isneginf(lse[:rows]).all()
+
+
+@pytest.mark.parametrize("rows", [4, 70])
+def test_a_pool_past_32_bits(rows):
+    """Elements past 2^32: 8.6 GB pools whose last pages hold the sequence."""
+    from mtp_speculative_decoding_draft_gb300 import binding as bd
+    d = make_case([rows], [200], 8, 2, 128, 128, seed=13)
+    n_pages = 2 ** 32 // (2 * 128 * 128) + 7
+    big = [torch.empty(n_pages, 2, 128, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    table = torch.zeros_like(d["table"])
+    for i in range(table.shape[1]):
+        table[0, i] = n_pages - 1 - i
+        for pool, name in zip(big, ("k_pages", "v_pages")):
+            pool[n_pages - 1 - i] = d[name][int(d["table"][0, i])]
+    # the last rows come through the append
+    ws = bd.alloc_workspace(256)
+    k, v = (x[200:].cuda() for x in d["seqs"][0])
+    for pool in big:
+        for j in range(200, 200 + rows):
+            pool[n_pages - 1 - j // 128, :, j % 128] = float("nan")
+    bd.mtp_cache_append(bd.make_paged_cache(big[0], big[1], table), None, d["row_start"], d["ctx_len"], None, k, v, None, ws)
+    d.update(k_pages=big[0], v_pages=big[1], table=table)
+    run(d)
+    assert bd.get_status(ws) == 0
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    cases = [make_case([4] * 20, [900 + 37 * i for i in range(20)], 8, 2, 128, 64, seed=14),
+             make_case([90, 4, 200], [700, 30, 400], 8, 2, 128, 64, seed=15),
+             make_case([2] * 9, [2000 + i for i in range(9)], 8, 2, 64, 16, seed=16, window=500, sinks=4)]
+    alone = [attend(d)[:2] for d in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for turn in range(4):
+        got = []
+        for d, s in zip(cases, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                from mtp_speculative_decoding_draft_gb300 import binding as bd
+                cache = bd.make_paged_cache(d["k_pages"], d["v_pages"], d["table"])
+                out, lse = torch.full_like(d["q"], 7.0), torch.full((d["n_rows"], d["Hq"]), 7.0, device="cuda")
+                ws = bd.alloc_workspace(bd.paged_attn_workspace_size(d["B"], d["n_rows"], 0, d["Hq"], d["Hkv"], d["Dh"]))
+                for _ in range(3):
+                    bd.mtp_paged_attn(cache, d["row_start"], d["ctx_len"], d["q"], out, lse, ws, window=d["window"], sinks=d["sinks"])
+                got.append((out, lse, ws))
+        torch.cuda.synchronize()
+        for (o, l, _), (ro, rl) in zip(got, alone):
+            assert torch.equal(o, ro) and torch.equal(l, rl)
+
+
+def test_calls_of_many_shapes_share_a_workspace():
+    from mtp_speculative_decoding_draft_gb300 import binding as bd
+    cases = [make_case([90, 4, 200], [700, 30, 400], 8, 2, 128, 64, seed=15), make_case([1], [5000], 8, 2, 128, 64, seed=17),
+             make_case([3, 9], [10, 900], 8, 1, 64, 16, seed=18), make_case([40] * 30, [64] * 30, 4, 4, 32, 16, seed=19)]
+    ws = bd.alloc_workspace(max(bd.paged_attn_workspace_size(d["B"], d["n_rows"], 0, d["Hq"], d["Hkv"], d["Dh"]) for d in cases))
+    for d in cases + cases[::-1]:
+        out, lse = torch.full_like(d["q"], 7.0), torch.full((d["n_rows"], d["Hq"]), 7.0, device="cuda")
+        bd.mtp_paged_attn(bd.make_paged_cache(d["k_pages"], d["v_pages"], d["table"]), d["row_start"], d["ctx_len"], d["q"], out,
+                          lse, ws)
+        check_attend(d, out, lse)
+    assert bd.get_status(ws) == 0

@@ -74,6 +74,7 @@ def test_attention_refusals(lib):
     assert attn(lib, max_rows=-1) == INVALID and attn(lib, window=-1) == INVALID and attn(lib, sinks=-1) == INVALID
     assert attn(lib, scale=-1.0) == INVALID and attn(lib, scale=math.inf) == INVALID and attn(lib, scale=math.nan) == INVALID
     assert attn(lib, q=None) == INVALID and attn(lib, out=None) == INVALID and attn(lib, out=OK_PTR) == INVALID
+    assert attn(lib, n=(1 << 29) + 1) == SHAPE and append(lib, n=(1 << 29) + 1) == SHAPE
     assert attn(lib, lse=ODD_PTR) == INVALID and attn(lib, ldo=4100) == INVALID
     need = lib.mtp_paged_attn_workspace_size(2, 8, 0, 32, 8, 128)
     assert need > 256 and attn(lib, wsb=need - 1) == WORKSPACE
