@@ -1043,7 +1043,8 @@ int mtp_cache_append(const MtpPagedCache *cache, const MtpRope *rope, int B, int
   if (q == q_out && q && ldq != ldqo) return MTP_ERR_INVALID_ARG;
   if (!rope_ok(rope, cache->Dh, &rc)) return rc;
   if (!aligned16(ws) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MTP_ERR_INVALID_ARG;
-  if ((long long)n_rows * (qw + 2 * kvw) / 8 >= (1ll << 36)) return MTP_ERR_UNSUPPORTED_SHAPE;  // warps of the launch
+  // the launch counts its warps (32 items of 8 elements at least) in 32 bits
+  if ((long long)n_rows * ((qw + 2 * kvw) / 256 + 1) >= (1ll << 31)) return MTP_ERR_UNSUPPORTED_SHAPE;
   if (ws_bytes < kAlign) return MTP_ERR_WORKSPACE;
   AppendArgs a{};
   a.B = B; a.Hq = q ? Hq : 0; a.Hkv = cache->Hkv; a.Dh = cache->Dh;

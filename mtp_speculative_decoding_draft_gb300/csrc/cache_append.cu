@@ -86,12 +86,12 @@ __global__ void __launch_bounds__(32 * kAppWarps, U == 1 ? 1 : 5) cache_append_k
   __shared__ float2 cs_all[kAppWarps][64];  // rot / 2 <= 64
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float2 *cs = cs_all[warp];
-  const int iph = p.Dh / (2 * VEC);                 // items of a head
+  const int ips = __ffs(p.Dh / (2 * VEC)) - 1, iph = 1 << ips;  // items of a head
   const int rph = p.rot / (2 * VEC);                // of them, rotated
   const int q_items = p.q ? p.Hq * iph : 0, kv_items = p.Hkv * iph;
   const int items = q_items + 2 * kv_items, upr = (items + 32 * U - 1) / (32 * U);
-  const long long unit = (long long)blockIdx.x * kAppWarps + warp;
-  const int row = (int)(unit / upr), first = (int)(unit % upr) * 32 * U;
+  const unsigned unit = blockIdx.x * kAppWarps + warp;
+  const int row = (int)(unit / (unsigned)upr), first = (int)(unit - (unsigned)row * (unsigned)upr) * 32 * U;
   const bool half = p.layout == 0;
   grid_dep_wait();
   trace_dep(kTkAppend);
@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(32 * kAppWarps, U == 1 ? 1 : 5) cache_append_k
     const int it = first + n * 32 + lane;
     which[n] = it >= items ? -1 : it < q_items ? 0 : it < q_items + kv_items ? 1 : 2;
     const int i = which[n] == 1 ? it - q_items : which[n] == 2 ? it - q_items - kv_items : it;
-    head[n] = i / iph;
-    const int u = i - head[n] * iph;
+    head[n] = i >> ips;
+    const int u = i & (iph - 1);
     rot[n] = which[n] < 2 && u < rph;
     e0[n] = rot[n] && half ? u * VEC : 2 * u * VEC;
     e1[n] = rot[n] && half ? e0[n] + p.rot / 2 : e0[n] + VEC;

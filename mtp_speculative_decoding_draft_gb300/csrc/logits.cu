@@ -175,6 +175,17 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// The same in shared memory: a whole vector read and written has no bank conflicts.
+__device__ __forceinline__ void cover_shared(float *x, uint32_t m) {
+  if (m == 0xfu) return;
+  float4 v = *reinterpret_cast<const float4 *>(x);
+  if (!(m & 1u)) v.x = -INFINITY;
+  if (!(m & 2u)) v.y = -INFINITY;
+  if (!(m & 4u)) v.z = -INFINITY;
+  if (!(m & 8u)) v.w = -INFINITY;
+  *reinterpret_cast<float4 *>(x) = v;
+}
+
 constexpr int range_bytes(bool bias) { return CH * (bias ? 10 : 6); }
 
 }  // namespace
@@ -198,8 +209,10 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
   const int n = r.c1 - r.c0;
   // rows of V % 4 != 0 start off a 16-byte boundary: the copies start at the first
   // aligned token and take whole vectors, the few tokens beside them go one by one
-  auto row_base = [&](int j) { return ((size_t)r.b * (p.k + 1) + j) * p.V + r.c0; };
-  auto row_lead = [&](int j) { return min(n, (int)((4 - (row_base(j) & 3)) & 3)); };
+  const size_t base0 = (size_t)r.b * (p.k + 1) * p.V + r.c0;
+  const unsigned off0 = (unsigned)(base0 & 3), offv = (unsigned)p.V & 3u;
+  auto row_base = [&](int j) { return base0 + (size_t)j * p.V; };
+  auto row_lead = [&](int j) { return min(n, (int)((4u - ((off0 + j * offv) & 3u)) & 3u)); };
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) mbar_init(&full[s], 1);
     fence_barrier_init();
@@ -221,7 +234,11 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
     const int lead = row_lead(j), nv = (n - lead) / 4;
     const uint32_t *mask = p.mask + ((size_t)r.b * (p.k + 1) + j) * words;
 #pragma unroll
-    for (int u = 0; u < VPT; ++u) next_mask[u] = tid + u * NT < nv ? mask4(mask, r.c0 + lead + 4 * (tid + u * NT)) : 0xfu;
+    for (int u = 0; u < VPT; ++u) {
+      const int i = tid + u * NT, t = r.c0 + lead + 4 * i;
+      next_mask[u] = 0xfu;
+      if (i < nv) next_mask[u] = offv | off0 ? mask4(mask, t) : __ldg(&mask[t >> 5]) >> (t & 31) & 0xfu;
+    }
   };
   if (p.mask) fetch_mask(j0);
   r.build(p);
@@ -245,7 +262,7 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
       if (n_list) __syncthreads();
 #pragma unroll
       for (int u = 0; u < VPT; ++u)
-        if (tid + u * NT < nv) cover(row + 4 * (tid + u * NT), m[u]);
+        if (tid + u * NT < nv) cover_shared(row + 4 * (tid + u * NT), m[u]);
     }
     // the tokens before the first vector and behind the last
     const int tail = lead + 4 * nv, singles = lead + (n - tail);
