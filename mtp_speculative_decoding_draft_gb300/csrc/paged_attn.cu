@@ -501,9 +501,9 @@ constexpr int kCombineThreads = 256;
 constexpr int kMaxDescs = 256;  // CTAs at most
 
 template <int DH>
-__global__ void __launch_bounds__(kCombineThreads) paged_combine_tc_kernel(const __grid_constant__ PagedArgs p, int ctas) {
+__global__ void __launch_bounds__(kCombineThreads, 6) paged_combine_tc_kernel(const __grid_constant__ PagedArgs p, int ctas) {
   trace_start(kTkPagedCombine);
-  constexpr int PER = DH / 32, kBatch = 4, NW = kCombineThreads / 32;
+  constexpr int PER = DH / 32, kBatch = 2, NW = kCombineThreads / 32;
   __shared__ PagedDesc desc[kMaxDescs];
   __shared__ int before[kMaxDescs + 1], sums[NW];
   __shared__ float part[NW][DH + 2];
@@ -769,7 +769,7 @@ cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const 
     if ((e = launch_paged_attn_tc(tp, n, s, pdl))) return e;
     static_assert(kMaxSms <= kMaxDescs, "a description a CTA");
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = config(dim3(4 * n), kCombineThreads, 0, s, attr, pdl);
+    cudaLaunchConfig_t cfg = config(dim3(6 * n), kCombineThreads, 0, s, attr, pdl);
     note_launch();
     return args.Dh == 64 ? cudaLaunchKernelEx(&cfg, paged_combine_tc_kernel<64>, tp.a, n)
                          : cudaLaunchKernelEx(&cfg, paged_combine_tc_kernel<128>, tp.a, n);

@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kTK = 128;          // keys per tile
 constexpr int kThreads = 384;   // three warpgroups: the registers move between whole ones
+constexpr int kItemCost = 6;     // tiles that a segment costs besides its own (4 x 2048 rows: 0 158 us, 4 145, 8 141)
 constexpr int kProducer = 8, kIssuer = 9, kQuery = 10, kClear = 11;
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -231,12 +232,13 @@ __device__ __forceinline__ long long block_scan(long long v, long long *incl, lo
 }
 
 // Walks a share's items in the plan's order, one segment at a time; the interface
-// of PagedWalk.
+// of PagedWalk.  On the line an item is kItemCost tiles, which stand for what a
+// segment costs besides its tiles (queries, first scores, output), then its tiles.
 template <int TK>
 struct PlanWalk {
   const PagedTcParams &sp;
   const PagedArgs &p;
-  long long pos, end, per;
+  long long first, end, per;  // where the item and the share's end lie on the line
   int i, b, h, t0;
   PagedSeq s;
   PagedRange r;
@@ -246,16 +248,17 @@ struct PlanWalk {
     const PagedStart *st = &sp.start[blockIdx.x];
     const longlong2 e = __ldcg(reinterpret_cast<const longlong2 *>(&st->end));
     i = __ldcg(&st->i);
-    const long long before = load(&st->item);
+    load(&st->item);
     end = e.x;
     per = e.y;
-    pos = per * (long long)blockIdx.x;
-    if (pos >= end) return;
-    i0 = (int)(pos - before);
+    const long long at = per * (long long)blockIdx.x - first - kItemCost;
+    if (at + first + kItemCost >= end) return;  // no share
+    i0 = at > 0 ? (int)at : 0;
     cut();
   }
-  __device__ __forceinline__ long long load(const PagedItem *it) {
+  __device__ __forceinline__ void load(const PagedItem *it) {
     const int4 x = __ldcg(reinterpret_cast<const int4 *>(&it->b)), y = __ldcg(reinterpret_cast<const int4 *>(&it->row0));
+    first = __ldcg(&it->first);
     b = x.x;
     h = x.y;
     t0 = x.z;
@@ -263,23 +266,22 @@ struct PlanWalk {
     s.n = y.y;
     s.ctx = y.z;
     r = paged_range<TK>(p, s, t0, t1());
-    return __ldcg(&it->first);
   }
   __device__ __forceinline__ int t1() const { return min(s.n, t0 + p.tpb); }
-  __device__ __forceinline__ bool valid() const { return pos < end; }
+  __device__ __forceinline__ bool valid() const { return i0 < i1; }
   __device__ __forceinline__ bool starts() const { return i0 == 0; }
   __device__ __forceinline__ bool ends() const { return i1 == r.count; }
+  __device__ __forceinline__ int last_cta() const { return (int)((first + kItemCost + r.count - 1) / per); }
   __device__ __forceinline__ void cut() {
-    const long long left = end - pos;
-    i1 = (long long)(r.count - i0) <= left ? r.count : i0 + (int)left;
+    const long long left = end - first - kItemCost;
+    i1 = left >= r.count ? r.count : left > 0 ? (int)left : 0;
   }
   __device__ __forceinline__ void next() {
-    pos += i1 - i0;
-    if (pos >= end) return;
+    i0 = i1 = 0;
+    if (first + kItemCost + r.count >= end) return;
     do ++i;
-    while (__ldcg(&sp.items[i].count) == 0);  // pos < end: an item follows
+    while (__ldcg(&sp.items[i].count) == 0);  // the line goes on: an item follows
     load(&sp.items[i]);
-    i0 = 0;
     cut();
   }
 };
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_tc_plan_kernel(const __gri
       else sp.blocks[b] = before;
     }
     nblk += sum;
-    total += block_scan(c * p.Hkv, &incl, scratch);
+    total += block_scan((c + (long long)nb * kItemCost) * p.Hkv, &incl, scratch);
   }
   if (tid == 0) {
     if (near) near_blocks[p.B] = (int)nblk;
@@ -356,14 +358,15 @@ __global__ void __launch_bounds__(kPlanThreads) paged_tc_plan_kernel(const __gri
       it.n = s.n;
       it.ctx = s.ctx;
     }
-    const long long sum = block_scan(it.count, &incl, scratch);
-    it.first = before + incl - it.count;
+    const int len = it.count > 0 ? kItemCost + it.count : 0;  // on the line
+    const long long sum = block_scan(len, &incl, scratch);
+    it.first = before + incl - len;
     before += sum;
     if (i < places) {
       sp.items[i] = it;
       // the shares that start inside this item
       if (it.count > 0)
-        for (long long c = (it.first + per - 1) / per; c * per < it.first + it.count && c < ctas; ++c) {
+        for (long long c = (it.first + per - 1) / per; c * per < it.first + len && c < ctas; ++c) {
           PagedStart st{};
           st.item = it;
           st.end = min(total, (c + 1) * per);
@@ -732,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         d.row0 = w.s.row0 + w.t0;
         d.rows = ntok * p.G;
         d.h = w.h;
-        d.last_cta = (int)((w.pos + w.r.count - 1) / w.per);
+        d.last_cta = w.last_cta();
         p.desc[blockIdx.x] = d;
       }
       tc_fence_before();

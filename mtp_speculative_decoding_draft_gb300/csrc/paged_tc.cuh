@@ -11,7 +11,7 @@ constexpr int kPagedMaxCtas = 160;  // CTAs (SMs) that the workspace has places 
 constexpr int kPagedTcRows = 256;  // packed query rows of a block at most
 
 // One item of the plan: tokens t0 .. of sequence b at kv head h, `count` key tiles
-// that lie behind `first` tiles of the line (count 0: a gap).
+// behind `first` tiles of the line (count 0: a gap).
 struct alignas(16) PagedItem {
   int b, h, t0, count;
   int row0, n, ctx, pad;
