@@ -9,7 +9,7 @@
 // item order, form one line that is cut into equal shares, one per CTA: every
 // CTA streams the same number of tiles whatever the lengths are.  An item that
 // crosses a cut leaves fp32 partial states (running maximum, sum, output) in
-// the workspace, which are joined in key order.
+// the workspace, which a second kernel joins in key order.
 #pragma once
 
 #include <cuda.h>
@@ -24,7 +24,7 @@ constexpr int kTkPagedAttn = 60, kTkPagedAttnTc = 61, kTkPagedCombine = 62, kTkA
 constexpr int kStatusBadRows = 32;
 constexpr int kStatusBadPage = 64;
 
-// What a CTA of the tensor-core kernel leaves for the combine kernel: the item that starts in it and does
+// What a CTA leaves for the combine kernel: the item that starts in it and does
 // not end in it (none: rows = 0).
 struct alignas(16) PagedDesc {
   int row0;      // first query row (of q) of the block
@@ -110,9 +110,12 @@ __device__ __forceinline__ PagedRange paged_range(const PagedArgs &p, const Page
 
 __device__ __forceinline__ int paged_blocks(const PagedArgs &p, int n) { return (n + p.tpb - 1) / p.tpb; }
 
-__device__ __forceinline__ int paged_units(const PagedArgs &p, int count) { return (count + p.min_tiles - 1) / p.min_tiles; }
+__device__ __forceinline__ int paged_units(const PagedArgs &p, int count) {
+  return (count + p.min_tiles - 1) / p.min_tiles;
+}
 
-// Tiles of one kv head of a sequence, and the CTAs they take when every item is cut by itself into runs of min_tiles.
+// Tiles of one kv head of a sequence, and the CTAs they take when every item is
+// cut by itself into runs of min_tiles.
 template <int TK>
 __device__ __forceinline__ long long paged_cost(const PagedArgs &p, const PagedSeq &s, long long *units) {
   *units = 0;
@@ -132,27 +135,32 @@ __device__ __forceinline__ long long paged_cost(const PagedArgs &p, const PagedS
 // one item and the head of the next.
 struct PagedShare {
   long long start, end, per, off;
+  long long head;  // tiles (or runs) of one kv head of sequence b
   int b;
+  PagedSeq s;
   bool cut;
 };
 
-// Executed by all NT threads of the CTA; scratch: 2 NT / 32 + 2 long longs of shared memory.
+// Executed by all NT threads of the CTA; scratch: 2 NT / 32 + 5 long longs of shared memory.
 template <int TK, int NT>
 __device__ PagedShare paged_plan(const PagedArgs &p, long long *scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int NW = NT / 32;
   long long *found = scratch + 2 * NW;
+  // the first NT sequences stay in registers: most batches are read once
+  PagedSeq first_s = {0, 0, 0};
   long long first = 0, first_u = 0, mine = 0, mine_u = 0;
   for (int b = tid; b < p.B; b += NT) {
     long long u;
-    const long long c = paged_cost<TK>(p, paged_seq(p, b, blockIdx.x == 0), &u) * p.Hkv;
-    u *= p.Hkv;
+    const PagedSeq s = paged_seq(p, b, blockIdx.x == 0);
+    const long long c = paged_cost<TK>(p, s, &u);
     if (b < NT) {
+      first_s = s;
       first = c;
       first_u = u;
     }
-    mine += c;
-    mine_u += u;
+    mine += c * p.Hkv;
+    mine_u += u * p.Hkv;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -183,12 +191,18 @@ __device__ PagedShare paged_plan(const PagedArgs &p, long long *scratch) {
   long long acc = 0;
   for (int base = 0; base < p.B; base += NT) {
     const int b = base + tid;
-    long long c = sh.cut ? first_u : first;
+    PagedSeq s = first_s;
+    long long head = sh.cut ? first_u : first;
     if (base > 0) {
       long long u = 0;
-      c = b < p.B ? paged_cost<TK>(p, paged_seq(p, b, false), &u) : 0;
-      c = (sh.cut ? u : c) * p.Hkv;
+      head = 0;
+      if (b < p.B) {
+        s = paged_seq(p, b, false);
+        head = paged_cost<TK>(p, s, &u);
+        if (sh.cut) head = u;
+      }
     }
+    const long long c = head * p.Hkv;
     long long inc = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -203,15 +217,21 @@ __device__ PagedShare paged_plan(const PagedArgs &p, long long *scratch) {
     for (int w = 0; w < warp; ++w) before += scratch[w];
     const long long lo = before + inc - c;
     if (c > 0 && sh.start >= lo && sh.start < lo + c) {
-      found[0] = b;
+      found[0] = (long long)b << 32 | (unsigned)s.row0;
       found[1] = sh.start - lo;
+      found[2] = head;
+      found[3] = (long long)s.n << 32 | (unsigned)s.ctx;
     }
 #pragma unroll
     for (int w = 0; w < NW; ++w) acc += scratch[w];
     __syncthreads();
     if (found[0] >= 0) {
-      sh.b = (int)found[0];
+      sh.b = (int)(found[0] >> 32);
+      sh.s.row0 = (int)(unsigned)found[0];
       sh.off = found[1];
+      sh.head = found[2];
+      sh.s.n = (int)(found[3] >> 32);
+      sh.s.ctx = (int)(unsigned)found[3];
       break;
     }
   }
@@ -228,17 +248,14 @@ struct PagedWalk {
   PagedSeq s;
   PagedRange r;
   int i0, i1;
-  int first, last;  // the CTAs in which the item starts and ends
+  int last;  // the CTA in which the item ends
 
   __device__ __forceinline__ PagedWalk(const PagedArgs &pa, const PagedShare &sh)
-      : p(pa), pos(sh.start), end(sh.end), per(sh.per), b(sh.b), h(0), t0(0), i0(0), i1(0), first(0), last(0) {
+      : p(pa), pos(sh.start), end(sh.end), per(sh.per), b(sh.b), h(0), t0(0), i0(0), i1(0), last(0) {
     if (pos >= end) return;
-    s = paged_seq(p, b, false);
-    long long u;
-    long long c = paged_cost<TK>(p, s, &u);
-    if (sh.cut) c = u;
-    h = (int)(sh.off / c);
-    long long rem = sh.off % c;
+    s = sh.s;
+    h = (int)(sh.off / sh.head);
+    long long rem = sh.off - h * sh.head;
     for (;;) {
       r = paged_range<TK>(p, s, t0, t1());
       const int n = sh.cut ? paged_units(p, r.count) : r.count;
@@ -250,8 +267,7 @@ struct PagedWalk {
       const int n = paged_units(p, r.count);  // the item's runs, alike to a tile
       i0 = (int)((long long)rem * r.count / n);
       i1 = (int)((long long)(rem + 1) * r.count / n);
-      first = (int)blockIdx.x - (int)rem;
-      last = first + n - 1;
+      last = (int)blockIdx.x - (int)rem + n - 1;
       pos = 0;
       end = i1 - i0;
     } else {
@@ -266,7 +282,6 @@ struct PagedWalk {
   __device__ __forceinline__ void cut() {
     const long long left = end - pos;
     i1 = (long long)(r.count - i0) <= left ? r.count : i0 + (int)left;
-    first = (int)((pos - i0) / per);
     last = (int)((pos - i0 + r.count - 1) / per);
   }
   __device__ __forceinline__ void next() {

