@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           const long long off = (long long)(row0 + r / p.G) * p.ldo + (w.h * p.G + r % p.G) * DH + d0 + c;
           if (in_bounds(row0 + r / p.G < p.n_rows, p.status)) {
             if (p.out_f32)
-              *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + off) = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+              *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + off) =
+                  make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
             else
               *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + off) =
                   make_uint2(pack2(a.x * f, a.y * f), pack2(a.z * f, a.w * f));
@@ -489,7 +490,8 @@ __global__ void __launch_bounds__(32 * kCombineRows)
         if (p.out_f32) static_cast<float *>(p.out)[off + e] = a[e] * inv;
         else static_cast<__nv_bfloat16 *>(p.out)[off + e] = __float2bfloat16_rn(a[e] * inv);
       }
-      if (lane == 0 && p.lse) p.lse[(size_t)row * p.Hq + hq] = S > 0.f ? (M + log2f(S)) * 0.6931471805599453f : -INFINITY;
+      if (lane == 0 && p.lse)
+        p.lse[(size_t)row * p.Hq + hq] = S > 0.f ? (M + log2f(S)) * 0.6931471805599453f : -INFINITY;
     }
   }
   trace_end(kTkPagedCombine);
@@ -645,7 +647,8 @@ __global__ void __launch_bounds__(kCombineThreads, 6)
         if (p.out_f32) static_cast<float *>(p.out)[at + e] = a[e] * inv;
         else static_cast<__nv_bfloat16 *>(p.out)[at + e] = __float2bfloat16_rn(a[e] * inv);
       }
-      if (lane == 0 && p.lse) p.lse[(size_t)row * p.Hq + hq] = S > 0.f ? (M + log2f(S)) * 0.6931471805599453f : -INFINITY;
+      if (lane == 0 && p.lse)
+        p.lse[(size_t)row * p.Hq + hq] = S > 0.f ? (M + log2f(S)) * 0.6931471805599453f : -INFINITY;
     }
   }
   trace_end(kTkPagedCombine);

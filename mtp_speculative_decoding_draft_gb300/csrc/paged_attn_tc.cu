@@ -14,9 +14,12 @@
 // S_g i+1 is issued behind O_g += P_g V_i, so when a group's scores arrive its
 // accumulator is at rest, and the group's own threads rescale it: only when a
 // row's maximum grew by more than 2^8.  4096 rows over 12288 keys, 32 / 8 heads of
-// 128: 620 us, 1550 TFLOP/s, 83% of the library's rate for one large product; the
-// chain scores -> exponentials -> product of a group (2300 cycles a tile against
-// 2048 of both groups' products) is what is left.
+// 128: 620 us, 1550 TFLOP/s, 83% of the library's rate for one large product (576 us
+// when the pages stay in L2 from call to call).  A tile takes about 2900 cycles, of
+// which both groups' products take 2048: the chain of a group, 1100 cycles from its
+// scores to its weights and 1550 until its next scores, is what is left.  A segment
+// costs about 9000 cycles beside its tiles: 4500 for the output, 2500 for the walk
+// to the next, the rest for its first scores and last product.
 //
 // Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1, 128 each; P_g lies in the
 // first half of S_g.  Warps 0-3 and 4-7 are the groups' softmax, warp 8 brings
@@ -28,7 +31,6 @@
 #include "paged_tc.cuh"
 #include "tcgen05.cuh"
 
-//
 // The order of the line (paged.cuh): with equal contiguous shares each CTA walks
 // the blocks of a few K/V heads one after another, and all heads of the batch are
 // read at the same time; past L2's size every block reads its keys from DRAM
@@ -40,8 +42,9 @@ namespace mtp {
 namespace {
 
 constexpr int kTK = 128;          // keys per tile
-constexpr int kThreads = 384;   // three warpgroups: the registers move between whole ones
-constexpr int kItemCost = 6;     // tiles that a segment costs besides its own (4 x 2048 rows: 0 158 us, 4 145, 8 141)
+constexpr int kThreads = 384;     // three warpgroups: the registers move between whole ones
+// tiles that a segment costs besides its own (4 x 2048 rows: 0 158 us, 4 145, 8 141)
+constexpr int kItemCost = 6;
 constexpr int kProducer = 8, kIssuer = 9, kQuery = 10, kClear = 11;
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -260,7 +263,8 @@ struct PlanWalk {
     cut();
   }
   __device__ __forceinline__ void load(const PagedItem *it) {
-    const int4 x = __ldcg(reinterpret_cast<const int4 *>(&it->b)), y = __ldcg(reinterpret_cast<const int4 *>(&it->row0));
+    const int4 x = __ldcg(reinterpret_cast<const int4 *>(&it->b));
+    const int4 y = __ldcg(reinterpret_cast<const int4 *>(&it->row0));
     first = __ldcg(&it->first);
     b = x.x;
     h = x.y;
@@ -292,7 +296,8 @@ struct PlanWalk {
 }  // namespace
 
 // One CTA: the items of the batch, their order, and where each share starts.
-__global__ void __launch_bounds__(kPlanThreads) paged_tc_plan_kernel(const __grid_constant__ PagedTcParams sp, int ctas) {
+__global__ void __launch_bounds__(kPlanThreads)
+    paged_tc_plan_kernel(const __grid_constant__ PagedTcParams sp, int ctas) {
   trace_start(kTkPagedPlan);
   constexpr int kNear = 1024;  // sequences whose blocks are kept in shared memory
   __shared__ long long scratch[kPlanThreads / 32];
@@ -640,7 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         }
         float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 128; e += 2) x[(e >> 1) & 3] = max3(x[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+        for (int e = 0; e < 128; e += 2)
+          x[(e >> 1) & 3] = max3(x[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
         if (__any_sync(kFull, live && mx > m + 8.f)) {
           const float n = fmaxf(m, mx);
@@ -668,7 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
           uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            float2 y = fma2(make_float2(__uint_as_float(s[64 * c + 2 * e]), __uint_as_float(s[64 * c + 2 * e + 1])), sc2, nu2);
+            const float2 sc = make_float2(__uint_as_float(s[64 * c + 2 * e]), __uint_as_float(s[64 * c + 2 * e + 1]));
+            float2 y = fma2(sc, sc2, nu2);
             y.x = ex2_approx(y.x);
             y.y = ex2_approx(y.y);
             sum[e & 1] = add2(sum[e & 1], y);
@@ -708,8 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
           uint4 v[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            v[e] = make_uint4(__float_as_uint(__uint_as_float(o[4 * e]) * f), __float_as_uint(__uint_as_float(o[4 * e + 1]) * f),
-                              __float_as_uint(__uint_as_float(o[4 * e + 2]) * f), __float_as_uint(__uint_as_float(o[4 * e + 3]) * f));
+            v[e] = make_uint4(__float_as_uint(__uint_as_float(o[4 * e]) * f),
+                              __float_as_uint(__uint_as_float(o[4 * e + 1]) * f),
+                              __float_as_uint(__uint_as_float(o[4 * e + 2]) * f),
+                              __float_as_uint(__uint_as_float(o[4 * e + 3]) * f));
           store_quads<8>(v, mine ? d : nullptr, lane);
         } else {
           uint16_t *d = static_cast<uint16_t *>(p.out) + (long long)qrow * p.ldo + hq * DH + 32 * c;
@@ -769,7 +778,9 @@ static size_t plan_items(int B, int n_rows, int G, int Hkv) {
   return ((size_t)n_rows / (2 * (128 / G)) + B) * Hkv + kPagedMaxCtas;
 }
 
-bool paged_tc_items_ok(int B, int n_rows, int G, int Hkv) { return plan_items(B, n_rows, G, Hkv) < (1ull << 31) - (1 << 20); }
+bool paged_tc_items_ok(int B, int n_rows, int G, int Hkv) {
+  return plan_items(B, n_rows, G, Hkv) < (1ull << 31) - (1 << 20);
+}
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
