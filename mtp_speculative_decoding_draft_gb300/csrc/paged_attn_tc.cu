@@ -14,12 +14,13 @@
 // S_g i+1 is issued behind O_g += P_g V_i, so when a group's scores arrive its
 // accumulator is at rest, and the group's own threads rescale it: only when a
 // row's maximum grew by more than 2^8.  4096 rows over 12288 keys, 32 / 8 heads of
-// 128: 620 us, 1550 TFLOP/s, 83% of the library's rate for one large product (576 us
-// when the pages stay in L2 from call to call).  A tile takes about 2900 cycles, of
-// which both groups' products take 2048: the chain of a group, 1100 cycles from its
-// scores to its weights and 1550 until its next scores, is what is left.  A segment
-// costs about 9000 cycles beside its tiles: 4500 for the output, 2500 for the walk
-// to the next, the rest for its first scores and last product.
+// 128: 580 us by itself (pages in L2 or not), 620 us between large library products;
+// 1660 and 1550 TFLOP/s, 89 and 83% of the library's rate for one large product.  A
+// tile takes about 2900 cycles, of which both groups' products take 2048: the chain
+// of a group, 1100 cycles from its scores to its weights and 1550 until its next
+// scores, is what is left.  A segment costs about 9000 cycles beside its tiles: 4500
+// for the output, 2500 for the walk to the next, the rest for its first scores and
+// last product.
 //
 // Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1, 128 each; P_g lies in the
 // first half of S_g.  Warps 0-3 and 4-7 are the groups' softmax, warp 8 brings
