@@ -14,7 +14,7 @@
 // S_g i+1 is issued behind O_g += P_g V_i, so when a group's scores arrive its
 // accumulator is at rest, and the group's own threads rescale it: only when a
 // row's maximum grew by more than 2^8.  4096 rows over 12288 keys, 32 / 8 heads of
-// 128: 580 us by itself (pages in L2 or not), 620 us between large library products;
+// 128: 580 us by itself (pages in L2 or not), 620 us timed in turn with a plain form;
 // 1660 and 1550 TFLOP/s, 89 and 83% of the library's rate for one large product.  A
 // tile takes about 2900 cycles, of which both groups' products take 2048: the chain
 // of a group, 1100 cycles from its scores to its weights and 1550 until its next
