@@ -59,7 +59,9 @@ enum {
     MTP_STATUS_BAD_TOKEN = 2,  /* a token id outside [0, V); token 0 was used instead */
     MTP_STATUS_BAD_CTX = 4,    /* ctx_len[b] < 0 or ctx_len[b] + k > Lmax; clamped */
     MTP_STATUS_NONFINITE = 8,  /* a logit row without a finite maximum */
-    MTP_STATUS_BAD_ROWS = 32,  /* row_start decreases or leaves the rows; clamped */
+    MTP_STATUS_BAD_ROWS = 32,  /* row_start leaves the rows (clamped), or decreases (the
+                                  attention then leaves every row as it was, an append may
+                                  leave rows out) */
     MTP_STATUS_BAD_PAGE = 64,  /* a page-table entry outside the pool where a position needs
                                   it: page 0 read in its place, an appended row dropped */
     MTP_STATUS_BOUNDS = 16     /* only a library built with MTP_BOUNDS: an index outside

@@ -75,6 +75,11 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs &p, int b, bool fl
   return s;
 }
 
+// Sequence b's rows end before they start.
+__device__ __forceinline__ bool paged_back(const PagedArgs &p, int b) {
+  return p.row_start && __ldcg(&p.row_start[b + 1]) < __ldcg(&p.row_start[b]);
+}
+
 // Keys that some row of tokens [t0, t1) sees: [0, sink_end) and [lo, hi); in
 // tiles of TK keys: the first ns tiles, then tiles ft ..; count in all (at least
 // one, so that a block that sees nothing is still written).
@@ -141,6 +146,9 @@ struct PagedShare {
   bool cut;
 };
 
+// Row starts that decrease may count rows twice: no bound on the blocks would hold and
+// two CTAs could write one row, so that nothing of such a call is attended.
+//
 // Executed by all NT threads of the CTA; scratch: 2 NT / 32 + 5 long longs of shared memory.
 template <int TK, int NT>
 __device__ PagedShare paged_plan(const PagedArgs &p, long long *scratch) {
@@ -150,6 +158,7 @@ __device__ PagedShare paged_plan(const PagedArgs &p, long long *scratch) {
   // the first NT sequences stay in registers: most batches are read once
   PagedSeq first_s = {0, 0, 0};
   long long first = 0, first_u = 0, mine = 0, mine_u = 0;
+  bool back = false;
   for (int b = tid; b < p.B; b += NT) {
     long long u;
     const PagedSeq s = paged_seq(p, b, blockIdx.x == 0);
@@ -161,15 +170,17 @@ __device__ PagedShare paged_plan(const PagedArgs &p, long long *scratch) {
     }
     mine += c * p.Hkv;
     mine_u += u * p.Hkv;
+    back |= paged_back(p, b);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     mine += __shfl_xor_sync(0xffffffffu, mine, o);
     mine_u += __shfl_xor_sync(0xffffffffu, mine_u, o);
   }
+  const bool none = __syncthreads_or(back);
   if (lane == 0) {
-    scratch[warp] = mine;
-    scratch[NW + warp] = mine_u;
+    scratch[warp] = none ? 0 : mine;
+    scratch[NW + warp] = none ? 0 : mine_u;
   }
   __syncthreads();
   long long total = 0, units = 0;

@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   grid_dep_launch();
   // ---- blocks of each sequence, and all tiles
   long long nblk = 0, total = 0, incl;
+  bool back = false;
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     long long c = 0, u;
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       const PagedSeq s = paged_seq(p, b, true);
       c = paged_cost<kTK>(p, s, &u);
       nb = paged_blocks(p, s.n);
+      back |= paged_back(p, b);
     }
     const long long sum = block_scan(nb, &incl, scratch);
     if (b < p.B) {
@@ -333,6 +335,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (near) near_blocks[p.B] = (int)nblk;
     else sp.blocks[p.B] = (int)nblk;
   }
+  // (the barrier also publishes the blocks)  The list has room for the blocks of
+  // disjoint rows: row starts that decrease leave no items, and no share any tiles
+  if (__syncthreads_or(back)) nblk = total = 0;
   // items fit 31 bits (the host checks), so that places and sequences divide in 32
   const unsigned N = (unsigned)(nblk * p.Hkv), q = (N + ctas - 1) / ctas, places = q * ctas;
   const long long per = max((long long)p.min_tiles, (total + ctas - 1) / ctas);
@@ -342,7 +347,6 @@ __global__ void __launch_bounds__(kPlanThreads)
       sp.start[c].end = 0;
       sp.start[c].per = per;
     }
-  __syncthreads();  // the blocks are read below
   auto first_item = [&](int b) { return (unsigned)(near ? near_blocks[b] : __ldcg(&sp.blocks[b])) * p.Hkv; };
   // ---- items, dealt out: place i = c * q + t holds item t * CTAs + c
   long long before = 0;
@@ -773,8 +777,9 @@ cudaError_t paged_tc_set_attributes() {
   return e;
 }
 
-// Items at most: one more block a sequence than its rows fill, a place's round of
-// CTAs for the gaps.
+// Items at most: one more block a sequence than its rows fill (the sequences' rows
+// are disjoint: row starts that decrease leave no items), a place's round of CTAs for
+// the gaps.
 static size_t plan_items(int B, int n_rows, int G, int Hkv) {
   return ((size_t)n_rows / (2 * (128 / G)) + B) * Hkv + kPagedMaxCtas;
 }
