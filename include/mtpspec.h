@@ -465,9 +465,10 @@ int mtp_rope_turns(int n, const double *inv_freq, uint64_t *turns);
  *   q_out     bf16 rows of Hq*Dh, ldqo elements apart; q itself (same stride) to
  *             rotate in place; no other overlap.  q and q_out both NULL: keys
  *             and values only.
- * Products and sums are fp32, rounded once to bf16.  A row whose position lies
- * past max_pages * page (MTP_STATUS_BAD_CTX) or in a page outside the pool
- * (MTP_STATUS_BAD_PAGE) is rotated but not written.  Two rows that map to one
+ * Products and sums are fp32, rounded once to bf16.  A row of a negative ctx_len
+ * or of a position past max_pages * page (MTP_STATUS_BAD_CTX), or in a page outside
+ * the pool (MTP_STATUS_BAD_PAGE), is not written to the pages; its query is rotated
+ * to the nearest position that there is.  Two rows that map to one
  * slot (a page in two sequences' tables) are written in no defined order.
  *   ws        at least 256 bytes, 256-byte aligned: the status word
  */

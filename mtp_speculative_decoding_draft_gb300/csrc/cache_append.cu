@@ -137,32 +137,34 @@ __global__ void __launch_bounds__(32 * kAppWarps, U == 1 ? 1 : 5) cache_append_k
   // start at the same row are empty but the last of them).  For up to 32 sequences
   // a lane has one's numbers in hand, and the search costs no second round trip.
   bool real = false;
-  int b, s0 = row, s1 = row + 1, c0 = 0, pos = 0, page = -1;
+  int b, s0 = row, s1 = row + 1, c0 = 0, pos = 0, page = -1;  // c0: the context as given
   if (!p.row_start) {
     b = row;
-    c0 = __ldcg(&p.ctx_len[b]) + p.ctx_add;
+    c0 = __ldcg(&p.ctx_len[b]);
   } else if (p.B <= 32) {
     const int mine = min(lane, p.B - 1);
     const int x0 = __ldcg(&p.row_start[mine]), x1 = __ldcg(&p.row_start[mine + 1]), x2 = __ldcg(&p.ctx_len[mine]);
     b = __popc(__ballot_sync(kFull, lane < p.B && x0 <= row)) - 1;
     s0 = __shfl_sync(kFull, x0, max(b, 0));
     s1 = __shfl_sync(kFull, x1, max(b, 0));
-    c0 = __shfl_sync(kFull, x2, max(b, 0)) + p.ctx_add;
+    c0 = __shfl_sync(kFull, x2, max(b, 0));
   } else {
     b = starts_upto(p.row_start, p.B, row, lane) - 1;
     if (b >= 0) {
       s0 = __ldcg(&p.row_start[b]);
       s1 = __ldcg(&p.row_start[b + 1]);
-      c0 = __ldcg(&p.ctx_len[b]) + p.ctx_add;
+      c0 = __ldcg(&p.ctx_len[b]);
     }
   }
   if (b >= 0) {
-    const int ctx = min(max(c0, 0), p.cap);
     real = row < s1 && s0 >= 0 && row >= s0;
-    pos = ctx + row - s0;
     if (real) {
-      if (lane == 0 && (c0 != ctx || pos >= p.cap)) set_status(p.status, kStatusBadCtx);
-      if (pos < p.cap) {
+      // a negative context places no row, whatever is added to it
+      const long long at = (long long)c0 + p.ctx_add + (row - s0);
+      const bool placed = c0 >= 0 && at < p.cap;
+      pos = (int)min(max(at, 0ll), (long long)p.cap);  // of a row that is not placed: for its rotation only
+      if (lane == 0 && !placed) set_status(p.status, kStatusBadCtx);
+      if (placed) {
         page = __ldg(&p.page_table[(size_t)b * p.max_pages + (pos >> p.page_shift)]);
         if (page < 0 || page >= p.n_pages) {
           if (lane == 0) set_status(p.status, kStatusBadPage);

@@ -63,11 +63,11 @@ struct PagedSeq {
 // Sequence b's rows and context, clamped to the buffers; flags what was out of range.
 __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs &p, int b, bool flag) {
   const int a = p.row_start ? __ldcg(&p.row_start[b]) : b, e = p.row_start ? __ldcg(&p.row_start[b + 1]) : b + 1;
-  const int c = __ldcg(&p.ctx_len[b]) + p.ctx_add;
+  const long long c = (long long)__ldcg(&p.ctx_len[b]) + p.ctx_add;
   PagedSeq s;
   s.row0 = min(max(a, 0), p.n_rows);
   s.n = min(max(e, s.row0), p.n_rows) - s.row0;
-  s.ctx = min(max(c, 0), p.cap);
+  s.ctx = (int)min(max(c, 0ll), (long long)p.cap);
   if (flag) {
     if (s.row0 != a || s.row0 + s.n != e) set_status(p.status, kStatusBadRows);
     if (s.ctx != c || (long long)s.ctx + s.n > p.cap) set_status(p.status, kStatusBadCtx);

@@ -59,3 +59,49 @@ def test_row_starts_past_the_rows_are_clamped(max_rows):
     out, lse, status = guarded_attention(d, max_rows, past)
     assert status & bd.STATUS_BAD_ROWS
     check_attend(d, out, lse)                                  # clamped to the rows that there are
+
+
+# A context that no position can have: the row is not written, the sequences beside it are.
+@pytest.mark.parametrize("bad", [-1, -3, 2 ** 31 - 1, 2 ** 31 - 2, -2 ** 31])
+@pytest.mark.parametrize("B", [3, 40])                         # row starts from a lane each, and by search
+def test_an_append_at_no_position_writes_nothing(bad, B):
+    from mtp_speculative_decoding_draft_gb300 import binding as bd
+    d = make_case([2] * B, [5 + b for b in range(B)], 4, 2, 64, 16, seed=B)
+    n = d["n_rows"]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(n, 2, 64, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    was = [d[name].clone() for name in ("k_pages", "v_pages")]
+    d["ctx_len"][1] = bad
+    ws = bd.alloc_workspace(256)
+    bd.mtp_cache_append(bd.make_paged_cache(d["k_pages"], d["v_pages"], d["table"]), None, d["row_start"], d["ctx_len"], None,
+                        k, v, None, ws)
+    torch.cuda.synchronize()
+    assert bd.get_status(ws) == bd.STATUS_BAD_CTX
+    for b in range(B):
+        if b != 1:
+            for i in range(2):
+                for pool, x in zip(was, (k, v)):
+                    pool[int(d["table"][b, (5 + b + i) // 16]), :, (5 + b + i) % 16] = x[2 * b + i]
+    for name, pool in zip(("k_pages", "v_pages"), was):
+        assert torch.equal(d[name].view(torch.int16), pool.view(torch.int16))
+
+
+# The draft's depths are appended one by one behind ctx_len: none of them lands on a
+# position that a wrapped or clamped sum gives.
+@pytest.mark.parametrize("bad", [-1, -2, 2 ** 31 - 1, 2 ** 31 - 2])
+def test_a_paged_draft_at_no_position_writes_nothing(bad):
+    from mtp_speculative_decoding_draft_gb300 import binding as bd
+    from mtp_speculative_decoding_draft_gb300 import workloads as W
+    from test_gpu_paged_draft import MID, paged_module
+    w, wts, ctx = MID, W.make_weights(MID), W.make_context(MID)
+    m, _ = paged_module(w, ctx, wts, 64)
+    for pool in m.cache.tensors[:2]:
+        pool.nan_to_num_(0.0)
+    was = [pool.clone() for pool in m.cache.tensors[:2]]
+    m.ctx_len.fill_(bad)
+    m.draft_paged(w.T, 0)
+    torch.cuda.synchronize()
+    assert bd.get_status(m.ws_paged) & bd.STATUS_BAD_CTX
+    m.check_canaries()
+    for pool, x in zip(m.cache.tensors[:2], was):
+        assert torch.equal(pool.view(torch.int16), x.view(torch.int16))
