@@ -526,7 +526,8 @@ int mtp_paged_attn(const MtpPagedCache *cache, int B, int Hq, int n_rows, int ma
  * no penalty is on);  logits, out [B, k+1, V] fp32; out may be logits itself (in
  * place: only what a rule changes is read and written) or must not overlap it.
  * A row that is masked whole is -inf everywhere, which spec_verify reports
- * (MTP_STATUS_NONFINITE).  Needs no workspace; sets no status.
+ * (MTP_STATUS_NONFINITE).  Needs no workspace; sets no status: a row whose copy into
+ * shared memory does not end within the wait limit is read by plain loads instead.
  */
 typedef struct {
     const int32_t *history, *prompt_len, *hist_len;
@@ -590,6 +591,14 @@ int mtp_clear_status(void *ws, mtp_stream_t stream);
  * MTP_ERR_INVALID_ARG (null or misaligned status) or MTP_ERR_CUDA.
  */
 int mtp_selftest_wait_timeout(int32_t *status, mtp_stream_t stream);
+
+/*
+ * Diagnostics.  spec_adjust_logits (out of place, k at least 1) with the copy of every
+ * sequence's second row withheld: the waits for it give up, and the result is the same
+ * all the same.  About 4 s of GPU time for every SM's CTAs.
+ */
+int mtp_selftest_logits_wait(int B, int k, int V, const MtpLogitRules *rules, const float *logits,
+                             const int32_t *draft_tok, float *out, mtp_stream_t stream);
 
 /* Human-readable text for an MTP_ERR_* code. */
 const char *mtp_error_string(int code);

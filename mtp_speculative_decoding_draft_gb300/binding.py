@@ -149,6 +149,8 @@ def _lib():
         L.spec_step_paged.restype = I
         L.spec_adjust_logits.argtypes = [I, I, I, ctypes.POINTER(MtpLogitRules), P, P, P, P]
         L.spec_adjust_logits.restype = I
+        L.mtp_selftest_logits_wait.argtypes = L.spec_adjust_logits.argtypes
+        L.mtp_selftest_logits_wait.restype = I
         L.mtp_get_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
         L.mtp_get_status.restype = I
         L.mtp_clear_status.argtypes = [P, P]
@@ -632,20 +634,24 @@ def make_logit_rules(history=None, prompt_len=None, hist_len=None, rep=None, fre
     return r
 
 
-def spec_adjust_logits(B, k, V, rules, logits, draft_tok, out, stream=None):
-    """Apply rules (make_logit_rules) to the target logits [B, k+1, V] fp32 into
-    out (logits itself: in place); draft_tok [B, k] int32."""
+def _adjust_logits(call, B, k, V, rules, logits, draft_tok, out, stream):
     if rules.B is not None and rules.B < B:
         raise ValueError("the rules hold %d sequences, B is %d" % (rules.B, B))
     mask = rules.tensors[-1]
     if mask is not None and mask.numel() < B * (k + 1) * ((V + 31) // 32):
         raise ValueError("mask must be [B, k+1, ceil(V/32)]")
     n = B * (k + 1) * V
-    rc = _lib().spec_adjust_logits(int(B), int(k), int(V), rules, _ptr(logits, "logits", torch.float32, n),
-                                   _ptr(draft_tok, "draft_tok", torch.int32, B * k) if k else None,
-                                   _ptr(out, "out", torch.float32, n), _stream(stream))
+    rc = getattr(_lib(), call)(int(B), int(k), int(V), rules, _ptr(logits, "logits", torch.float32, n),
+                               _ptr(draft_tok, "draft_tok", torch.int32, B * k) if k else None,
+                               _ptr(out, "out", torch.float32, n), _stream(stream))
     if rc != 0:
-        raise MtpError(rc, "spec_adjust_logits")
+        raise MtpError(rc, call)
+
+
+def spec_adjust_logits(B, k, V, rules, logits, draft_tok, out, stream=None):
+    """Apply rules (make_logit_rules) to the target logits [B, k+1, V] fp32 into
+    out (logits itself: in place); draft_tok [B, k] int32."""
+    _adjust_logits("spec_adjust_logits", B, k, V, rules, logits, draft_tok, out, stream)
 
 
 def get_status(ws, stream=None):
@@ -668,6 +674,11 @@ def selftest_wait_timeout(status, stream=None):
     rc = _lib().mtp_selftest_wait_timeout(_ptr(status, "status", torch.int32, 1), _stream(stream))
     if rc != 0:
         raise MtpError(rc, "mtp_selftest_wait_timeout")
+
+
+def selftest_logits_wait(B, k, V, rules, logits, draft_tok, out, stream=None):
+    """spec_adjust_logits with a copy withheld, so that the waits for it give up."""
+    _adjust_logits("mtp_selftest_logits_wait", B, k, V, rules, logits, draft_tok, out, stream)
 
 
 def profiler_enable(on=True):

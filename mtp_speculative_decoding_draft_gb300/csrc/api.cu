@@ -1108,8 +1108,8 @@ int mtp_paged_attn(const MtpPagedCache *cache, int B, int Hq, int n_rows, int ma
   return e == cudaErrorNotSupported ? MTP_ERR_CUDA : cuda_rc(e);
 }
 
-int spec_adjust_logits(int B, int k, int V, const MtpLogitRules *rules, const float *logits, const int32_t *draft_tok,
-                       float *out, mtp_stream_t stream) {
+static int adjust_logits(int B, int k, int V, const MtpLogitRules *rules, const float *logits, const int32_t *draft_tok,
+                         float *out, mtp_stream_t stream, bool stall) {
   if (!rules || B < 1 || k < 0 || k > 8 || V < 1 || V > (1 << 30) || B > (1 << 20)) return MTP_ERR_INVALID_ARG;
   if (!aligned16(logits) || !aligned16(out)) return MTP_ERR_INVALID_ARG;
   if ((long long)B * ((V + 1023) / 1024) >= (1ll << 31)) return MTP_ERR_UNSUPPORTED_SHAPE;
@@ -1136,9 +1136,20 @@ int spec_adjust_logits(int B, int k, int V, const MtpLogitRules *rules, const fl
   a.draft_tok = penal ? draft_tok : nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   NvtxRange r("spec adjust logits");
-  cudaError_t e = launch_adjust_logits(a, di.sms, s, use_pdl());
+  cudaError_t e = launch_adjust_logits(a, di.sms, s, use_pdl(), stall);
   if (e == cudaSuccess) e = cudaGetLastError();
   return cuda_rc(e);
+}
+
+int spec_adjust_logits(int B, int k, int V, const MtpLogitRules *rules, const float *logits, const int32_t *draft_tok,
+                       float *out, mtp_stream_t stream) {
+  return adjust_logits(B, k, V, rules, logits, draft_tok, out, stream, false);
+}
+
+int mtp_selftest_logits_wait(int B, int k, int V, const MtpLogitRules *rules, const float *logits,
+                             const int32_t *draft_tok, float *out, mtp_stream_t stream) {
+  if (k < 1 || logits == out) return MTP_ERR_INVALID_ARG;
+  return adjust_logits(B, k, V, rules, logits, draft_tok, out, stream, true);
 }
 
 int mtp_get_status(const void *ws, mtp_stream_t stream, int32_t *status) {

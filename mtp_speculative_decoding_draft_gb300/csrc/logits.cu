@@ -190,6 +190,9 @@ constexpr int range_bytes(bool bias) { return CH * (bias ? 10 : 6); }
 
 }  // namespace
 
+// STALL: for the self-test alone, the second row of every CTA is announced and never
+// brought, so that its wait runs out.
+template <bool STALL>
 __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant__ LogitArgs p) {
   trace_start(kTkLogits);
   extern __shared__ __align__(128) unsigned char smem[];
@@ -224,8 +227,8 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
   auto bring = [&](int j) {  // thread 0
     const int lead = row_lead(j), nv = (n - lead) / 4;
     const int s = (j - j0) % kRing;
-    mbar_arrive_expect_tx(&full[s], (uint32_t)nv * 16u);
-    if (nv) bulk_g2s(ring + s * CH, p.logits + row_base(j) + lead, (uint32_t)nv * 16u, &full[s]);
+    mbar_arrive_expect_tx(&full[s], STALL && j == j0 + 1 ? 16u : (uint32_t)nv * 16u);
+    if (nv && !(STALL && j == j0 + 1)) bulk_g2s(ring + s * CH, p.logits + row_base(j) + lead, (uint32_t)nv * 16u, &full[s]);
   };
   if (tid == 0)
     for (int j = j0; j < j1 && j < j0 + kRing; ++j) bring(j);
@@ -244,8 +247,9 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
   r.build(p);
 
   const int n_list = listed;
-  bool ok = true;
-  for (int j = j0; j < j1; ++j) {
+  bool ok = true;  // this thread's waits have all ended
+  int j = j0;
+  for (; j < j1; ++j) {
     const int lead = row_lead(j), nv = (n - lead) / 4, s = (j - j0) % kRing;
     float *row = ring + s * CH;
     const uint32_t *mask = p.mask ? p.mask + ((size_t)r.b * (p.k + 1) + j) * words : nullptr;
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
     for (int u = 0; u < VPT; ++u) m[u] = next_mask[u];
     if (p.mask && j + 1 < j1) fetch_mask(j + 1);
     if (ok) ok = mbar_wait(&full[s], (uint32_t)((j - j0) / kRing) & 1u, nullptr);
-    for (int i = tid; i < n_list; i += NT) {
+    for (int i = tid; ok && i < n_list; i += NT) {
       const int o = r.list[i], at = o - lead;
       if (at >= 0 && at < 4 * nv) row[at] = r.rule(row[at], o, j);
     }
@@ -262,7 +266,7 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
       if (n_list) __syncthreads();
 #pragma unroll
       for (int u = 0; u < VPT; ++u)
-        if (tid + u * NT < nv) cover_shared(row + 4 * (tid + u * NT), m[u]);
+        if (ok && tid + u * NT < nv) cover_shared(row + 4 * (tid + u * NT), m[u]);
     }
     // the tokens before the first vector and behind the last
     const int tail = lead + 4 * nv, singles = lead + (n - tail);
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
           !mask || mask1(mask, r.c0 + o) ? r.rule(__ldcg(p.logits + row_base(j) + o), o, j) : -INFINITY;
     }
     fence_proxy_async_smem();
-    __syncthreads();
+    if (!__syncthreads_and(ok)) break;
     if (tid == 0) {
       if (nv) bulk_s2g(p.out + row_base(j) + lead, row, (uint32_t)nv * 16u);
       bulk_commit();
@@ -281,6 +285,19 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
         bulk_wait_read();
         bring(j + kRing);
       }
+    }
+  }
+  // A row whose load did not land within the wait limit is not taken from the ring,
+  // nor is any after it: they are read from the logits by plain loads.  What was
+  // brought for them has the limit once more to land before the CTA exits.
+  if (j < j1) {
+    if (tid == 0)
+      for (int i = j; i < j1 && i < j + kRing; ++i) mbar_wait(&full[(i - j0) % kRing], (uint32_t)((i - j0) / kRing) & 1u, nullptr);
+    for (; j < j1; ++j) {
+      const uint32_t *mask = p.mask ? p.mask + ((size_t)r.b * (p.k + 1) + j) * words : nullptr;
+      for (int o = tid; o < n; o += NT)
+        p.out[row_base(j) + o] =
+            !mask || mask1(mask, r.c0 + o) ? r.rule(__ldcg(p.logits + row_base(j) + o), o, j) : -INFINITY;
     }
   }
   if (tid == 0) bulk_wait_all();
@@ -335,21 +352,24 @@ __global__ void __launch_bounds__(NT) adjust_logits_in_place_kernel(const __grid
 }
 
 cudaError_t logits_set_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(adjust_logits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(adjust_logits_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        range_bytes(true) + kRing * CH * 4);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(adjust_logits_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             range_bytes(true) + kRing * CH * 4);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(adjust_logits_in_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              range_bytes(true));
   return e;
 }
 
-cudaError_t launch_adjust_logits(const LogitArgs &args, int sms, cudaStream_t s, bool pdl) {
+cudaError_t launch_adjust_logits(const LogitArgs &args, int sms, cudaStream_t s, bool pdl, bool stall) {
   LogitArgs a = args;
   const bool in_place = a.logits == a.out;
   const long long ranges = (long long)a.B * ((a.V + CH - 1) / CH);
   // One scan of the history serves all rows of a range; with few ranges the rows
   // go to CTAs of their own instead, each with its scan.
-  a.rows = ranges >= 2 * sms ? a.k + 1 : 1;
+  a.rows = stall || ranges >= 2 * sms ? a.k + 1 : 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)ranges, (unsigned)((a.k + a.rows) / a.rows));
   cfg.blockDim = dim3(NT);
@@ -361,8 +381,9 @@ cudaError_t launch_adjust_logits(const LogitArgs &args, int sms, cudaStream_t s,
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   note_launch();
-  return in_place ? cudaLaunchKernelEx(&cfg, adjust_logits_in_place_kernel, a)
-                  : cudaLaunchKernelEx(&cfg, adjust_logits_kernel, a);
+  if (in_place) return cudaLaunchKernelEx(&cfg, adjust_logits_in_place_kernel, a);
+  return stall ? cudaLaunchKernelEx(&cfg, adjust_logits_kernel<true>, a)
+               : cudaLaunchKernelEx(&cfg, adjust_logits_kernel<false>, a);
 }
 
 MTP_TRACE_COLLECTOR(logits)

@@ -26,6 +26,7 @@ struct LogitArgs {
   int rows;               // rows of a CTA (set by the launch)
 };
 cudaError_t logits_set_attributes();
-cudaError_t launch_adjust_logits(const LogitArgs &a, int sms, cudaStream_t s, bool pdl);
+// stall: the self-test's kernel, in which the second row of every CTA never arrives
+cudaError_t launch_adjust_logits(const LogitArgs &a, int sms, cudaStream_t s, bool pdl, bool stall);
 
 }  // namespace mtp
