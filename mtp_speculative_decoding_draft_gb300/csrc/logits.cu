@@ -186,6 +186,18 @@ __device__ __forceinline__ void cover_shared(float *x, uint32_t m) {
   *reinterpret_cast<float4 *>(x) = v;
 }
 
+// Rows [j0, j1) of a range by plain loads and stores.
+__device__ __noinline__ void plain_rows(const LogitArgs &p, const Range r, int j0, int j1) {
+  const int words = (p.V + 31) / 32;
+  for (int j = j0; j < j1; ++j) {
+    const size_t row = (size_t)r.b * (p.k + 1) + j;
+    const uint32_t *mask = p.mask ? p.mask + row * words : nullptr;
+    for (int t = r.c0 + threadIdx.x; t < r.c1; t += NT)
+      p.out[row * p.V + t] =
+          !mask || mask1(mask, t) ? r.rule(__ldcg(p.logits + row * p.V + t), t - r.c0, j) : -INFINITY;
+  }
+}
+
 constexpr int range_bytes(bool bias) { return CH * (bias ? 10 : 6); }
 
 }  // namespace
@@ -197,7 +209,7 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
   trace_start(kTkLogits);
   extern __shared__ __align__(128) unsigned char smem[];
   float *ring = reinterpret_cast<float *>(smem);  // [kRing][CH]
-  __shared__ int listed, drafts[8];
+  __shared__ int listed, drafts[8], stalled;
   __shared__ __align__(8) uint64_t full[kRing];
   const int tid = threadIdx.x, ranges = (p.V + CH - 1) / CH, words = (p.V + 31) / 32;
   Range r;
@@ -218,6 +230,7 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
   auto row_lead = [&](int j) { return min(n, (int)((4u - ((off0 + j * offv) & 3u)) & 3u)); };
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) mbar_init(&full[s], 1);
+    stalled = p.k + 1;
     fence_barrier_init();
   }
   grid_dep_wait();
@@ -247,9 +260,8 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
   r.build(p);
 
   const int n_list = listed;
-  bool ok = true;  // this thread's waits have all ended
-  int j = j0;
-  for (; j < j1; ++j) {
+  int missed = j1;  // the first row whose load this thread has given up on
+  for (int j = j0; j < j1; ++j) {
     const int lead = row_lead(j), nv = (n - lead) / 4, s = (j - j0) % kRing;
     float *row = ring + s * CH;
     const uint32_t *mask = p.mask ? p.mask + ((size_t)r.b * (p.k + 1) + j) * words : nullptr;
@@ -257,8 +269,11 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
 #pragma unroll
     for (int u = 0; u < VPT; ++u) m[u] = next_mask[u];
     if (p.mask && j + 1 < j1) fetch_mask(j + 1);
-    if (ok) ok = mbar_wait(&full[s], (uint32_t)((j - j0) / kRing) & 1u, nullptr);
-    for (int i = tid; ok && i < n_list; i += NT) {
+    if (missed == j1 && !mbar_wait(&full[s], (uint32_t)((j - j0) / kRing) & 1u, nullptr)) {
+      missed = j;
+      atomicMin(&stalled, j);
+    }
+    for (int i = tid; i < n_list; i += NT) {
       const int o = r.list[i], at = o - lead;
       if (at >= 0 && at < 4 * nv) row[at] = r.rule(row[at], o, j);
     }
@@ -266,7 +281,7 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
       if (n_list) __syncthreads();
 #pragma unroll
       for (int u = 0; u < VPT; ++u)
-        if (ok && tid + u * NT < nv) cover_shared(row + 4 * (tid + u * NT), m[u]);
+        if (tid + u * NT < nv) cover_shared(row + 4 * (tid + u * NT), m[u]);
     }
     // the tokens before the first vector and behind the last
     const int tail = lead + 4 * nv, singles = lead + (n - tail);
@@ -276,8 +291,8 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
           !mask || mask1(mask, r.c0 + o) ? r.rule(__ldcg(p.logits + row_base(j) + o), o, j) : -INFINITY;
     }
     fence_proxy_async_smem();
-    if (!__syncthreads_and(ok)) break;
-    if (tid == 0) {
+    __syncthreads();
+    if (tid == 0 && missed == j1) {
       if (nv) bulk_s2g(p.out + row_base(j) + lead, row, (uint32_t)nv * 16u);
       bulk_commit();
       // the row kRing ahead takes this row's place once the copy out has read it
@@ -287,20 +302,17 @@ __global__ void __launch_bounds__(NT) adjust_logits_kernel(const __grid_constant
       }
     }
   }
-  // A row whose load did not land within the wait limit is not taken from the ring,
-  // nor is any after it: they are read from the logits by plain loads.  What was
-  // brought for them has the limit once more to land before the CTA exits.
-  if (j < j1) {
-    if (tid == 0)
-      for (int i = j; i < j1 && i < j + kRing; ++i) mbar_wait(&full[(i - j0) % kRing], (uint32_t)((i - j0) / kRing) & 1u, nullptr);
-    for (; j < j1; ++j) {
-      const uint32_t *mask = p.mask ? p.mask + ((size_t)r.b * (p.k + 1) + j) * words : nullptr;
-      for (int o = tid; o < n; o += NT)
-        p.out[row_base(j) + o] =
-            !mask || mask1(mask, r.c0 + o) ? r.rule(__ldcg(p.logits + row_base(j) + o), o, j) : -INFINITY;
-    }
-  }
   if (tid == 0) bulk_wait_all();
+  // A load that did not land within the wait limit: the rows from there on may have
+  // been copied out as they were, and are written again.  What thread 0 has brought
+  // since has the limit once more to land before the CTA exits.
+  if (const int from = stalled; from < j1) {
+    if (tid == 0)
+      for (int j = missed; j < j1 && j < missed + kRing; ++j)
+        mbar_wait(&full[(j - j0) % kRing], (uint32_t)((j - j0) / kRing) & 1u, nullptr);
+    __syncthreads();
+    plain_rows(p, r, from, j1);
+  }
   trace_end(kTkLogits);
 }
 
