@@ -75,6 +75,7 @@ class DraftModule:
             wd["E"] = self.weights["E"]
             self.extra.append(wd)
         self.mods = None
+        self.ws_paged = None
         self.dims = bd.make_dims(w.B, w.d, w.Hq, w.Hkv, w.Dh, w.F, w.V, w.ctx_max + self.k, w.eps)
         self.wptr = bd.make_weights(self.weights)
         # outputs and workspace inside canary bands (check_canaries)
@@ -167,7 +168,9 @@ class DraftModule:
                            self.ws_paged, self.window, self.sinks, stream)
 
     def status(self, stream=None):
-        return bd.get_status(self.ws, stream)
+        """MTP_STATUS_* bits of the calls since the workspaces were cleared, paged ones included."""
+        bits = bd.get_status(self.ws, stream)
+        return bits | bd.get_status(self.ws_paged, stream) if self.ws_paged is not None else bits
 
     def check_canaries(self):
         """Raise if any call wrote outside an output or the workspace."""
