@@ -151,17 +151,26 @@ class DraftModule:
     def set_pages(self, k_pages, v_pages, page_table, rope=None, window=0, sinks=0):
         """Keep the K/V in pages from now on (draft_paged, step_paged): pools
         [n_pages, Hkv, page, Dh] bf16 and page_table [B, max_pages] int32 on the
-        device; rope from bd.make_rope."""
+        device; rope from bd.make_rope.  One module alone: the paged chain has one
+        module's weights and pools."""
+        if self.extra:
+            raise ValueError("the paged chain runs one module: extra_modules have no pages")
         self.cache = bd.make_paged_cache(k_pages, v_pages, page_table)
         self.rope, self.window, self.sinks = rope, window, sinks
         self.ws_paged = self.guard.alloc("paged workspace", bd.paged_workspace_size(self.dims, self.k), torch.uint8)
 
+    def _need_pages(self):
+        if self.ws_paged is None:
+            raise ValueError("set_pages comes first")
+
     def draft_paged(self, T, mode, u_draft=None, logits=True, stream=None):
+        self._need_pages()
         bd.mtp_draft_paged(self.dims, self.wptr, self.cache, self.rope, self.h, self.last_tok, self.ctx_len, self.k, T,
                            mode, u_draft, self.draft_tok, self.draft_logits if logits else None, self.ws_paged,
                            self.window, self.sinks, stream)
 
     def step_paged(self, T, mode, target_logits, u_draft=None, u_accept=None, u_final=None, logits=True, stream=None):
+        self._need_pages()
         bd.spec_step_paged(self.dims, self.wptr, self.cache, self.rope, self.h, self.last_tok, self.ctx_len, self.k, T,
                            mode, u_draft, target_logits, u_accept, u_final, self.draft_tok,
                            self.draft_logits if logits else None, self.out_tok, self.accept_len, self.num_accepted,

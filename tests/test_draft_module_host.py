@@ -21,3 +21,18 @@ def test_status_covers_both_workspaces(module, monkeypatch, bits):
     assert module.status() == bits.get("contiguous", 0)          # no pages yet
     module.ws_paged = "paged"
     assert module.status() == bits.get("contiguous", 0) | bits.get("paged", 0)
+
+
+def test_pages_are_refused_to_a_module_per_depth(module, monkeypatch):
+    """The paged chain would run the first module at every depth."""
+    def fail(*a, **k):
+        raise AssertionError("reached the library")
+    for name in ("make_paged_cache", "paged_workspace_size", "mtp_draft_paged", "spec_step_paged"):
+        monkeypatch.setattr(bd, name, fail)
+    module.extra = [{"E": None}]
+    with pytest.raises(ValueError, match="one module"):
+        module.set_pages(None, None, None)
+    assert module.ws_paged is None
+    for call in (lambda: module.draft_paged(1.0, 0), lambda: module.step_paged(1.0, 0, None)):
+        with pytest.raises(ValueError, match="set_pages"):
+            call()
