@@ -157,7 +157,8 @@ class DraftModule:
             raise ValueError("the paged chain runs one module: extra_modules have no pages")
         self.cache = bd.make_paged_cache(k_pages, v_pages, page_table)
         self.rope, self.window, self.sinks = rope, window, sinks
-        self.ws_paged = self.guard.alloc("paged workspace", bd.paged_workspace_size(self.dims, self.k), torch.uint8)
+        if self.ws_paged is None:  # its size does not go by the pages
+            self.ws_paged = self.guard.alloc("paged workspace", bd.paged_workspace_size(self.dims, self.k), torch.uint8)
 
     def _need_pages(self):
         if self.ws_paged is None:

@@ -36,3 +36,20 @@ def test_pages_are_refused_to_a_module_per_depth(module, monkeypatch):
     for call in (lambda: module.draft_paged(1.0, 0), lambda: module.step_paged(1.0, 0, None)):
         with pytest.raises(ValueError, match="set_pages"):
             call()
+
+
+def test_new_pages_keep_the_workspace(module, monkeypatch):
+    """A program that grows its page table calls set_pages again and again."""
+    class Guard:
+        made = 0
+
+        def alloc(self, name, numel, dtype):
+            self.made += 1
+            return (name, numel)
+    monkeypatch.setattr(bd, "make_paged_cache", lambda *pools: pools)
+    monkeypatch.setattr(bd, "paged_workspace_size", lambda dims, k: 1024)
+    module.dims, module.k, module.guard = None, 3, Guard()
+    for table in ("small", "larger"):
+        module.set_pages("k", "v", table, window=7, sinks=1)
+        assert module.cache == ("k", "v", table) and module.ws_paged == ("paged workspace", 1024)
+    assert module.guard.made == 1
