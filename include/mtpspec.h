@@ -492,7 +492,8 @@ int mtp_cache_append(const MtpPagedCache *cache, const MtpRope *rope, int B, int
  *   out       bf16 rows of Hq*Dh, ldo elements apart; must not overlap q
  *   lse       [n_rows, Hq] fp32, or NULL: ln sum_j exp(scale q.k_j)
  *   ws        mtp_paged_attn_workspace_size() bytes, 256-byte aligned
- * A row that sees no key (a ctx_len past the cache) gets zeros and lse -inf.
+ * A row that sees no key (a window that lies past the cache) gets zeros and lse -inf;
+ * one that sees a NaN score, or a score of +inf, gets NaN in both.
  * Scores, softmax statistics and output sums are fp32; the softmax weights are
  * rounded to bf16 for their product with V.  What no row of a sequence sees may
  * hold anything, NaN included; a V row that one of its rows sees has to be

@@ -326,6 +326,14 @@ __device__ __forceinline__ int paged_page(const PagedArgs &p, int b, int j) {
   return id;
 }
 
+// A row's normalisation and log-sum from its sum S of weights over 2^M: zeros and -inf
+// for a row that saw no key.  A NaN that it saw is in S and stays one in both: -inf
+// would tell a caller who joins pieces by their log-sums to leave the piece out.
+__device__ __forceinline__ float paged_inverse(float S) { return S == 0.f ? 0.f : 1.f / S; }
+__device__ __forceinline__ float paged_lse(float M, float S) {
+  return S == 0.f ? -INFINITY : (M + log2f(S)) * 0.6931471805599453f;
+}
+
 // Host side.
 
 // A 2-D map over a pool of K or V pages as [rows, Dh] bf16, boxes of box_rows

@@ -348,11 +348,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         x[0] = f;  // from here on the group's weight
       }
       rowm[r] = M;
-      rowl[r] = S > 0.f ? 1.f / S : 0.f;
+      rowl[r] = paged_inverse(S);
       if (whole_item) {
         if (p.lse)
-          p.lse[(size_t)(row0 + r / p.G) * p.Hq + w.h * p.G + r % p.G] =
-              S > 0.f ? (M + log2f(S)) * 0.6931471805599453f : -INFINITY;
+          p.lse[(size_t)(row0 + r / p.G) * p.Hq + w.h * p.G + r % p.G] = paged_lse(M, S);
       } else {
         float *x = p.part_ml + (((size_t)blockIdx.x * 2 + slot) * RB + r) * 2;
         x[0] = M;
@@ -481,7 +480,7 @@ __global__ void __launch_bounds__(32 * kCombineRows)
         }
       }
     }
-    const float inv = S > 0.f ? 1.f / S : 0.f;
+    const float inv = paged_inverse(S);
     const int row = d.row0 + r / p.G, hq = d.h * p.G + r % p.G;
     const long long off = (long long)row * p.ldo + hq * DH + lane * PER;
     if (in_bounds(row < p.n_rows, p.status)) {
@@ -490,8 +489,7 @@ __global__ void __launch_bounds__(32 * kCombineRows)
         if (p.out_f32) static_cast<float *>(p.out)[off + e] = a[e] * inv;
         else static_cast<__nv_bfloat16 *>(p.out)[off + e] = __float2bfloat16_rn(a[e] * inv);
       }
-      if (lane == 0 && p.lse)
-        p.lse[(size_t)row * p.Hq + hq] = S > 0.f ? (M + log2f(S)) * 0.6931471805599453f : -INFINITY;
+      if (lane == 0 && p.lse) p.lse[(size_t)row * p.Hq + hq] = paged_lse(M, S);
     }
   }
   trace_end(kTkPagedCombine);
@@ -638,7 +636,7 @@ __global__ void __launch_bounds__(kCombineThreads, 6)
       }
       __syncthreads();
     }
-    const float inv = S > 0.f ? 1.f / S : 0.f;
+    const float inv = paged_inverse(S);
     const int row = d.row0 + r / p.G, hq = d.h * p.G + r % p.G;
     const long long at = (long long)row * p.ldo + hq * DH + lane * PER;
     if (mine && q == 0 && in_bounds(row < p.n_rows, p.status)) {
@@ -647,8 +645,7 @@ __global__ void __launch_bounds__(kCombineThreads, 6)
         if (p.out_f32) static_cast<float *>(p.out)[at + e] = a[e] * inv;
         else static_cast<__nv_bfloat16 *>(p.out)[at + e] = __float2bfloat16_rn(a[e] * inv);
       }
-      if (lane == 0 && p.lse)
-        p.lse[(size_t)row * p.Hq + hq] = S > 0.f ? (M + log2f(S)) * 0.6931471805599453f : -INFINITY;
+      if (lane == 0 && p.lse) p.lse[(size_t)row * p.Hq + hq] = paged_lse(M, S);
     }
   }
   trace_end(kTkPagedCombine);

@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
       const int slot = w.starts() ? 1 : 0;
       const int qrow = w.s.row0 + tok, hq = w.h * p.G + row % p.G;
       const bool mine = live && in_bounds(qrow < p.n_rows, p.status);
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = paged_inverse(l);
       const size_t pr = ((size_t)blockIdx.x * 2 + slot) * kPagedTcRows + g * rpg + row;
       // not unrolled: run once a segment, the code comes from memory each time
 #pragma unroll 1
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
           p.part_ml[pr * 2] = m;
           p.part_ml[pr * 2 + 1] = l;
         } else if (p.lse) {
-          p.lse[(size_t)qrow * p.Hq + hq] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          p.lse[(size_t)qrow * p.Hq + hq] = paged_lse(m, l);
         }
       }
       if (tid == 0 && w.starts() && !w.ends()) {

@@ -105,3 +105,59 @@ def test_a_paged_draft_at_no_position_writes_nothing(bad):
     m.check_canaries()
     for pool, x in zip(m.cache.tensors[:2], was):
         assert torch.equal(pool.view(torch.int16), x.view(torch.int16))
+
+
+def attended(d, max_rows):
+    from mtp_speculative_decoding_draft_gb300 import binding as bd
+    n, Hq = d["n_rows"], d["Hq"]
+    out, lse = torch.zeros_like(d["q"]), torch.zeros(n, Hq, device="cuda")
+    ws = bd.alloc_workspace(bd.paged_attn_workspace_size(d["B"], n, max_rows, Hq, d["Hkv"], d["Dh"]))
+    bd.mtp_paged_attn(bd.make_paged_cache(d["k_pages"], d["v_pages"], d["table"]), d["row_start"], d["ctx_len"], d["q"], out, lse,
+                      ws, max_rows=max_rows)
+    torch.cuda.synchronize()
+    assert bd.get_status(ws) == 0
+    return out, lse
+
+
+@pytest.mark.parametrize("ctx", [20, 3000])                    # one share, and states that are joined
+@pytest.mark.parametrize("Dh,max_rows", [(32, 0), (64, 0), (128, 0), (64, 3), (128, 3)])
+def test_a_nan_in_sight_is_a_nan_in_lse(Dh, max_rows, ctx):
+    """A NaN score leaves the row's sum without a value: lse says so, as the output
+    does, and not that the row saw no key.  Every other row keeps its value."""
+    d = make_case([40, 2], [ctx, 7], 8, 2, Dh, 32, seed=Dh)
+    good, good_lse = attended(d, max_rows)
+    check_attend(d, good, good_lse)
+    # query head 1 of row 3; the key at position ctx + 30, which rows 30 .. 39 of kv head 1 see
+    clean = d["q"].clone()
+    d["q"][3, 1, 5] = float("nan")
+    pos = ctx + 30
+    d["k_pages"][int(d["table"][0, pos // 32]), 1, pos % 32, 9] = float("nan")
+    out, lse = attended(d, max_rows)
+    hit = torch.zeros(d["n_rows"], 8, dtype=torch.bool, device="cuda")
+    hit[3, 1] = True
+    hit[30:40, 4:] = True
+    assert torch.isnan(lse[hit]).all() and torch.isnan(out[hit]).all()
+    # the rest within the definition's bounds (a row's maximum may move with its warp's)
+    check_attend(dict(d, q=clean), torch.where(hit[..., None], good, out), torch.where(hit, good_lse, lse))
+
+
+@pytest.mark.parametrize("max_rows", [0, 3])
+def test_infinite_scores(max_rows):
+    """A key of score +inf: weight inf / inf, no value.  One of -inf: weight zero."""
+    d = make_case([40], [200], 4, 1, 64, 32, seed=2)
+    good, good_lse = attended(d, max_rows)
+    q = d["q"]
+    q.abs_()
+    d["k_pages"][int(d["table"][0, 0]), 0, 4, :] = float("-inf")
+    out, lse = attended(d, max_rows)
+    k, v = d["seqs"][0]
+    k[4] = float("-inf")
+    assert torch.isfinite(out).all()
+    s = (q.double().cpu().permute(1, 0, 2) @ k.double().permute(1, 2, 0)) / 8
+    s = s.masked_fill(torch.arange(240)[None, None] > torch.arange(200, 240)[None, :, None], float("-inf"))
+    ref = torch.logsumexp(s, dim=-1).T
+    # the score's fp32 products, as in check_attend, of |q| |k| below 64 * 5 * 5 / 8
+    assert ((lse.double().cpu() - ref).abs() <= 200 * 68 * 2.0 ** -24 + 2.0 ** -19 + 2.0 ** -22 * ref.abs()).all()
+    d["k_pages"][int(d["table"][0, 0]), 0, 4, :] = float("inf")
+    out, lse = attended(d, max_rows)
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
