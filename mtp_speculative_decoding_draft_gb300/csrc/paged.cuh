@@ -44,7 +44,7 @@ struct PagedArgs {
   const uint16_t *q;      // bf16 rows of Hq * Dh, ldq elements apart
   long long ldq, ldo;
   void *out;              // bf16 (or fp32) rows, ldo elements apart
-  int out_f32;
+  int out_f32;            // (streaming kernel only)
   float *lse;             // [n_rows, Hq] or null
   float scale_log2;       // softmax scale * log2(e)
   int window, sinks;      // window 0: every earlier key

@@ -641,10 +641,7 @@ __global__ void __launch_bounds__(kCombineThreads, 6)
     const long long at = (long long)row * p.ldo + hq * DH + lane * PER;
     if (mine && q == 0 && in_bounds(row < p.n_rows, p.status)) {
 #pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        if (p.out_f32) static_cast<float *>(p.out)[at + e] = a[e] * inv;
-        else static_cast<__nv_bfloat16 *>(p.out)[at + e] = __float2bfloat16_rn(a[e] * inv);
-      }
+      for (int e = 0; e < PER; ++e) static_cast<__nv_bfloat16 *>(p.out)[at + e] = __float2bfloat16_rn(a[e] * inv);
       if (lane == 0 && p.lse) p.lse[(size_t)row * p.Hq + hq] = paged_lse(M, S);
     }
   }
@@ -759,6 +756,7 @@ cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const 
   char *base = static_cast<char *>(scratch);
   cudaError_t e;
   if (wants_tc(packed, args.Dh)) {
+    if (args.out_f32) return cudaErrorInvalidValue;  // the draft's, whose rows all fit a streaming block
     PagedTcParams tp;
     tp.a = args;
     tp.a.tpb = 2 * (128 / args.G);

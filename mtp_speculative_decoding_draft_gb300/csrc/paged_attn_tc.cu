@@ -713,18 +713,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
         tmem_wait_ld();
         pin32(o);
         // O of a row without keys was multiplied by zero weights only: still zero
-        if (!whole_item || p.out_f32) {
-          float *d = whole_item ? static_cast<float *>(p.out) + (long long)qrow * p.ldo + hq * DH + 32 * c
-                                : p.part_o + pr * DH + 32 * c;
-          const float f = whole_item ? inv : 1.f;
+        if (!whole_item) {
           uint4 v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            v[e] = make_uint4(__float_as_uint(__uint_as_float(o[4 * e]) * f),
-                              __float_as_uint(__uint_as_float(o[4 * e + 1]) * f),
-                              __float_as_uint(__uint_as_float(o[4 * e + 2]) * f),
-                              __float_as_uint(__uint_as_float(o[4 * e + 3]) * f));
-          store_quads<8>(v, mine ? d : nullptr, lane);
+          for (int e = 0; e < 8; ++e) v[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          store_quads<8>(v, mine ? p.part_o + pr * DH + 32 * c : nullptr, lane);
         } else {
           uint16_t *d = static_cast<uint16_t *>(p.out) + (long long)qrow * p.ldo + hq * DH + 32 * c;
           uint4 v[4];

@@ -35,3 +35,24 @@ def test_a_copy_that_never_lands_changes_no_logit(V, kw):
     bd.spec_adjust_logits(B, k, V, rules, logits, drafts, out)
     torch.cuda.synchronize()
     check_logits(out, ref, mag)
+
+
+@pytest.mark.parametrize("V", [30004, 30001])
+@pytest.mark.parametrize("kw", [dict(), dict(penalties=False, bias=0), dict(bias=70, hist=300)])
+def test_nine_rows_of_one_block_under_a_mask(V, kw):
+    """Enough ranges that a block takes all rows of its range: the ring of rows in shared
+    memory goes round four times and a half, with the rows on 16-byte boundaries or not."""
+    from mtp_speculative_decoding_draft_gb300 import binding as bd
+    B, k = 24, 8
+    assert B * ((V + 2047) // 2048) >= 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    logits, drafts, r = rules_case(B, k, V, seed=V, **kw)
+    out = torch.zeros_like(logits)
+    bd.spec_adjust_logits(B, k, V, bd.make_logit_rules(**r), logits, drafts, out)
+    torch.cuda.synchronize()
+    pick = [0, 11, B - 1]
+    sub = {n: None if t is None else t[pick] for n, t in r.items()}
+    ref, mag = logits_reference(logits[pick], drafts[pick], V, **sub)
+    check_logits(out[pick], ref, mag)
+    # the rules in place, on the same rows
+    bd.spec_adjust_logits(B, k, V, bd.make_logit_rules(**r), logits, drafts, logits)
+    assert torch.equal(logits, out)

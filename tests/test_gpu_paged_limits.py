@@ -161,3 +161,19 @@ def test_infinite_scores(max_rows):
     d["k_pages"][int(d["table"][0, 0]), 0, 4, :] = float("inf")
     out, lse = attended(d, max_rows)
     assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("B", [513, 600, 1024, 1025, 1100])
+@pytest.mark.parametrize("Hq,Hkv,Dh", [(4, 2, 64), (8, 1, 128)])
+def test_large_batches_on_the_tensor_cores(B, Hq, Hkv, Dh):
+    """More sequences than the plan's one block has threads, and than it keeps the
+    blocks of in shared memory; empty ones first, last and between; two chunks."""
+    rows = [(b * 7) % 4 for b in range(B)]
+    ctx = [(b * 37) % 91 for b in range(B)]
+    rows[0] = rows[1] = rows[-1] = rows[-2] = 0
+    rows[B // 2], rows[min(B - 3, 512)] = 150, 90
+    d = make_case(rows, ctx, Hq, Hkv, Dh, 16, seed=B, pad=3)
+    out, lse = attended(d, 0)
+    check_attend(d, out, lse)
+    n = sum(rows)
+    assert (out[n:] == 0).all() and (lse[n:] == 0).all()
