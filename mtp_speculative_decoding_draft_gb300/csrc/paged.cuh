@@ -60,24 +60,21 @@ struct PagedSeq {
   int row0, n, ctx;
 };
 
-// Sequence b's rows and context, clamped to the buffers; flags what was out of range.
-__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs &p, int b, bool flag) {
+// Sequence b's rows and context, clamped to the buffers; flags what was out of range, and
+// sets *back if the rows end before they start.
+__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs &p, int b, bool flag, bool *back = nullptr) {
   const int a = p.row_start ? __ldcg(&p.row_start[b]) : b, e = p.row_start ? __ldcg(&p.row_start[b + 1]) : b + 1;
-  const long long c = (long long)__ldcg(&p.ctx_len[b]) + p.ctx_add;
+  const int c = min(__ldcg(&p.ctx_len[b]), 0x7fffffff - p.ctx_add) + p.ctx_add;  // past the cache either way
   PagedSeq s;
   s.row0 = min(max(a, 0), p.n_rows);
   s.n = min(max(e, s.row0), p.n_rows) - s.row0;
-  s.ctx = (int)min(max(c, 0ll), (long long)p.cap);
+  s.ctx = min(max(c, 0), p.cap);
+  if (back) *back |= e < a;
   if (flag) {
     if (s.row0 != a || s.row0 + s.n != e) set_status(p.status, kStatusBadRows);
     if (s.ctx != c || (long long)s.ctx + s.n > p.cap) set_status(p.status, kStatusBadCtx);
   }
   return s;
-}
-
-// Sequence b's rows end before they start.
-__device__ __forceinline__ bool paged_back(const PagedArgs &p, int b) {
-  return p.row_start && __ldcg(&p.row_start[b + 1]) < __ldcg(&p.row_start[b]);
 }
 
 // Keys that some row of tokens [t0, t1) sees: [0, sink_end) and [lo, hi); in
@@ -161,7 +158,7 @@ __device__ PagedShare paged_plan(const PagedArgs &p, long long *scratch) {
   bool back = false;
   for (int b = tid; b < p.B; b += NT) {
     long long u;
-    const PagedSeq s = paged_seq(p, b, blockIdx.x == 0);
+    const PagedSeq s = paged_seq(p, b, blockIdx.x == 0, &back);
     const long long c = paged_cost<TK>(p, s, &u);
     if (b < NT) {
       first_s = s;
@@ -170,7 +167,6 @@ __device__ PagedShare paged_plan(const PagedArgs &p, long long *scratch) {
     }
     mine += c * p.Hkv;
     mine_u += u * p.Hkv;
-    back |= paged_back(p, b);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {

@@ -317,10 +317,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     long long c = 0, u;
     int nb = 0;
     if (b < p.B) {
-      const PagedSeq s = paged_seq(p, b, true);
+      const PagedSeq s = paged_seq(p, b, true, &back);
       c = paged_cost<kTK>(p, s, &u);
       nb = paged_blocks(p, s.n);
-      back |= paged_back(p, b);
     }
     const long long sum = block_scan(nb, &incl, scratch);
     if (b < p.B) {
