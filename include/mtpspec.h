@@ -494,10 +494,11 @@ int mtp_cache_append(const MtpPagedCache *cache, const MtpRope *rope, int B, int
  *   ws        mtp_paged_attn_workspace_size() bytes, 256-byte aligned
  * A row that sees no key (a window that lies past the cache) gets zeros and lse -inf;
  * one that sees a NaN score, or a score of +inf, gets NaN in both.
- * Scores, softmax statistics and output sums are fp32; the softmax weights are
- * rounded to bf16 for their product with V.  What no row of a sequence sees may
- * hold anything, NaN included; a V row that one of its rows sees has to be
- * finite.  Results are the same bit for bit from run to run.
+ * Scores, softmax statistics and output sums are fp32; for their product with V the
+ * softmax weights are carried in 16 bits where no sequence has more than 16 packed
+ * rows (rows x Hq/Hkv; as far as n_rows and max_rows tell), else rounded to bf16.
+ * What no row of a sequence sees may hold anything, NaN included; a V row that one of
+ * its rows sees has to be finite.  Results are the same bit for bit from run to run.
  */
 size_t mtp_paged_attn_workspace_size(int B, int n_rows, int max_rows, int Hq, int Hkv, int Dh);
 int mtp_paged_attn(const MtpPagedCache *cache, int B, int Hq, int n_rows, int max_rows,
@@ -554,7 +555,7 @@ int spec_adjust_logits(int B, int k, int V, const MtpLogitRules *rules, const fl
  *   rope, window, sinks  as above (NULL, 0, 0: mtp_draft's block)
  *   ws     mtp_paged_workspace_size(dims, k) bytes, zero before its first use
  * Everything else is as for mtp_draft / spec_step.  Queries are rounded to bf16
- * after the rotation, keys once more, and the softmax weights to bf16 (mtp_draft
+ * after the rotation, keys once more, and the softmax weights to 16 bits (mtp_draft
  * keeps fp32 there): its tolerance on the logits holds all the same.
  */
 size_t mtp_paged_workspace_size(const MtpDims *dims, int k);

@@ -13,8 +13,15 @@
 //   online softmax on the accumulator fragments, base 2; the running maximum
 //               moves only when a row's maximum grew by more than 2^8, so the
 //               accumulators are seldom rescaled
-//   O += P V    P rounded to bf16, as a product's operand has to be; the
-//               row's sum takes the unrounded values in fp32
+//   O += P V    with P in bf16, as an operand beside bf16 values has to be; the
+//               row's sum takes the unrounded weights in fp32.  Blocks of 16
+//               packed rows, whose matrix pipe waits for bytes, carry P in two
+//               terms, what the first rounding left as a second operand (2^-16 of
+//               a weight is lost, not 2^-8): 64 x 4 rows over 1024-8192 keys 198.3
+//               -> 199.8 us, 4 rows over 4096 13.3 -> 13.7, and outputs as far from
+//               64 bits as their own rounding (0.0017 against 0.0023 in all).
+//               Wider blocks keep one term: a second costs 32 x 30 rows over 16384
+//               3.5%, blocks of 64 rows 13%
 // Warps split a tile by rows (16 each) and what is left of them by keys, and
 // merge through shared memory at the end of a segment.  Two CTAs an SM, 96 KB of
 // tiles in flight each: 32 sequences of 6 rows over 16384 keys run at 6.6 TB/s,
@@ -38,6 +45,7 @@ struct Lay {
   static constexpr int RB = 16 * RG;                   // packed query rows of a block
   static constexpr int KG = kCW / RG;                  // key groups
   static constexpr int KW = kTK / KG;                  // keys of a warp per tile
+  static constexpr int TERMS = RG == 1 ? 2 : 1;        // bf16 terms of a weight
   static constexpr int NB = DH >= 64 ? DH / 64 : 1;    // boxes across a head
   static constexpr int PITCH = DH >= 64 ? 128 : 64;    // bytes of a row in a box
   static constexpr int BOX = kTK * PITCH;
@@ -98,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   trace_start(kTkPagedAttn);
   using L = Lay<DH, RG>;
   constexpr int RB = L::RB, NB = L::NB, KS = DH / 16, ND = DH / 8, NT = L::KW / 8;
+  constexpr int VX = L::TERMS;  // V fragments in hand: the terms' products of one accumulator lie 2 VX apart
   const PagedArgs &p = sp.a;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char *ring = smem;
@@ -277,15 +286,20 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           }
         }
         const float u0 = m[0] == -INFINITY ? 0.f : m[0], u1 = m[1] == -INFINITY ? 0.f : m[1];
-        uint32_t pa[NT / 2][4];
+        uint32_t pa[NT / 2][4], pr[NT / 2][4];  // bf16 weights, and with two terms what the rounding left of them
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float a = ex2_approx(sc[nt][0] - u0), b = ex2_approx(sc[nt][1] - u0);
           const float c = ex2_approx(sc[nt][2] - u1), d = ex2_approx(sc[nt][3] - u1);
           l[0] += a + b;  // this lane's columns; the quad's sums meet at the end
           l[1] += c + d;
-          pa[nt >> 1][2 * (nt & 1)] = pack2(a, b);
-          pa[nt >> 1][2 * (nt & 1) + 1] = pack2(c, d);
+          const uint32_t ab = pack2(a, b), cd = pack2(c, d);
+          pa[nt >> 1][2 * (nt & 1)] = ab;
+          pa[nt >> 1][2 * (nt & 1) + 1] = cd;
+          if (L::TERMS == 2) {
+            pr[nt >> 1][2 * (nt & 1)] = pack2(a - bf16_lo(ab), b - bf16_hi(ab));
+            pr[nt >> 1][2 * (nt & 1) + 1] = pack2(c - bf16_lo(cd), d - bf16_hi(cd));
+          }
         }
         // ---- O += P V.  Rows of V that no row of the block sees (past the
         // last key, before the window, never loaded) may hold anything, NaN
@@ -299,17 +313,23 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
             z1 = (w.r.sees(j + 8) ? 0xffffu : 0u) | (w.r.sees(j + 9) ? 0xffff0000u : 0u);
           }
 #pragma unroll
-          for (int n = 0; n < ND; n += 2) {
-            uint32_t v[4];
-            ldsm4t(vb + at<DH>(R0 + 16 * kk + (lane & 7) + 8 * ((lane >> 3) & 1), n + (lane >> 4), kTK), v);
-            if (!whole) {
-              v[0] &= z0;
-              v[1] &= z1;
-              v[2] &= z0;
-              v[3] &= z1;
+          for (int n = 0; n < ND; n += 2 * VX) {
+            uint32_t v[VX][4];
+#pragma unroll
+            for (int x = 0; x < VX; ++x) {
+              ldsm4t(vb + at<DH>(R0 + 16 * kk + (lane & 7) + 8 * ((lane >> 3) & 1), n + 2 * x + (lane >> 4), kTK), v[x]);
+              if (!whole) {
+                v[x][0] &= z0;
+                v[x][1] &= z1;
+                v[x][2] &= z0;
+                v[x][3] &= z1;
+              }
             }
-            mma(o[n], pa[kk], v[0], v[1]);
-            mma(o[n + 1], pa[kk], v[2], v[3]);
+#pragma unroll
+            for (int x = 0; x < 2 * VX; ++x) mma(o[n + x], pa[kk], v[x >> 1][2 * (x & 1)], v[x >> 1][2 * (x & 1) + 1]);
+            if (L::TERMS == 2)
+#pragma unroll
+              for (int x = 0; x < 2 * VX; ++x) mma(o[n + x], pr[kk], v[x >> 1][2 * (x & 1)], v[x >> 1][2 * (x & 1) + 1]);
           }
         }
       }

@@ -8,7 +8,9 @@
 // the other group's products:
 //   S_g = Q_g K_i^T     tcgen05.mma, both operands in shared memory by TMA
 //   P_g = 2^(S_g - m)   one thread a row: S from tensor memory, the maximum and
-//                       the sum in registers, P back over S as bf16
+//                       the sum in registers, P back over S as bf16 (the sum takes
+//                       the unrounded weights; a second term would be a third
+//                       product where the first two are the bound: half as much again)
 //   O_g += P_g V_i      tcgen05.mma, P from tensor memory, V as it lies in its
 //                       pages (row-major keys: the MN-major form of operand B)
 // S_g i+1 is issued behind O_g += P_g V_i, so when a group's scores arrive its

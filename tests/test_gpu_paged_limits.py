@@ -4,7 +4,7 @@ are flagged, and what the calls then leave alone."""
 import pytest
 import torch
 
-from paged_helpers import check_attend, make_case
+from paged_helpers import attend_reference, check_attend, make_case
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +177,24 @@ def test_large_batches_on_the_tensor_cores(B, Hq, Hkv, Dh):
     check_attend(d, out, lse)
     n = sum(rows)
     assert (out[n:] == 0).all() and (lse[n:] == 0).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,Dh,rows", [(32, 8, 128, 4), (8, 1, 64, 2), (10, 2, 128, 3), (4, 2, 32, 8), (8, 8, 64, 1)])
+@pytest.mark.parametrize("ctx,window", [(40, 0), (1000, 0), (9000, 0), (2000, 300)])
+def test_few_rows_carry_their_weights_in_16_bits(Hq, Hkv, Dh, rows, ctx, window):
+    """Up to 16 packed rows: a weight is a bf16 value and a second one that holds what the
+    first rounding left, at most 2^-8 of it; the second's own rounding is 2^-8 of that."""
+    d = make_case([rows, 1], [ctx, ctx // 3], Hq, Hkv, Dh, 32, seed=ctx + Dh, window=window, sinks=3 if window else 0)
+    from mtp_speculative_decoding_draft_gb300 import binding as bd
+    out = torch.zeros_like(d["q"])
+    ws = bd.alloc_workspace(bd.paged_attn_workspace_size(2, d["n_rows"], rows, Hq, Hkv, Dh))
+    bd.mtp_paged_attn(bd.make_paged_cache(d["k_pages"], d["v_pages"], d["table"]), d["row_start"], d["ctx_len"], d["q"], out, None,
+                      ws, window=window, sinks=d["sinks"], max_rows=rows)
+    torch.cuda.synchronize()
+    assert bd.get_status(ws) == 0
+    ref, _, spread, serr = attend_reference(d)
+    # the weights' two roundings, scores, exponentials (2^-21) and fp32 sums as in
+    # check_attend, and the output's own rounding (2^-8)
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -16 + 2 * serr[..., None] + 2.0 ** -18) * spread * (1 + 2.0 ** -8)
+    err = (out.double().cpu() - ref).abs()
+    assert (err <= tol).all(), float((err / tol).max())
