@@ -19,7 +19,7 @@
 // computes the row's rot/2 sines and cosines two a lane into its own corner of
 // shared memory, then rotates and stores.  Recomputing the sines for each unit of
 // a row costs less than a block-wide barrier a row: 8190 rows of 40 + 16 heads of
-// 128 took 96 us with a block a row, 45 us this way (5.2 TB/s, 77% of the copy
+// 128 took 96 us with a block a row, 43 us this way (5.45 TB/s, 80% of the copy
 // rate; what is left is the chain position -> page -> store of each warp).
 #include "internal.h"
 #include "paged.cuh"
@@ -260,11 +260,13 @@ cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t s, bool pdl) {
   // 16-byte accesses need the pairs' halves in whole vectors
   const bool wide = a.rot % 16 == 0;
   const int items = (a.Hq + 2 * a.Hkv) * a.Dh / (wide ? 16 : 8);
-  // few rows: an item a lane, more warps, the shortest chain
-  if ((long long)a.n_rows * items < 152ll * 2048)
+  // Few rows: an item a lane, more warps, the shortest chain; many rows: two items a
+  // lane at five blocks an SM.  In graphs of 20 calls (us, one item / two): 64 rows of
+  // 32 + 16 heads of 128 3.1 / 3.5, 256 rows 8.0 / 5.3, 1000 rows 19.2 / 12.1; 256 rows
+  // of 14 + 4 heads of 64 3.2 / 3.7, 1024 rows 6.6 / 4.7; 8190 rows of 40 + 16 heads of
+  // 128 63 / 43 (four items at three blocks 46, at five, spilling, 60).
+  if ((long long)a.n_rows * items < 152ll * 256)
     return wide ? launch_append<8, 1>(a, items, s, pdl) : launch_append<4, 1>(a, items, s, pdl);
-  // many rows: two items a lane at five blocks an SM (8190 rows of 40 + 16 heads of
-  // 128: 45 us; one item 64, four items at three blocks 46, at five, spilling, 60)
   return wide ? launch_append<8, 2>(a, items, s, pdl) : launch_append<4, 2>(a, items, s, pdl);
 }
 
