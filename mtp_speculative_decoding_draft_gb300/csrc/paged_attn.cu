@@ -5,7 +5,7 @@
 //
 // For the k + 1 candidate rows of a verification the work is bound by the
 // cache's bytes: every visible K/V row is read once, and the group's query
-// rows (tokens x G, up to 64 a block) share it.  Each CTA takes an equal share
+// rows (tokens x G, up to 64 a block; 32 with heads of 128) share it.  Each CTA takes an equal share
 // of the line of 64-key tiles (paged.cuh).  A producer warp brings the pages'
 // pieces of a tile by TMA into a three-stage ring; four compute warps hold
 // their rows' states in registers:
@@ -21,7 +21,7 @@
 //               -> 199.8 us, 4 rows over 4096 13.3 -> 13.7, and outputs as far from
 //               64 bits as their own rounding (0.0017 against 0.0023 in all).
 //               Wider blocks keep one term: a second costs 32 x 30 rows over 16384
-//               3.5%, blocks of 64 rows 13%
+//               3.5%, blocks of 64 rows of heads of 64 16%
 // Warps split a tile by rows (16 each) and what is left of them by keys, and
 // merge through shared memory at the end of a segment.  Two CTAs an SM, 96 KB of
 // tiles in flight each: 32 sequences of 6 rows over 16384 keys run at 6.6 TB/s,
@@ -673,7 +673,23 @@ __global__ void __launch_bounds__(kCombineThreads, 6)
 namespace {
 
 constexpr int kMaxSms = kPagedMaxCtas;
-constexpr int kStreamRows = 64;      // block rows of the widest streaming variant
+
+// Packed rows of the widest streaming block, and so of the largest sequence that the
+// streaming kernel takes where there is a tensor-core kernel (heads of 64 and 128).  In
+// graphs of 20 calls (us, streaming / tensor cores), 32 / 8 heads of 128:
+//   sequences x keys   16 rows      32 rows      36 rows      64 rows
+//   1 x 512             9.9 / 17.5  12.1 / 17.6  17.4 / 17.6  18.4 / 17.8
+//   8 x 512            11.3 / 21.4  14.0 / 21.7  20.2 / 22.4  21.9 / 22.4
+//   8 x 4096             33 / 41      41 / 42      61 / 42      66 / 43
+//   64 x 1024-8192      193 / 204    217 / 205    364 / 205    391 / 211
+// past 32 rows the streaming block of 64 rows has no registers left and its products
+// bind.  16 / 4 heads of 64:
+//   1 x 512             8.3 / 15.9   9.1 / 15.9  12.1 / 16.0  12.5 / 16.0
+//   8 x 4096           13.8 / 23.7  16.2 / 24.2  22.4 / 24.0  23.8 / 24.4
+//   64 x 1024-8192       58 / 79      69 / 79     105 / 79     112 / 83
+// where small batches would lose up to a third with the bound of heads of 128.  The
+// lengths are the device's, so that the host cannot tell the two apart.
+constexpr int stream_rows(int Dh) { return Dh == 128 ? 32 : 64; }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -714,8 +730,9 @@ cudaError_t launch_stream(const StreamParams &sp, int ctas, cudaStream_t s, bool
 template <int DH>
 cudaError_t launch_rows(const StreamParams &sp, int rb, int ctas, cudaStream_t s, bool pdl) {
   if (rb == 16) return launch_stream<DH, 1>(sp, ctas, s, pdl);
-  if (rb == 32) return launch_stream<DH, 2>(sp, ctas, s, pdl);
-  return launch_stream<DH, 4>(sp, ctas, s, pdl);
+  if constexpr (stream_rows(DH) == 64)
+    if (rb == 64) return launch_stream<DH, 4>(sp, ctas, s, pdl);
+  return launch_stream<DH, 2>(sp, ctas, s, pdl);
 }
 
 template <int DH>
@@ -736,7 +753,8 @@ template <int DH>
 cudaError_t set_head() {
   cudaError_t e = set_smem<DH, 1>();
   if (e == cudaSuccess) e = set_smem<DH, 2>();
-  if (e == cudaSuccess) e = set_smem<DH, 4>();
+  if constexpr (stream_rows(DH) == 64)
+    if (e == cudaSuccess) e = set_smem<DH, 4>();
   return e;
 }
 
@@ -756,15 +774,17 @@ static long long packed_rows(int n_rows, int max_rows, int G) {
 }
 
 // A call with a sequence of more packed rows than a streaming block holds goes to
-// the tensor cores whole: there a few rows cost a tile about what its bytes cost
-// (2300 cycles of one query group against 2800 of DRAM time for 128 keys of 128),
-// and one kernel takes any mixture.  Heads of 32 stay: their products are too thin.
-static bool wants_tc(long long packed, int Dh) { return packed > kStreamRows && Dh != 32; }
+// the tensor cores whole: one kernel takes any mixture.  Heads of 32, for which there is
+// no such kernel (its tiles are rows of 128 bytes), stay.  A call whose largest sequence
+// the host does not know (max_rows 0) is chosen for by all its rows: decoding batches
+// lose 7% with heads of 128 and up to 44% with heads of 64 that way (the 16-row columns
+// above), chunks taken for decoding would lose up to six times.
+static bool wants_tc(long long packed, int Dh) { return packed > stream_rows(Dh) && Dh != 32; }
 
 bool paged_attn_items_ok(int B, int Hkv, int n_rows, int G) { return paged_tc_items_ok(B, n_rows, G, Hkv); }
 
 size_t paged_attn_scratch_bytes(int B, int Hkv, int n_rows, int max_rows, int G, int Dh) {
-  if (!wants_tc(packed_rows(n_rows, max_rows, G), Dh)) return region_bytes(2 * kMaxSms, kStreamRows, Dh);
+  if (!wants_tc(packed_rows(n_rows, max_rows, G), Dh)) return region_bytes(2 * kMaxSms, stream_rows(Dh), Dh);
   return region_bytes(kMaxSms, kPagedTcRows, Dh) + paged_tc_plan_bytes(B, n_rows, G, Hkv);
 }
 
@@ -799,7 +819,9 @@ cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const 
   sp.a = args;
   const int rb = packed <= 16 ? 16 : packed <= 32 ? 32 : 64, ctas = 2 * n;
   sp.a.tpb = rb / args.G;
-  // at 4096 keys of 8 heads: runs of 2 tiles 15.1 us a call, of 4 14.1, of 6 14.4
+  // runs of 2, 4, 6 and 8 tiles (us, 32 / 8 heads of 128, 4 rows): 1 x 512 keys 9.6, 10.3,
+  // 11.8, 11.8; 1 x 4096 14.2, 13.7, 14.1, 15.2; 1 x 8192 18.2, 16.3, 16.4, 17.8; 2 x 4096
+  // 16.3, 14.4, 15.5, 17.0; 8 x 1024 15.8, 15.8, 14.7, 14.7; 4 x 4096 and 1 x 16384 within 7%
   sp.a.min_tiles = 4;
   bind_region(sp.a, base, ctas, rb);
   const uint32_t box = (uint32_t)(args.page < kTK ? args.page : kTK);
