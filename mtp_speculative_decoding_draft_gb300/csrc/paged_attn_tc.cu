@@ -46,7 +46,10 @@ namespace {
 
 constexpr int kTK = 128;          // keys per tile
 constexpr int kThreads = 384;     // three warpgroups: the registers move between whole ones
-// tiles that a segment costs besides its own (4 x 2048 rows: 0 158 us, 4 145, 8 141)
+// Tiles that a segment costs besides its own, 0 / 3 / 6 / 12 (us): 4 x 2048 rows from
+// nothing 155-163 / 138-141 / 140-144 / 146-149, 24 x 512 over 3584 538 / 528 / 526 / 527, 16 x
+// 128 over 512 54 / 50 / 44 / 44, 40 rows over 8192 30.6 / 26.4 / 26.4 / 26.9; 24 ragged
+// chunks 312-317 with each
 constexpr int kItemCost = 6;
 constexpr int kProducer = 8, kIssuer = 9, kQuery = 10, kClear = 11;
 constexpr unsigned kFull = 0xffffffffu;
