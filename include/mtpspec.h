@@ -446,8 +446,10 @@ typedef struct {
  *   MTP_ROPE_SCALING_LINEAR  every frequency / factor (position interpolation)
  *   MTP_ROPE_SCALING_YARN    by parts (the YaRN paper): pairs that turn more than
  *       high_turns times over original_len positions keep their frequency, those
- *       below low_turns are divided by factor, linear in between; *scale =
- *       0.1 ln(factor) + 1, else 1.
+ *       below low_turns are divided by factor, in between linear in the turns;
+ *       *scale = 0.1 ln(factor) + 1, else 1.  Programs that ramp linearly in the
+ *       pair's index t instead give other frequencies in the middle of the head: a
+ *       checkpoint served that way brings its own (mtp_rope_turns takes any).
  * low_turns, high_turns and original_len are read by YARN only.
  * mtp_rope_turns converts n frequencies (radians a position) to the table.
  */

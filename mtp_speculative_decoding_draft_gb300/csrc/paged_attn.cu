@@ -18,15 +18,15 @@
 //               packed rows, whose matrix pipe waits for bytes, carry P in two
 //               terms, what the first rounding left as a second operand (2^-16 of
 //               a weight is lost, not 2^-8): 64 x 4 rows over 1024-8192 keys 198.3
-//               -> 199.8 us, 4 rows over 4096 13.3 -> 13.7, and outputs as far from
+//               -> 199.8 us, 4 rows over 4096 13.3 -> 13.6, and outputs as far from
 //               64 bits as their own rounding (0.0017 against 0.0023 in all).
 //               Wider blocks keep one term: a second costs 32 x 30 rows over 16384
 //               3.5%, blocks of 64 rows of heads of 64 16%
 // Warps split a tile by rows (16 each) and what is left of them by keys, and
 // merge through shared memory at the end of a segment.  Two CTAs an SM, 96 KB of
 // tiles in flight each: 32 sequences of 6 rows over 16384 keys run at 6.6 TB/s,
-// 98% of the copy rate; the tensor pipe is at 15%, so that the warp-level product
-// is no limit at these row counts.
+// 97-98% of the copy rate; at 16 packed rows the tensor pipe is at 23%, so that the
+// warp-level product is no limit at these row counts.
 #include "internal.h"
 #include "paged_tc.cuh"
 
