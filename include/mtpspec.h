@@ -599,7 +599,7 @@ int mtp_selftest_wait_timeout(int32_t *status, mtp_stream_t stream);
 /*
  * Diagnostics.  spec_adjust_logits (out of place, k at least 1) with the copy of every
  * sequence's second row withheld: the waits for it give up, and the result is the same
- * all the same.  About 4 s of GPU time for every SM's CTAs.
+ * all the same.  About 4 s of GPU time; B at most 64, B * V at most 2^17.
  */
 int mtp_selftest_logits_wait(int B, int k, int V, const MtpLogitRules *rules, const float *logits,
                              const int32_t *draft_tok, float *out, mtp_stream_t stream);

@@ -1148,7 +1148,9 @@ int spec_adjust_logits(int B, int k, int V, const MtpLogitRules *rules, const fl
 
 int mtp_selftest_logits_wait(int B, int k, int V, const MtpLogitRules *rules, const float *logits,
                              const int32_t *draft_tok, float *out, mtp_stream_t stream) {
-  if (k < 1 || logits == out) return MTP_ERR_INVALID_ARG;
+  if (B < 1 || V < 1 || k < 1 || logits == out) return MTP_ERR_INVALID_ARG;
+  // every block waits: they have to be resident together for the time to stay what it is
+  if (B > 64 || (long long)B * V > (1 << 17)) return MTP_ERR_UNSUPPORTED_SHAPE;
   return adjust_logits(B, k, V, rules, logits, draft_tok, out, stream, true);
 }
 

@@ -101,7 +101,7 @@ def test_a_paged_draft_at_no_position_writes_nothing(bad):
     m.ctx_len.fill_(bad)
     m.draft_paged(w.T, 0)
     torch.cuda.synchronize()
-    assert bd.get_status(m.ws_paged) & bd.STATUS_BAD_CTX
+    assert m.status() & bd.STATUS_BAD_CTX
     m.check_canaries()
     for pool, x in zip(m.cache.tensors[:2], was):
         assert torch.equal(pool.view(torch.int16), x.view(torch.int16))

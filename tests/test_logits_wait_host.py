@@ -15,3 +15,5 @@ def test_the_self_test_needs_a_second_row_and_a_second_array():
     assert call(1, 1, 100, rules, IN, None, IN, None) == -1     # in place: no copy to withhold
     assert call(1, 1, 100, None, IN, None, OUT, None) == -1
     assert call(0, 1, 100, rules, IN, None, OUT, None) == -1
+    assert call(65, 1, 100, rules, IN, None, OUT, None) == -2    # more blocks than wait side by side
+    assert call(2, 1, 100000, rules, IN, None, OUT, None) == -2
