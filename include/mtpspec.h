@@ -509,6 +509,125 @@ int mtp_paged_attn(const MtpPagedCache *cache, int B, int Hq, int n_rows, int ma
                    size_t ws_bytes, mtp_stream_t stream);
 
 /*
+ * Latent attention: the target's side of a step for targets whose keys and values
+ * come from one latent vector a token.  With c the token's normed latent (R
+ * elements), k its rotated key part (Dr, shared by the heads) and a head's up
+ * projection W = [Wk; Wv] (Dn and Dv rows of R), a head of query (a, r), its Dn
+ * plain and Dr rotated elements, has the score a.(Wk c) + r.k and the value Wv c.
+ *   Absorbed (candidate rows, plain decoding): the score is (Wk^T a, r).(c, k) and
+ *     the weighted sum of values Wv (sum p c), so that every head reads the same
+ *     cached row: mtp_latent_append, mtp_latent_heads (queries in), mtp_latent_attn,
+ *     mtp_latent_heads (outputs out).
+ *   Expanded (prompts, with 3.4 times fewer operations a score at the sizes 512, 64,
+ *     128, 128): mtp_latent_append, mtp_latent_expand (or the caller's own keys and
+ *     values, if all are in hand), mtp_latent_prefill.
+ * Rows, row_start and ctx_len are as above.
+ *
+ * The cache: pages [n_pages, page, R + Dr] bf16, a position's row being (c, k);
+ * position j of sequence b is slot j % page of page page_table[b, j / page].
+ *   R 256 or 512;  Dr 32 or 64;  page 16, 32, 64 or 128;  heads 1 .. 128
+ *   n_pages * page < 2^31, max_pages * page <= 2^30, n_rows <= 2^29
+ */
+typedef struct {
+    int32_t R, Dr, page, n_pages, max_pages;
+    void *pages;
+    const int32_t *page_table; /* [B, max_pages], as in MtpPagedCache */
+} MtpLatentCache;
+
+/*
+ * mtp_latent_append -- norm the new rows' latents, rotate their key parts and the
+ * queries' rotary parts, and write the latent rows into their page slots.
+ *   rope    NULL: nothing rotates; rot_dim at most Dr
+ *   kv      bf16 rows of R + Dr (one projection's output), ldkv elements apart
+ *   gain    [R] bf16: c = x / sqrt(mean(x^2) + eps) * gain; NULL: c = x
+ *   q       bf16: head h of a row's rotary part (Dr elements) is hsq * h elements
+ *           behind the row's first, rows ldq apart; q and q_out both NULL: keys only
+ *   q_out   alike, ldqo and hsqo apart; q itself (same strides) to rotate in place;
+ *           no other overlap.  The other elements of its rows are left as they are.
+ * Pointers are aligned to 16 bytes, strides are multiples of 8.  Products and sums are
+ * fp32, rounded once to bf16.  A row that cannot be placed is handled as by
+ * mtp_cache_append.  ws: at least 256 bytes, 256-byte aligned: the status word.
+ */
+int mtp_latent_append(const MtpLatentCache *cache, const MtpRope *rope, int B, int Hq, int n_rows,
+                      const int32_t *row_start, const int32_t *ctx_len, const void *kv, int64_t ldkv,
+                      const void *gain, float eps, const void *q, int64_t ldq, int64_t hsq, void *q_out,
+                      int64_t ldqo, int64_t hsqo, void *ws, size_t ws_bytes, mtp_stream_t stream);
+
+/*
+ * mtp_latent_heads -- a product a head: y[n, h, :] = W[h] x[n, h, :], which takes
+ * queries into the latent space (W[h] = Wk^T, [R, Dn]) and outputs out of it (Wv,
+ * [Dv, R]).
+ *   K, N    elements of an x and of a y head: multiples of 8, at most 4096
+ *   x, y    bf16, rows ldx / ldy and heads hsx / hsy elements apart (in either order);
+ *           y must not overlap x or w, nor its own rows each other
+ *   w       bf16, heads hsw apart: W[h] row-major [N, K], rows ldw apart, or, with
+ *           `transposed`, row-major [K, N] (so that Wk^T is read where Wk lies)
+ * Strides are multiples of 8, pointers aligned to 16 bytes.  n_rows <= 2^29, H <= 65535.
+ * Sums are fp32, rounded once to bf16.  ws: at least 256 bytes (the status word).
+ */
+int mtp_latent_heads(int n_rows, int H, int K, int N, const void *x, int64_t ldx, int64_t hsx, const void *w,
+                     int64_t ldw, int64_t hsw, int transposed, void *y, int64_t ldy, int64_t hsy, void *ws,
+                     size_t ws_bytes, mtp_stream_t stream);
+
+/*
+ * mtp_latent_expand -- keys and values of every head from the cached latents:
+ * kv[r, h, :] = W[h] c and k_rope[r, :] = k for the rows r = key_start[b] + j of
+ * positions j = 0, 1, .. of each sequence.
+ *   key_start [B+1] int32 (device): sequence b has rows key_start[b] ..
+ *             key_start[b+1] - 1 of the n_keys rows that kv and k_rope hold, its
+ *             first positions; the other rows are left as they were
+ *   N         elements of a kv head (Dn + Dv): a multiple of 8, at most 4096
+ *   w         bf16 [H, N, R], rows ldw and heads hsw elements apart
+ *   kv        bf16 rows of H * N, ldkv elements apart;  k_rope  rows of Dr, ldkr apart
+ * Starts out of order or outside the rows set MTP_STATUS_BAD_ROWS, positions past the
+ * cache MTP_STATUS_BAD_CTX; their rows are not written.  An entry of the page table
+ * outside the pool sets MTP_STATUS_BAD_PAGE, and page 0 is read in its place.
+ */
+int mtp_latent_expand(const MtpLatentCache *cache, int B, int H, int N, int n_keys, const int32_t *key_start,
+                      const void *w, int64_t ldw, int64_t hsw, void *kv, int64_t ldkv, void *k_rope, int64_t ldkr,
+                      void *ws, size_t ws_bytes, mtp_stream_t stream);
+
+/*
+ * mtp_latent_attn -- absorbed attention of the new rows over the cache, whose pages
+ * already hold the rows' own latents.  Visibility (causal; window, sinks) is
+ * mtp_paged_attn's.
+ *   q      bf16 rows of Hq * (R + Dr), ldq elements apart
+ *   scale  softmax scale (> 0), usually 1 / sqrt(Dn + Dr)
+ *   out    bf16 rows of Hq * R, ldo apart: sum_j p_j c_j; must not overlap q
+ *   lse    [n_rows, Hq] fp32, or NULL: ln sum_j exp(score)
+ *   ws     mtp_latent_attn_workspace_size() bytes, 256-byte aligned
+ * Scores, statistics and sums are fp32; the softmax weights are rounded to bf16 for
+ * their product with the latents.  What a row without keys gives, NaN and infinities, and
+ * what unseen positions may hold are as for mtp_paged_attn.
+ */
+size_t mtp_latent_attn_workspace_size(int B, int n_rows, int Hq, int R);
+int mtp_latent_attn(const MtpLatentCache *cache, int B, int Hq, int n_rows, const int32_t *row_start,
+                    const int32_t *ctx_len, const void *q, int64_t ldq, float scale, int window, int sinks,
+                    void *out, int64_t ldo, float *lse, void *ws, size_t ws_bytes, mtp_stream_t stream);
+
+/*
+ * mtp_latent_prefill -- attention of the new rows over keys and values of each head,
+ * the rotated key part shared by the heads.
+ *   Dn, Dv 64 or 128;  Dr 32 or 64
+ *   key_start [B] int32 (device): position j of sequence b is row key_start[b] + j of
+ *          the n_keys rows of kv and k_rope (mtp_latent_expand's; for prompts without a
+ *          context, row_start itself).  A sequence whose ctx_len[b] + rows positions
+ *          leave those rows sets MTP_STATUS_BAD_CTX; what its rows hold then is not
+ *          specified.
+ *   q      bf16 rows of H * (Dn + Dr), ldq elements apart
+ *   kv     bf16 rows of H * (Dn + Dv): a head's key elements, then its value;  k_rope
+ *          bf16 rows of Dr
+ *   out    bf16 rows of H * Dv, ldo apart; must not overlap q
+ *   scale, window, sinks, lse, ws as for mtp_latent_attn, with
+ *   mtp_latent_prefill_workspace_size() bytes of workspace
+ */
+size_t mtp_latent_prefill_workspace_size(int B, int n_rows, int H, int Dv);
+int mtp_latent_prefill(int B, int H, int Dn, int Dr, int Dv, int n_rows, int n_keys, const int32_t *row_start,
+                       const int32_t *ctx_len, const int32_t *key_start, const void *q, int64_t ldq, const void *kv,
+                       int64_t ldkv, const void *k_rope, int64_t ldkr, float scale, int window, int sinks, void *out,
+                       int64_t ldo, float *lse, void *ws, size_t ws_bytes, mtp_stream_t stream);
+
+/*
  * spec_adjust_logits -- penalties for repeated tokens, biases and a grammar mask
  * on the target's logits of every candidate position, before spec_verify.
  * Position j of sequence b follows its history and its drafts 0 .. j-1.  With
@@ -658,7 +777,11 @@ enum {
     MTP_TK_PAGED_COMBINE = 62, /* paged attention: joins partial items */
     MTP_TK_CACHE_APPEND = 63,  /* mtp_cache_append */
     MTP_TK_LOGITS = 64,        /* spec_adjust_logits */
-    MTP_TK_PAGED_PLAN = 65     /* paged attention: the tensor-core kernel's plan */
+    MTP_TK_PAGED_PLAN = 65,    /* the plan of the tensor-core kernels over ragged rows */
+    MTP_TK_LATENT_APPEND = 70, /* mtp_latent_append */
+    MTP_TK_LATENT_HEADS = 71,  /* mtp_latent_heads, mtp_latent_expand */
+    MTP_TK_LATENT_ATTN = 72,   /* mtp_latent_attn */
+    MTP_TK_LATENT_PREFILL = 73 /* mtp_latent_prefill */
 };
 typedef struct MtpTraceEntry {
     uint64_t launch;      /* the launch's grid id */

@@ -61,6 +61,11 @@ class MtpPagedCache(ctypes.Structure):
                 ("v_pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
 
 
+class MtpLatentCache(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("Dr", ctypes.c_int32), ("page", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
 class MtpRope(ctypes.Structure):
     _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
@@ -147,6 +152,21 @@ def _lib():
         L.spec_step_paged.argtypes = [ctypes.POINTER(MtpDims), ctypes.POINTER(MtpWeights), PC, PR, I, I, P, P, P, I, F,
                                       I, P, P, P, P, P, P, P, P, P, P, Z, P]
         L.spec_step_paged.restype = I
+        LC = ctypes.POINTER(MtpLatentCache)
+        L.mtp_latent_append.argtypes = [LC, PR, I, I, I, P, P, P, L64, P, F, P, L64, L64, P, L64, L64, P, Z, P]
+        L.mtp_latent_append.restype = I
+        L.mtp_latent_heads.argtypes = [I, I, I, I, P, L64, L64, P, L64, L64, I, P, L64, L64, P, Z, P]
+        L.mtp_latent_heads.restype = I
+        L.mtp_latent_expand.argtypes = [LC, I, I, I, I, P, P, L64, L64, P, L64, P, L64, P, Z, P]
+        L.mtp_latent_expand.restype = I
+        L.mtp_latent_attn_workspace_size.argtypes = [I, I, I, I]
+        L.mtp_latent_attn_workspace_size.restype = Z
+        L.mtp_latent_attn.argtypes = [LC, I, I, I, P, P, P, L64, F, I, I, P, L64, P, P, Z, P]
+        L.mtp_latent_attn.restype = I
+        L.mtp_latent_prefill_workspace_size.argtypes = [I, I, I, I]
+        L.mtp_latent_prefill_workspace_size.restype = Z
+        L.mtp_latent_prefill.argtypes = [I, I, I, I, I, I, I, P, P, P, P, L64, P, L64, P, L64, F, I, I, P, L64, P, P, Z, P]
+        L.mtp_latent_prefill.restype = I
         L.spec_adjust_logits.argtypes = [I, I, I, ctypes.POINTER(MtpLogitRules), P, P, P, P]
         L.spec_adjust_logits.restype = I
         L.mtp_selftest_logits_wait.argtypes = L.spec_adjust_logits.argtypes
@@ -565,6 +585,158 @@ def mtp_paged_attn(cache, row_start, ctx_len, q, out, lse, ws, scale=0.0, window
         raise MtpError(rc, "mtp_paged_attn")
 
 
+def make_latent_cache(pages, page_table, rope_dim):
+    """MtpLatentCache over a pool pages [n_pages, page, R + rope_dim] bf16 and
+    page_table [B, max_pages] int32 (CUDA tensors; the struct keeps them alive)."""
+    if pages.dim() != 3 or pages.shape[2] <= rope_dim:
+        raise ValueError("pages must be [n_pages, page, R + rope_dim]")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    n_pages, page, w = pages.shape
+    c = MtpLatentCache(w - int(rope_dim), int(rope_dim), page, n_pages, page_table.shape[1],
+                       _ptr(pages, "pages", torch.bfloat16), _ptr(page_table, "page_table", torch.int32))
+    c.tensors = (pages, page_table)
+    c.B = page_table.shape[0]
+    return c
+
+
+def _heads(t, name):
+    """(pointer, row stride, head stride, rows, heads, elements) of [rows, heads, D] bf16
+    whose heads are contiguous; strides in elements."""
+    if not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype is not _BF16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    st, sh = t.stride(), t.shape
+    if len(st) != 3 or (st[2] != 1 and sh[2] != 1):
+        raise ValueError("%s must be [rows, heads, D], contiguous within a head" % name)
+    # torch keeps any stride for a dimension of one
+    D = -(-sh[2] // 8) * 8
+    hs = st[1] if sh[1] > 1 else max(st[1], D)
+    return t.data_ptr(), st[0] if sh[0] > 1 else max(st[0], (sh[1] - 1) * hs + D), hs, sh[0], sh[1], sh[2]
+
+
+def mtp_latent_append(cache, rope, row_start, ctx_len, kv, gain, eps, q, q_out, ws, stream=None):
+    """Norm (gain [R] bf16, or None: not) and rotate (rope None: not) the new rows kv
+    [rows, R + Dr] bf16 and write them into the pages of cache (make_latent_cache); rotate
+    q into q_out, the rotary parts [rows, heads, Dr] of the queries (any strides that are
+    multiples of 8; both may be None)."""
+    B, rs, cl = _row_args(cache, row_start, ctx_len)
+    kp, ldkv, n, w = _rows(kv, "kv", cache.R + cache.Dr)
+    if w != cache.R + cache.Dr:
+        raise ValueError("kv must be rows of R + Dr")
+    qp = qo = None
+    ldq = hsq = ldqo = hsqo = H = 0
+    if q is not None and q_out is not None:
+        qp, ldq, hsq, nq, H, d = _heads(q, "q")
+        qo, ldqo, hsqo, no, Ho, do = _heads(q_out, "q_out")
+        if nq != n or no != n or Ho != H or d != cache.Dr or do != cache.Dr:
+            raise ValueError("q and q_out must be [rows, heads, Dr] of kv's rows")
+    elif q is not None or q_out is not None:
+        raise ValueError("q and q_out are given together")
+    rc = _lib().mtp_latent_append(cache, rope, B, H, n, rs, cl, kp, ldkv, _ptr(gain, "gain", _BF16, cache.R), float(eps), qp,
+                                  ldq, hsq, qo, ldqo, hsqo, _ptr(ws, "ws"), ws.nbytes, _stream(stream))
+    if rc != 0:
+        raise MtpError(rc, "mtp_latent_append")
+
+
+def _head_weights(w, name):
+    """(pointer, row stride, head stride, transposed) of [H, N, K] bf16 weights whose K, or
+    whose N, is contiguous."""
+    if not w.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if w.dtype is not _BF16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, w.dtype))
+    st = w.stride()
+    if len(st) != 3 or (st[2] != 1 and st[1] != 1):
+        raise ValueError("%s must be [heads, N, K], contiguous along N or K" % name)
+    t = st[2] != 1
+    return w.data_ptr(), st[2] if t else st[1], st[0] if w.shape[0] > 1 else max(st[0], 8), int(t)
+
+
+def mtp_latent_heads(x, w, y, ws, stream=None):
+    """y[n, h, :] = w[h] x[n, h, :]: x [rows, H, K], w [H, N, K] (or the transposed view of
+    [H, K, N]), y [rows, H, N], bf16, any strides that are multiples of 8."""
+    xp, ldx, hsx, n, H, K = _heads(x, "x")
+    yp, ldy, hsy, ny, Hy, N = _heads(y, "y")
+    wp, ldw, hsw, t = _head_weights(w, "w")
+    if ny != n or Hy != H or tuple(w.shape) != (H, N, K):
+        raise ValueError("x, w and y must be [rows, H, K], [H, N, K] and [rows, H, N]")
+    rc = _lib().mtp_latent_heads(n, H, K, N, xp, ldx, hsx, wp, ldw, hsw, t, yp, ldy, hsy, _ptr(ws, "ws"), ws.nbytes,
+                                 _stream(stream))
+    if rc != 0:
+        raise MtpError(rc, "mtp_latent_heads")
+
+
+def mtp_latent_expand(cache, key_start, w, kv, k_rope, ws, stream=None):
+    """Keys and values of every head from the cached latents: kv [n_keys, H, N] = w [H, N, R]
+    times the latents, k_rope [n_keys, Dr] the shared key parts, of the first
+    key_start[b+1] - key_start[b] positions of each sequence (key_start [B+1] int32)."""
+    B = key_start.numel() - 1
+    if B < 1 or B > cache.B:
+        raise ValueError("key_start must be [B+1], page_table has %d sequences" % cache.B)
+    if kv.dim() != 3 or k_rope.dim() != 2:
+        raise ValueError("kv must be [n_keys, H, N], k_rope [n_keys, Dr]")
+    kp, ldkv, n, _ = _rows(kv, "kv", kv.shape[2])
+    rp, ldkr, nr, dr = _rows(k_rope, "k_rope", cache.Dr)
+    wp, ldw, hsw, t = _head_weights(w, "w")
+    H, N = kv.shape[1], kv.shape[2]
+    if nr != n or dr != cache.Dr or t or tuple(w.shape) != (H, N, cache.R):
+        raise ValueError("w, kv and k_rope must be [H, N, R], [n_keys, H, N] and [n_keys, Dr]")
+    rc = _lib().mtp_latent_expand(cache, B, H, N, n, _ptr(key_start, "key_start", torch.int32), wp, ldw, hsw, kp, ldkv, rp, ldkr,
+                                  _ptr(ws, "ws"), ws.nbytes, _stream(stream))
+    if rc != 0:
+        raise MtpError(rc, "mtp_latent_expand")
+
+
+def latent_attn_workspace_size(B, n_rows, Hq, R):
+    return int(_lib().mtp_latent_attn_workspace_size(int(B), int(n_rows), int(Hq), int(R)))
+
+
+def mtp_latent_attn(cache, row_start, ctx_len, q, out, lse, ws, scale, window=0, sinks=0, stream=None):
+    """Absorbed attention of the new rows q [rows, Hq, R + Dr] over the pages of cache, into
+    out [rows, Hq, R] bf16 and, if given, lse [rows, Hq] fp32."""
+    B, rs, cl = _row_args(cache, row_start, ctx_len)
+    if q.dim() != 3 or out.dim() != 3 or q.shape[:2] != out.shape[:2] or q.shape[2] != cache.R + cache.Dr or \
+            out.shape[2] != cache.R:
+        raise ValueError("q and out must be [rows, Hq, R + Dr] and [rows, Hq, R]")
+    qp, ldq, n, _ = _rows(q, "q", q.shape[2])
+    op, ldo, _, _ = _rows(out, "out", out.shape[2])
+    H = q.shape[1]
+    rc = _lib().mtp_latent_attn(cache, B, H, n, rs, cl, qp, ldq, float(scale), int(window), int(sinks), op, ldo,
+                                _ptr(lse, "lse", torch.float32, n * H), _ptr(ws, "ws"), ws.nbytes, _stream(stream))
+    if rc != 0:
+        raise MtpError(rc, "mtp_latent_attn")
+
+
+def latent_prefill_workspace_size(B, n_rows, H, Dv):
+    return int(_lib().mtp_latent_prefill_workspace_size(int(B), int(n_rows), int(H), int(Dv)))
+
+
+def mtp_latent_prefill(row_start, ctx_len, key_start, q, kv, k_rope, out, lse, ws, scale, window=0, sinks=0, stream=None):
+    """Attention of the new rows q [rows, H, Dn + Dr] over keys and values of each head, kv
+    [n_keys, H, Dn + Dv] and the shared k_rope [n_keys, Dr] (mtp_latent_expand's), into out
+    [rows, H, Dv] bf16 and, if given, lse [rows, H] fp32.  Position j of sequence b is row
+    key_start[b] + j."""
+    B = ctx_len.numel()
+    if q.dim() != 3 or kv.dim() != 3 or k_rope.dim() != 2 or out.dim() != 3:
+        raise ValueError("q, kv and out must have three dimensions, k_rope two")
+    qp, ldq, n, _ = _rows(q, "q", q.shape[2])
+    kp, ldkv, nk, _ = _rows(kv, "kv", kv.shape[2])
+    rp, ldkr, nr, Dr = _rows(k_rope, "k_rope", k_rope.shape[1])
+    op, ldo, no, _ = _rows(out, "out", out.shape[2])
+    H, Dn, Dv = q.shape[1], q.shape[2] - Dr, out.shape[2]
+    if kv.shape[1] != H or out.shape[1] != H or no != n or nr != nk or kv.shape[2] != Dn + Dv:
+        raise ValueError("q, kv, k_rope and out must be [rows, H, Dn + Dr], [n_keys, H, Dn + Dv], [n_keys, Dr] and "
+                         "[rows, H, Dv]")
+    rc = _lib().mtp_latent_prefill(B, H, Dn, Dr, Dv, n, nk, _ptr(row_start, "row_start", torch.int32, B + 1),
+                                   _ptr(ctx_len, "ctx_len", torch.int32), _ptr(key_start, "key_start", torch.int32, B), qp, ldq,
+                                   kp, ldkv, rp, ldkr, float(scale), int(window), int(sinks), op, ldo,
+                                   _ptr(lse, "lse", torch.float32, n * H), _ptr(ws, "ws"), ws.nbytes, _stream(stream))
+    if rc != 0:
+        raise MtpError(rc, "mtp_latent_prefill")
+
+
 def paged_workspace_size(dims, k):
     return int(_lib().mtp_paged_workspace_size(ctypes.byref(dims), int(k)))
 
@@ -708,7 +880,8 @@ TRACE_KIND_NAMES = {0: "gemv input projection", 1: "gemv QKV", 2: "gemv output p
                     4: "gemv down", 5: "gemv LM head", 10: "attention", 11: "attention (tensor cores)",
                     20: "verify (cluster)", 21: "verify (ticketed)", 30: "tc GEMM", 31: "tc prologue/select",
                     40: "fused verify GEMM", 41: "fused verify aux (stats, decisions, draws)", 50: "chain", 60: "paged attention (streaming)", 61: "paged attention (tensor cores)",
-                    62: "paged attention combine", 63: "cache append", 64: "logit rules", 65: "paged attention plan"}
+                    62: "paged attention combine", 63: "cache append", 64: "logit rules", 65: "paged attention plan",
+                    70: "latent append", 71: "latent head products", 72: "latent attention", 73: "latent prefill"}
 
 
 def trace_read(max_entries=16384):

@@ -12,6 +12,7 @@
 
 #include "internal.h"
 #include "logits.cuh"
+#include "latent.cuh"
 #include "paged.cuh"
 #include "mtpspec.h"
 
@@ -79,6 +80,7 @@ int device_info(DevInfo *out) {
     if (tc_set_attributes() != cudaSuccess) return MTP_ERR_CUDA;
     if (fused_set_attributes() != cudaSuccess) return MTP_ERR_CUDA;
     if (paged_set_attributes() != cudaSuccess) return MTP_ERR_CUDA;
+    if (latent_set_attributes() != cudaSuccess) return MTP_ERR_CUDA;
     if (logits_set_attributes() != cudaSuccess) return MTP_ERR_CUDA;
     di.ctx = context_id();  // set up (made current) by the calls above
     di.init = true;
@@ -638,7 +640,9 @@ static_assert(kTkGemv == MTP_TK_GEMV && kTkAttn == MTP_TK_ATTN && kTkAttnTc == M
                   kTkTcAux == MTP_TK_TC_AUX && kTkFusedGemm == MTP_TK_FUSED_GEMM &&
                   kTkFusedAux == MTP_TK_FUSED_AUX && kTkChain == MTP_TK_CHAIN && kTkPagedAttn == MTP_TK_PAGED_ATTN &&
                   kTkPagedAttnTc == MTP_TK_PAGED_ATTN_TC && kTkPagedCombine == MTP_TK_PAGED_COMBINE &&
-                  kTkAppend == MTP_TK_CACHE_APPEND && kTkPagedPlan == MTP_TK_PAGED_PLAN && kTkLogits == MTP_TK_LOGITS,
+                  kTkAppend == MTP_TK_CACHE_APPEND && kTkPagedPlan == MTP_TK_PAGED_PLAN && kTkLogits == MTP_TK_LOGITS &&
+                  kTkLatentAppend == MTP_TK_LATENT_APPEND && kTkLatentHeads == MTP_TK_LATENT_HEADS &&
+                  kTkLatentAttn == MTP_TK_LATENT_ATTN && kTkLatentPrefill == MTP_TK_LATENT_PREFILL,
               "trace kinds match the header");
 
 // the launch-trace collectors of the kernel files (MTP_TRACE_COLLECTOR)
@@ -654,6 +658,10 @@ int trace_collect_paged_attn(TraceRec *, int);
 int trace_collect_paged_attn_tc(TraceRec *, int);
 int trace_collect_cache_append(TraceRec *, int);
 int trace_collect_logits(TraceRec *, int);
+int trace_collect_latent_append(TraceRec *, int);
+int trace_collect_latent_heads(TraceRec *, int);
+int trace_collect_latent_attn(TraceRec *, int);
+int trace_collect_latent_prefill(TraceRec *, int);
 
 }  // namespace mtp
 
@@ -1108,6 +1116,241 @@ int mtp_paged_attn(const MtpPagedCache *cache, int B, int Hq, int n_rows, int ma
   return e == cudaErrorNotSupported ? MTP_ERR_CUDA : cuda_rc(e);
 }
 
+}  // extern "C"
+
+namespace mtp {
+namespace {
+
+int check_latent(const MtpLatentCache *c) {
+  if (!c || c->n_pages < 1 || c->max_pages < 1) return MTP_ERR_INVALID_ARG;
+  if (!aligned16(c->pages) || !aligned16(c->page_table)) return MTP_ERR_INVALID_ARG;
+  if ((c->R != 256 && c->R != 512) || (c->Dr != 32 && c->Dr != 64)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return MTP_ERR_UNSUPPORTED_SHAPE;
+  // rows of the pool are TMA coordinates, positions 32-bit
+  if ((long long)c->n_pages * c->page >= (1ll << 31)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if ((long long)c->max_pages * c->page > (1ll << 30)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  return MTP_OK;
+}
+
+constexpr int kMaxLatentHeads = 128;
+
+int check_latent_rows(int B, int H, int n_rows, const int32_t *row_start, const int32_t *ctx_len) {
+  if (B < 1 || n_rows < 1 || H < 1) return MTP_ERR_INVALID_ARG;
+  if (B > (1 << 20) || n_rows > (1 << 29) || H > kMaxLatentHeads) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(row_start) || !aligned16(ctx_len)) return MTP_ERR_INVALID_ARG;
+  return MTP_OK;
+}
+
+// A stride in elements: whole 16-byte vectors, below the 2^40 bytes of a tensor map.
+bool stride_ok(int64_t ld, long long width) { return ld >= width && ld % 8 == 0 && ld < (1ll << 38); }
+
+bool workspace_ok(const void *ws) { return aligned16(ws) && (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) == 0; }
+
+int check_attention(float scale, int window, int sinks, const void *q, const void *out, const float *lse) {
+  if (window < 0 || sinks < 0 || !(scale > 0.f && scale < 1e30f)) return MTP_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || q == out || (lse && !aligned16(lse))) return MTP_ERR_INVALID_ARG;
+  return MTP_OK;
+}
+
+}  // namespace
+}  // namespace mtp
+
+extern "C" {
+
+int mtp_latent_append(const MtpLatentCache *cache, const MtpRope *rope, int B, int Hq, int n_rows,
+                      const int32_t *row_start, const int32_t *ctx_len, const void *kv, int64_t ldkv, const void *gain,
+                      float eps, const void *q, int64_t ldq, int64_t hsq, void *q_out, int64_t ldqo, int64_t hsqo,
+                      void *ws, size_t ws_bytes, mtp_stream_t stream) {
+  int rc = check_latent(cache);
+  if (!rc) rc = check_latent_rows(B, q ? Hq : 1, n_rows, row_start, ctx_len);
+  if (rc) return rc;
+  if (!aligned16(kv) || !stride_ok(ldkv, cache->R + cache->Dr)) return MTP_ERR_INVALID_ARG;
+  if (gain && (!aligned16(gain) || !(eps >= 0.f && eps < 1e30f))) return MTP_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr)) return MTP_ERR_INVALID_ARG;
+  if (q) {
+    if (!aligned16(q) || !aligned16(q_out)) return MTP_ERR_INVALID_ARG;
+    if (!stride_ok(hsq, cache->Dr) || !stride_ok(ldq, (Hq - 1) * hsq + cache->Dr)) return MTP_ERR_INVALID_ARG;
+    if (!stride_ok(hsqo, cache->Dr) || !stride_ok(ldqo, (Hq - 1) * hsqo + cache->Dr)) return MTP_ERR_INVALID_ARG;
+    if (q == q_out && (ldq != ldqo || hsq != hsqo)) return MTP_ERR_INVALID_ARG;
+  }
+  if (!rope_ok(rope, cache->Dr, &rc)) return rc;
+  if (!workspace_ok(ws)) return MTP_ERR_INVALID_ARG;
+  // the launch counts its warps in 32 bits
+  if ((long long)n_rows * ((q ? Hq : 0) * cache->Dr / 256 + 3) >= (1ll << 31)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if (ws_bytes < kAlign) return MTP_ERR_WORKSPACE;
+  LatentAppendArgs a{};
+  a.B = B; a.Hq = q ? Hq : 0; a.R = cache->R; a.Dr = cache->Dr;
+  a.page = cache->page; a.page_shift = page_shift(cache->page); a.n_pages = cache->n_pages;
+  a.max_pages = cache->max_pages; a.cap = cache->max_pages * cache->page; a.n_rows = n_rows;
+  a.rot = rope ? rope->rot_dim : 0;
+  a.layout = rope ? rope->layout : 0;
+  a.turns = rope ? reinterpret_cast<const unsigned long long *>(rope->turns) : nullptr;
+  a.scale = rope ? rope->scale : 1.f;
+  a.eps = eps;
+  a.row_start = row_start; a.ctx_len = ctx_len; a.page_table = cache->page_table;
+  a.kv = static_cast<const uint16_t *>(kv); a.gain = static_cast<const uint16_t *>(gain);
+  a.q = static_cast<const uint16_t *>(q); a.q_out = static_cast<uint16_t *>(q_out);
+  a.pages = static_cast<uint16_t *>(cache->pages);
+  a.ldkv = ldkv; a.ldq = ldq; a.hsq = hsq; a.ldqo = ldqo; a.hsqo = hsqo;
+  a.status = static_cast<int *>(ws);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  NvtxRange r("mtp latent append");
+  cudaError_t e = launch_latent_append(a, s, use_pdl());
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return cuda_rc(e);
+}
+
+// The products' launch, with its device set up.
+static int run_heads(const LatentHeadsArgs &a, mtp_stream_t stream) {
+  if (!tc_available()) return MTP_ERR_CUDA;
+  DevInfo di;
+  if (int rc = device_info(&di)) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_latent_heads(a, di.sms, s, use_pdl());
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaErrorNotSupported ? MTP_ERR_CUDA : cuda_rc(e);
+}
+
+int mtp_latent_heads(int n_rows, int H, int K, int N, const void *x, int64_t ldx, int64_t hsx, const void *w,
+                     int64_t ldw, int64_t hsw, int transposed, void *y, int64_t ldy, int64_t hsy, void *ws,
+                     size_t ws_bytes, mtp_stream_t stream) {
+  if (n_rows < 1 || H < 1 || K < 1 || N < 1) return MTP_ERR_INVALID_ARG;
+  if (n_rows > (1 << 29) || H > 65535 || K % 8 || N % 8 || K > 4096 || N > 4096) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(y) || x == y || w == y) return MTP_ERR_INVALID_ARG;
+  if (!stride_ok(ldx, K) || !stride_ok(hsx, K) || !stride_ok(ldy, N) || !stride_ok(hsy, N)) return MTP_ERR_INVALID_ARG;
+  if (!stride_ok(ldw, transposed ? N : K) || !stride_ok(hsw, 8)) return MTP_ERR_INVALID_ARG;
+  // y's rows are apart, heads within rows or rows within heads
+  if (ldy < (__int128)(H - 1) * hsy + N && hsy < (__int128)(n_rows - 1) * ldy + N) return MTP_ERR_INVALID_ARG;
+  if (!workspace_ok(ws)) return MTP_ERR_INVALID_ARG;
+  if (ws_bytes < kAlign) return MTP_ERR_WORKSPACE;
+  LatentHeadsArgs a{};
+  a.n_rows = n_rows; a.H = H; a.K = K; a.N = N; a.transposed = transposed != 0;
+  a.x = static_cast<const uint16_t *>(x); a.w = static_cast<const uint16_t *>(w); a.y = static_cast<uint16_t *>(y);
+  a.ldx = ldx; a.hsx = hsx; a.ldw = ldw; a.hsw = hsw; a.ldy = ldy; a.hsy = hsy;
+  a.status = static_cast<int *>(ws);
+  NvtxRange r("mtp latent heads");
+  return run_heads(a, stream);
+}
+
+int mtp_latent_expand(const MtpLatentCache *cache, int B, int H, int N, int n_keys, const int32_t *key_start,
+                      const void *w, int64_t ldw, int64_t hsw, void *kv, int64_t ldkv, void *k_rope, int64_t ldkr,
+                      void *ws, size_t ws_bytes, mtp_stream_t stream) {
+  int rc = check_latent(cache);
+  if (rc) return rc;
+  if (B < 1 || H < 1 || N < 1 || n_keys < 1) return MTP_ERR_INVALID_ARG;
+  if (B > (1 << 20) || H > kMaxLatentHeads || N % 8 || N > 4096 || n_keys > (1 << 29)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(key_start) || !aligned16(w) || !aligned16(kv) || !aligned16(k_rope)) return MTP_ERR_INVALID_ARG;
+  if (!stride_ok(ldw, cache->R) || !stride_ok(hsw, 8)) return MTP_ERR_INVALID_ARG;
+  if (!stride_ok(ldkv, (long long)H * N) || !stride_ok(ldkr, cache->Dr)) return MTP_ERR_INVALID_ARG;
+  if (!workspace_ok(ws)) return MTP_ERR_INVALID_ARG;
+  if (ws_bytes < kAlign) return MTP_ERR_WORKSPACE;
+  LatentHeadsArgs a{};
+  a.n_rows = n_keys; a.H = H; a.K = cache->R; a.N = N;
+  a.w = static_cast<const uint16_t *>(w); a.y = static_cast<uint16_t *>(kv);
+  a.ldw = ldw; a.hsw = hsw; a.ldy = ldkv; a.hsy = N;
+  a.status = static_cast<int *>(ws);
+  a.pages = static_cast<const uint16_t *>(cache->pages);
+  a.B = B; a.Dr = cache->Dr; a.page = cache->page; a.page_shift = page_shift(cache->page); a.n_pages = cache->n_pages;
+  a.max_pages = cache->max_pages; a.cap = cache->max_pages * cache->page;
+  a.key_start = key_start; a.page_table = cache->page_table;
+  a.k_rope = static_cast<uint16_t *>(k_rope); a.ldkr = ldkr;
+  NvtxRange r("mtp latent expand");
+  return run_heads(a, stream);
+}
+
+size_t mtp_latent_attn_workspace_size(int B, int n_rows, int Hq, int R) {
+  if (B < 1 || n_rows < 1 || Hq < 1 || Hq > kMaxLatentHeads || (R != 256 && R != 512)) return 0;
+  if (B > (1 << 20) || n_rows > (1 << 29) || !latent_attn_items_ok(B, n_rows, Hq)) return 0;
+  return kAlign + latent_attn_scratch_bytes(B, n_rows, Hq, R);
+}
+
+int mtp_latent_attn(const MtpLatentCache *cache, int B, int Hq, int n_rows, const int32_t *row_start,
+                    const int32_t *ctx_len, const void *q, int64_t ldq, float scale, int window, int sinks, void *out,
+                    int64_t ldo, float *lse, void *ws, size_t ws_bytes, mtp_stream_t stream) {
+  int rc = check_latent(cache);
+  if (!rc) rc = check_latent_rows(B, Hq, n_rows, row_start, ctx_len);
+  if (!rc) rc = check_attention(scale, window, sinks, q, out, lse);
+  if (rc) return rc;
+  if (!stride_ok(ldq, (long long)Hq * (cache->R + cache->Dr)) || !stride_ok(ldo, (long long)Hq * cache->R))
+    return MTP_ERR_INVALID_ARG;
+  if (!latent_attn_items_ok(B, n_rows, Hq)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if (!workspace_ok(ws)) return MTP_ERR_INVALID_ARG;
+  if (ws_bytes < mtp_latent_attn_workspace_size(B, n_rows, Hq, cache->R)) return MTP_ERR_WORKSPACE;
+  if (!tc_available()) return MTP_ERR_CUDA;
+  DevInfo di;
+  if ((rc = device_info(&di))) return rc;
+  LatentAttnArgs la{};
+  PagedArgs &a = la.a;
+  a.B = B; a.Hq = Hq; a.Hkv = 1; a.G = Hq; a.Dh = cache->R;
+  a.page = cache->page; a.page_shift = page_shift(cache->page); a.n_pages = cache->n_pages;
+  a.max_pages = cache->max_pages; a.cap = cache->max_pages * cache->page; a.n_rows = n_rows;
+  a.row_start = row_start; a.ctx_len = ctx_len; a.page_table = cache->page_table;
+  a.q = static_cast<const uint16_t *>(q); a.ldq = ldq; a.out = out; a.ldo = ldo; a.lse = lse;
+  a.scale_log2 = scale * kLog2e;
+  a.window = window; a.sinks = window ? sinks : 0;
+  a.status = static_cast<int *>(ws);
+  la.Dr = cache->Dr;
+  la.pages = static_cast<const uint16_t *>(cache->pages);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  NvtxRange r("mtp latent attention");
+  cudaError_t e = timed(MTP_KC_ATTN, s, [&] {
+    return launch_latent_attn(la, static_cast<char *>(ws) + kAlign, di.sms, s, use_pdl());
+  });
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaErrorNotSupported ? MTP_ERR_CUDA : cuda_rc(e);
+}
+
+size_t mtp_latent_prefill_workspace_size(int B, int n_rows, int H, int Dv) {
+  if (B < 1 || n_rows < 1 || H < 1 || H > kMaxLatentHeads || (Dv != 64 && Dv != 128)) return 0;
+  if (B > (1 << 20) || n_rows > (1 << 29) || !latent_prefill_items_ok(B, n_rows, H)) return 0;
+  return kAlign + latent_prefill_scratch_bytes(B, n_rows, H, Dv);
+}
+
+int mtp_latent_prefill(int B, int H, int Dn, int Dr, int Dv, int n_rows, int n_keys, const int32_t *row_start,
+                       const int32_t *ctx_len, const int32_t *key_start, const void *q, int64_t ldq, const void *kv,
+                       int64_t ldkv, const void *k_rope, int64_t ldkr, float scale, int window, int sinks, void *out,
+                       int64_t ldo, float *lse, void *ws, size_t ws_bytes, mtp_stream_t stream) {
+  int rc = check_latent_rows(B, H, n_rows, row_start, ctx_len);
+  if (!rc) rc = check_attention(scale, window, sinks, q, out, lse);
+  if (rc) return rc;
+  if (n_keys < 1) return MTP_ERR_INVALID_ARG;
+  if ((Dn != 64 && Dn != 128) || (Dv != 64 && Dv != 128) || (Dr != 32 && Dr != 64) || n_keys > (1 << 30))
+    return MTP_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(key_start) || !aligned16(kv) || !aligned16(k_rope)) return MTP_ERR_INVALID_ARG;
+  if (!stride_ok(ldq, (long long)H * (Dn + Dr)) || !stride_ok(ldkv, (long long)H * (Dn + Dv)) || !stride_ok(ldkr, Dr) ||
+      !stride_ok(ldo, (long long)H * Dv))
+    return MTP_ERR_INVALID_ARG;
+  if (!latent_prefill_items_ok(B, n_rows, H)) return MTP_ERR_UNSUPPORTED_SHAPE;
+  if (!workspace_ok(ws)) return MTP_ERR_INVALID_ARG;
+  if (ws_bytes < mtp_latent_prefill_workspace_size(B, n_rows, H, Dv)) return MTP_ERR_WORKSPACE;
+  if (!tc_available()) return MTP_ERR_CUDA;
+  DevInfo di;
+  if ((rc = device_info(&di))) return rc;
+  LatentPrefillArgs lp{};
+  PagedArgs &a = lp.a;
+  a.B = B; a.Hq = H; a.Hkv = H; a.G = 1; a.Dh = Dv;
+  a.page = 128; a.page_shift = 7; a.cap = n_keys; a.n_rows = n_rows;
+  a.row_start = row_start; a.ctx_len = ctx_len;
+  a.q = static_cast<const uint16_t *>(q); a.ldq = ldq; a.out = out; a.ldo = ldo; a.lse = lse;
+  a.scale_log2 = scale * kLog2e;
+  a.window = window; a.sinks = window ? sinks : 0;
+  a.status = static_cast<int *>(ws);
+  lp.Dn = Dn; lp.Dr = Dr; lp.Dv = Dv; lp.n_keys = n_keys; lp.key_start = key_start;
+  lp.kv = static_cast<const uint16_t *>(kv); lp.k_rope = static_cast<const uint16_t *>(k_rope);
+  lp.ldkv = ldkv; lp.ldkr = ldkr;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  NvtxRange r("mtp latent prefill");
+  cudaError_t e = timed(MTP_KC_ATTN, s, [&] {
+    return launch_latent_prefill(lp, static_cast<char *>(ws) + kAlign, di.sms, s, use_pdl());
+  });
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaErrorNotSupported ? MTP_ERR_CUDA : cuda_rc(e);
+}
+
+}  // extern "C"
+
+extern "C" {
+
 static int adjust_logits(int B, int k, int V, const MtpLogitRules *rules, const float *logits, const int32_t *draft_tok,
                          float *out, mtp_stream_t stream, bool stall) {
   if (!rules || B < 1 || k < 0 || k > 8 || V < 1 || V > (1 << 30) || B > (1 << 20)) return MTP_ERR_INVALID_ARG;
@@ -1221,7 +1464,9 @@ int mtp_trace_read(MtpTraceEntry *entries, int max_entries) {
                                          mtp::trace_collect_fused, mtp::trace_collect_chain,
                                          mtp::trace_collect_diag, mtp::trace_collect_paged_attn,
                                          mtp::trace_collect_paged_attn_tc,
-                                         mtp::trace_collect_cache_append, mtp::trace_collect_logits};
+                                         mtp::trace_collect_cache_append, mtp::trace_collect_logits,
+                                         mtp::trace_collect_latent_append, mtp::trace_collect_latent_heads,
+                                         mtp::trace_collect_latent_attn, mtp::trace_collect_latent_prefill};
   static mtp::TraceRec recs[mtp::kTraceSlots];
   int n = 0;
   for (Collector col : collectors) {

@@ -66,19 +66,6 @@ __device__ __forceinline__ typename Bf<VEC>::T pack(const float (&x)[VEC]) {
 
 }  // namespace
 
-// How many of the B sequences start at or before `row` (32 probes a round).
-__device__ __forceinline__ int starts_upto(const int *row_start, int B, int row, int lane) {
-  int lo = 0, n = B;
-  while (n > 0) {
-    const int step = (n + 31) / 32, i = lane * step;
-    const int c = __popc(__ballot_sync(kFull, i < n && __ldcg(&row_start[lo + i]) <= row));
-    if (c == 0) break;
-    lo += (c - 1) * step + 1;
-    n = min(step - 1, n - ((c - 1) * step + 1));
-  }
-  return lo;
-}
-
 template <int VEC, int U>
 __global__ void __launch_bounds__(32 * kAppWarps, U == 1 ? 1 : 5) cache_append_kernel(const __grid_constant__ AppendArgs p) {
   trace_start(kTkAppend);

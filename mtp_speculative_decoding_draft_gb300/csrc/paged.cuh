@@ -311,6 +311,19 @@ struct PagedWalk {
   }
 };
 
+// How many of the B sequences start at or before `row` (32 probes a round).
+__device__ __forceinline__ int starts_upto(const int *row_start, int B, int row, int lane) {
+  int lo = 0, n = B;
+  while (n > 0) {
+    const int step = (n + 31) / 32, i = lane * step;
+    const int c = __popc(__ballot_sync(0xffffffffu, i < n && __ldcg(&row_start[lo + i]) <= row));
+    if (c == 0) break;
+    lo += (c - 1) * step + 1;
+    n = min(step - 1, n - ((c - 1) * step + 1));
+  }
+  return lo;
+}
+
 // The page of key position j of sequence b: a table entry outside the pool is
 // flagged and page 0 read in its place.
 __device__ __forceinline__ int paged_page(const PagedArgs &p, int b, int j) {
