@@ -66,159 +66,6 @@ struct Lay {
   __host__ __device__ static constexpr uint32_t O(int g) { return 256u + 128u * g; }
 };
 
-// D[tmem] (+)= A[tmem] * B[smem], issued by a single thread.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Descriptor of an operand whose rows (of 128 bytes, 128-byte swizzle) run along
-// K: 64 elements of N in a row, 8-row groups 1024 bytes apart (stride), the next
-// 64 of N one half further (leading).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t addr, uint32_t half_bytes) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(half_bytes >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
-         ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
-}
-
-// 32 columns of this thread's lane, without the wait: the values are valid after
-// tmem_wait_ld() and pin32().
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t *r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Ties the registers of an asynchronous load to the wait before it: no use of
-// them is scheduled above this statement.
-__device__ __forceinline__ void pin32(uint32_t *r) {
-  asm volatile(""
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-      "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
-      : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
-// The n lowest bits.
-__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
-
-// N lanes that hold N quads of a row each exchange them: lane j of the N leaves
-// with quad j of every row, so that N lanes store one row's quads side by side.
-// (A lane a row, the stores touched 32 lines an instruction and an epilogue took
-// 6000 cycles.)
-template <int N>
-__device__ __forceinline__ void transpose_quads(uint4 (&q)[N], int lane) {
-#pragma unroll
-  for (int s = 1; s < N; s <<= 1) {
-    const bool up = lane & s;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (i & s) continue;
-      uint4 v = up ? q[i] : q[i | s];
-      v.x = __shfl_xor_sync(kFull, v.x, s);
-      v.y = __shfl_xor_sync(kFull, v.y, s);
-      v.z = __shfl_xor_sync(kFull, v.z, s);
-      v.w = __shfl_xor_sync(kFull, v.w, s);
-      if (up) q[i] = v;
-      else q[i | s] = v;
-    }
-  }
-}
-
-// Stores N quads of each lane's row at the lane's address (null: none).
-template <int N>
-__device__ __forceinline__ void store_quads(uint4 (&q)[N], void *at, int lane) {
-  transpose_quads<N>(q, lane);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const unsigned long long a = __shfl_sync(kFull, reinterpret_cast<unsigned long long>(at), (lane & ~(N - 1)) + i);
-    if (a) reinterpret_cast<uint4 *>(a)[lane & (N - 1)] = q[i];
-  }
-}
-
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(e));
-  return e != 0;
-}
-
-__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *m, int x, int y, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *m, int x, int y, int z, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-          "r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-
 constexpr int kPlanThreads = 512;
 
 // Inclusive scan over the block's threads; returns the block's sum.
@@ -243,65 +90,10 @@ __device__ __forceinline__ long long block_scan(long long v, long long *incl, lo
   return __shfl_sync(kFull, w, 31);
 }
 
-// Walks a share's items in the plan's order, one segment at a time; the interface
-// of PagedWalk.  On the line an item is kItemCost tiles, which stand for what a
-// segment costs besides its tiles (queries, first scores, output), then its tiles.
-template <int TK>
-struct PlanWalk {
-  const PagedTcParams &sp;
-  const PagedArgs &p;
-  long long first, end, per;  // where the item and the share's end lie on the line
-  int i, b, h, t0;
-  PagedSeq s;
-  PagedRange r;
-  int i0, i1;
-
-  __device__ __forceinline__ explicit PlanWalk(const PagedTcParams &x) : sp(x), p(x.a), i0(0), i1(0) {
-    const PagedStart *st = &sp.start[blockIdx.x];
-    const longlong2 e = __ldcg(reinterpret_cast<const longlong2 *>(&st->end));
-    i = __ldcg(&st->i);
-    load(&st->item);
-    end = e.x;
-    per = e.y;
-    const long long at = per * (long long)blockIdx.x - first - kItemCost;
-    if (at + first + kItemCost >= end) return;  // no share
-    i0 = at > 0 ? (int)at : 0;
-    cut();
-  }
-  __device__ __forceinline__ void load(const PagedItem *it) {
-    const int4 x = __ldcg(reinterpret_cast<const int4 *>(&it->b));
-    const int4 y = __ldcg(reinterpret_cast<const int4 *>(&it->row0));
-    first = __ldcg(&it->first);
-    b = x.x;
-    h = x.y;
-    t0 = x.z;
-    s.row0 = y.x;
-    s.n = y.y;
-    s.ctx = y.z;
-    r = paged_range<TK>(p, s, t0, t1());
-  }
-  __device__ __forceinline__ int t1() const { return min(s.n, t0 + p.tpb); }
-  __device__ __forceinline__ bool valid() const { return i0 < i1; }
-  __device__ __forceinline__ bool starts() const { return i0 == 0; }
-  __device__ __forceinline__ bool ends() const { return i1 == r.count; }
-  __device__ __forceinline__ int last_cta() const { return (int)((first + kItemCost + r.count - 1) / per); }
-  __device__ __forceinline__ void cut() {
-    const long long left = end - first - kItemCost;
-    i1 = left >= r.count ? r.count : left > 0 ? (int)left : 0;
-  }
-  __device__ __forceinline__ void next() {
-    i0 = i1 = 0;
-    if (first + kItemCost + r.count >= end) return;
-    do ++i;
-    while (__ldcg(&sp.items[i].count) == 0);  // the line goes on: an item follows
-    load(&sp.items[i]);
-    cut();
-  }
-};
-
 }  // namespace
 
 // One CTA: the items of the batch, their order, and where each share starts.
+template <int TK>
 __global__ void __launch_bounds__(kPlanThreads)
     paged_tc_plan_kernel(const __grid_constant__ PagedTcParams sp, int ctas) {
   trace_start(kTkPagedPlan);
@@ -323,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     int nb = 0;
     if (b < p.B) {
       const PagedSeq s = paged_seq(p, b, true, &back);
-      c = paged_cost<kTK>(p, s, &u);
+      c = paged_cost<TK>(p, s, &u);
       nb = paged_blocks(p, s.n);
     }
     const long long sum = block_scan(nb, &incl, scratch);
@@ -333,7 +125,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       else sp.blocks[b] = before;
     }
     nblk += sum;
-    total += block_scan((c + (long long)nb * kItemCost) * p.Hkv, &incl, scratch);
+    total += block_scan((c + (long long)nb * sp.item_cost) * p.Hkv, &incl, scratch);
   }
   if (tid == 0) {
     if (near) near_blocks[p.B] = (int)nblk;
@@ -370,12 +162,12 @@ __global__ void __launch_bounds__(kPlanThreads)
       it.b = lo;
       it.h = off / nb;
       it.t0 = (off % nb) * p.tpb;
-      it.count = paged_range<kTK>(p, s, it.t0, min(s.n, it.t0 + p.tpb)).count;
+      it.count = paged_range<TK>(p, s, it.t0, min(s.n, it.t0 + p.tpb)).count;
       it.row0 = s.row0;
       it.n = s.n;
       it.ctx = s.ctx;
     }
-    const int len = it.count > 0 ? kItemCost + it.count : 0;  // on the line
+    const int len = it.count > 0 ? sp.item_cost + it.count : 0;  // on the line
     const long long sum = block_scan(len, &incl, scratch);
     it.first = before + incl - len;
     before += sum;
@@ -434,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_tc_kernel(const __grid
   grid_dep_wait();
   trace_dep(kTkPagedAttnTc);
   grid_dep_launch();
-  PlanWalk<kTK> w(sp);
+  PlanWalk<kTK> w(sp, blockIdx.x);
   if (tid == 0) p.desc[blockIdx.x].rows = 0;
   if (!w.valid()) {  // the same for the whole CTA
     trace_end(kTkPagedAttnTc);
@@ -777,19 +569,19 @@ cudaError_t paged_tc_set_attributes() {
 // Items at most: one more block a sequence than its rows fill (the sequences' rows
 // are disjoint: row starts that decrease leave no items), a place's round of CTAs for
 // the gaps.
-static size_t plan_items(int B, int n_rows, int G, int Hkv) {
-  return ((size_t)n_rows / (2 * (128 / G)) + B) * Hkv + kPagedMaxCtas;
+static size_t plan_items(int B, int n_rows, int tpb, int Hkv) {
+  return ((size_t)n_rows / tpb + B) * Hkv + kPagedMaxCtas;
 }
 
-bool paged_tc_items_ok(int B, int n_rows, int G, int Hkv) {
-  return plan_items(B, n_rows, G, Hkv) < (1ull << 31) - (1 << 20);
+bool paged_tc_items_ok(int B, int n_rows, int tpb, int Hkv) {
+  return plan_items(B, n_rows, tpb, Hkv) < (1ull << 31) - (1 << 20);
 }
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-size_t paged_tc_plan_bytes(int B, int n_rows, int G, int Hkv) {
+size_t paged_tc_plan_bytes(int B, int n_rows, int tpb, int Hkv) {
   return up256((size_t)kPagedMaxCtas * sizeof(PagedStart)) + up256(((size_t)B + 1) * 4) +
-         up256(plan_items(B, n_rows, G, Hkv) * sizeof(PagedItem));
+         up256(plan_items(B, n_rows, tpb, Hkv) * sizeof(PagedItem));
 }
 
 void paged_tc_bind_plan(PagedTcParams &sp, char *base) {
@@ -800,27 +592,37 @@ void paged_tc_bind_plan(PagedTcParams &sp, char *base) {
   sp.items = reinterpret_cast<PagedItem *>(base);
 }
 
-cudaError_t launch_paged_attn_tc(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl) {
+static cudaLaunchConfig_t config(int ctas, int threads, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr, bool pdl) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sp.a.Dh == 128 ? Lay<128>::SMEM : Lay<64>::SMEM;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  const int smem = cfg.dynamicSmemBytes;
-  cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = 0;
+  return cfg;
+}
+
+template <int TK>
+cudaError_t launch_paged_plan(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl) {
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = config(1, kPlanThreads, 0, s, attr, pdl);
   note_launch();
-  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_tc_plan_kernel, sp, ctas);
+  return cudaLaunchKernelEx(&cfg, paged_tc_plan_kernel<TK>, sp, ctas);
+}
+template cudaError_t launch_paged_plan<64>(const PagedTcParams &, int, cudaStream_t, bool);
+template cudaError_t launch_paged_plan<128>(const PagedTcParams &, int, cudaStream_t, bool);
+
+cudaError_t launch_paged_attn_tc(const PagedTcParams &params, int ctas, cudaStream_t s, bool pdl) {
+  PagedTcParams sp = params;
+  sp.item_cost = kItemCost;
+  cudaError_t e = launch_paged_plan<kTK>(sp, ctas, s, pdl);
   if (e) return e;
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      config(ctas, kThreads, sp.a.Dh == 128 ? Lay<128>::SMEM : Lay<64>::SMEM, s, attr, pdl);
   note_launch();
   return sp.a.Dh == 128 ? cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<128>, sp)
                         : cudaLaunchKernelEx(&cfg, paged_attn_tc_kernel<64>, sp);

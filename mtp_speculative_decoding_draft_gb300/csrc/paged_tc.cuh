@@ -33,14 +33,75 @@ struct PagedTcParams {
   int *blocks;        // [B + 1] blocks of the sequences before b
   PagedStart *start;  // [CTAs]
   PagedItem *items;   // the line's items
+  int item_cost;      // tiles that an item counts for besides its own
+};
+
+// Walks a share's items in the plan's order, one segment at a time; the interface
+// of PagedWalk.  On the line an item is item_cost tiles, which stand for what a
+// segment costs besides its tiles (queries, first scores, output), then its tiles.
+template <int TK>
+struct PlanWalk {
+  const PagedTcParams &sp;
+  const PagedArgs &p;
+  long long first, end, per;  // where the item and the share's end lie on the line
+  int i, b, h, t0;
+  PagedSeq s;
+  PagedRange r;
+  int i0, i1;
+
+  __device__ __forceinline__ explicit PlanWalk(const PagedTcParams &x, int share) : sp(x), p(x.a), i0(0), i1(0) {
+    const PagedStart *st = &sp.start[share];
+    const longlong2 e = __ldcg(reinterpret_cast<const longlong2 *>(&st->end));
+    i = __ldcg(&st->i);
+    load(&st->item);
+    end = e.x;
+    per = e.y;
+    const long long at = per * (long long)share - first - sp.item_cost;
+    if (at + first + sp.item_cost >= end) return;  // no share
+    i0 = at > 0 ? (int)at : 0;
+    cut();
+  }
+  __device__ __forceinline__ void load(const PagedItem *it) {
+    const int4 x = __ldcg(reinterpret_cast<const int4 *>(&it->b));
+    const int4 y = __ldcg(reinterpret_cast<const int4 *>(&it->row0));
+    first = __ldcg(&it->first);
+    b = x.x;
+    h = x.y;
+    t0 = x.z;
+    s.row0 = y.x;
+    s.n = y.y;
+    s.ctx = y.z;
+    r = paged_range<TK>(p, s, t0, t1());
+  }
+  __device__ __forceinline__ int t1() const { return min(s.n, t0 + p.tpb); }
+  __device__ __forceinline__ bool valid() const { return i0 < i1; }
+  __device__ __forceinline__ bool starts() const { return i0 == 0; }
+  __device__ __forceinline__ bool ends() const { return i1 == r.count; }
+  __device__ __forceinline__ int last_cta() const { return (int)((first + sp.item_cost + r.count - 1) / per); }
+  __device__ __forceinline__ void cut() {
+    const long long left = end - first - sp.item_cost;
+    i1 = left >= r.count ? r.count : left > 0 ? (int)left : 0;
+  }
+  __device__ __forceinline__ void next() {
+    i0 = i1 = 0;
+    if (first + sp.item_cost + r.count >= end) return;
+    do ++i;
+    while (__ldcg(&sp.items[i].count) == 0);  // the line goes on: an item follows
+    load(&sp.items[i]);
+    cut();
+  }
 };
 
 // Queries as a 3-D map, boxes of `tokens` x G x 64 elements, 128-byte swizzle (tc.cu).
 bool make_query_map(CUtensorMap *m, const void *q, int Dh, int Hq, int n_rows, long long ldq, int G, int tokens);
 cudaError_t paged_tc_set_attributes();
-bool paged_tc_items_ok(int B, int n_rows, int G, int Hkv);  // the plan counts items in 31 bits
-size_t paged_tc_plan_bytes(int B, int n_rows, int G, int Hkv);
+// tpb: tokens of a block
+bool paged_tc_items_ok(int B, int n_rows, int tpb, int Hkv);  // the plan counts items in 31 bits
+size_t paged_tc_plan_bytes(int B, int n_rows, int tpb, int Hkv);
 void paged_tc_bind_plan(PagedTcParams &sp, char *base);
+// The plan of shares for `ctas` CTAs (or pairs), with tiles of TK keys (64 or 128).
+template <int TK>
+cudaError_t launch_paged_plan(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_attn_tc(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl);
 
 }  // namespace mtp

@@ -274,6 +274,12 @@ def test_attend_chunks(H, rows, ctx):
     check_attend(d, *attend(d))
 
 
+def test_attend_many_blocks_under_a_window():
+    """Every block begins with a tile of four visible keys, so that its maximum grows later."""
+    d = make_latent([150, 90, 120], [6000, 600, 3000], 40, 256, 32, 32, seed=1, window=1500, sinks=4)
+    check_attend(d, *attend(d))
+
+
 def test_attend_long_contexts_split_and_joined():
     d = make_latent([2, 1], [6000, 9000], 16, 512, 64, 64, seed=1)
     check_attend(d, *attend(d))
