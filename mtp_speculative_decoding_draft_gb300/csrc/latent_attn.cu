@@ -3,8 +3,8 @@
 // Every head of a row reads the same cached row: R + Dr elements as key, the first R
 // as value.  A block is 64 packed rows (tokens x heads); with more heads than that, a
 // block holds part of a token's heads.  Its items are cut and dealt out by the plan of
-// paged_attn_tc.cu, a CTA an SM, tiles of 64 keys:
-//   S = Q K_i^T     64 x 64, over R + 64 elements; both operands in shared memory by TMA
+// paged_attn_tc.cu, a CTA an SM, tiles of 32 or 64 keys:
+//   S = Q K_i^T     64 rows, over R + 64 elements; both operands in shared memory by TMA
 //   P = 2^(S - m)   two threads a row, half of the keys each
 //   O += P V_i      V_i the first R elements of K_i as they lie in shared memory
 //                   (row-major keys: the MN-major form of operand B)
@@ -16,8 +16,7 @@
 // S of 64 rows arrives in the lanes l < 16 of each 32.
 //
 // S_{i+1} is issued ahead of O += P_i V_i, so that the softmax of one tile runs under
-// the products of another.  Tensor memory (512 columns): O 256 | S_0 64 | S_1 64 |
-// P_0 64 | P_1 64.  Warps 0-3 are the softmax, warp 4 brings pages, warp 5 issues the
+// the products of another.  Tensor memory (512 columns): O 256 | S_0 S_1 128 | P_0 P_1 128.  Warps 0-3 are the softmax, warp 4 brings pages, warp 5 issues the
 // products, warp 6 brings the next block's queries, warp 7 clears rows that no row sees.
 #include "internal.h"
 #include "latent.cuh"
@@ -33,24 +32,41 @@ bool make_rows_map(CUtensorMap *m, const void *base, uint64_t width, uint64_t ro
 
 namespace {
 
-constexpr int kTK = 64;    // keys per tile
 constexpr int kRows = 64;  // packed rows of a block
 constexpr int kThreads = 256;
-constexpr int kItemCost = 4;
 constexpr int kProducer = 4, kIssuer = 5, kQuery = 6, kClear = 7;
 constexpr unsigned kFull = 0xffffffffu;
 
 template <int R>
 struct Lay {
-  static constexpr int NB = R / 64 + 1;      // 64-element blocks of a row, the rotary one last
-  static constexpr int BLK = 64 * 128;       // bytes of a block: 64 rows of 128 bytes
-  static constexpr int TILE = NB * BLK;      // a tile of keys, or a block's queries
-  static constexpr int STAGES = R == 512 ? 2 : 4;
-  static constexpr int NG = (NB + 2) / 3;    // groups of up to three blocks that arrive together
-  static constexpr size_t SMEM = (size_t)TILE * (1 + STAGES) + 512;
-  __host__ __device__ static constexpr uint32_t S(int b) { return 256u + 64u * b; }
-  __host__ __device__ static constexpr uint32_t P(int b) { return 384u + 64u * b; }
+  static constexpr int TK = R == 512 ? 32 : 64;  // keys per tile
+  static constexpr int NB = R / 64 + 1;          // 64-element blocks of a row, the rotary one last
+  static constexpr int BLK = TK * 128;           // bytes of a block of a tile: rows of 128 bytes
+  static constexpr int TILE = NB * BLK;
+  static constexpr int QBLK = kRows * 128, QTILE = NB * QBLK;
+  static constexpr int STAGES = 4;
+  static constexpr int NG = (NB + 2) / 3;        // groups of up to three blocks that arrive together
+  static constexpr size_t SMEM = (size_t)QTILE + STAGES * TILE + 512;
+  __host__ __device__ static constexpr uint32_t S(int b) { return 256u + TK * b; }
+  __host__ __device__ static constexpr uint32_t P(int b) { return 384u + TK * b; }
 };
+
+// A thread's scores of a tile: the lanes l < 16 hold a row's, and lane l + 16 takes its
+// second half from lane l.
+template <int KH>
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&s)[KH], int lane) {
+  uint32_t t[2][32];
+#pragma unroll
+  for (int c = 0; c < KH / 16; ++c) tmem_ld32_async(taddr + 32 * c, t[c]);
+  tmem_wait_ld();
+#pragma unroll
+  for (int c = 0; c < KH / 16; ++c) pin32(t[c]);
+#pragma unroll
+  for (int e = 0; e < KH; ++e) {
+    const uint32_t v = __shfl_sync(kFull, t[(KH + e) / 32][(KH + e) % 32], lane & 15);
+    s[e] = lane < 16 ? t[e / 32][e % 32] : v;
+  }
+}
 
 }  // namespace
 
@@ -58,10 +74,10 @@ template <int R>
 __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_constant__ PagedTcParams sp) {
   trace_start(kTkLatentAttn);
   using L = Lay<R>;
-  constexpr int NB = L::NB, ST = L::STAGES, NG = L::NG;
+  constexpr int TK = L::TK, NB = L::NB, ST = L::STAGES, NG = L::NG;
   const PagedArgs &p = sp.a;
   extern __shared__ __align__(1024) unsigned char smem[];
-  unsigned char *qbuf = smem, *ring = smem + L::TILE;
+  unsigned char *qbuf = smem, *ring = smem + L::QTILE;
   uint64_t *full = reinterpret_cast<uint64_t *>(ring + ST * L::TILE);  // [stages][groups]
   uint64_t *empty = full + ST * NG, *zbar = empty + ST;
   uint64_t *q_full = zbar + ST, *q_empty = q_full + 1, *drain = q_full + 2;
@@ -89,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   grid_dep_wait();
   trace_dep(kTkLatentAttn);
   grid_dep_launch();
-  PlanWalk<kTK> w(sp, blockIdx.x);
+  PlanWalk<TK> w(sp, blockIdx.x);
   if (tid == 0) p.desc[blockIdx.x].rows = 0;
   if (!w.valid()) {  // the same for the whole CTA
     trace_end(kTkLatentAttn);
@@ -104,12 +120,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
 
   if (warp == kProducer) {
     // -------------------------------------------------- pages into the ring
-    const int prow = min(p.page, kTK), npc = kTK / prow;  // rows and number of a tile's pieces
+    const int prow = min(p.page, TK), npc = TK / prow;  // rows and number of a tile's pieces
     int it = 0;
     for (; w.valid() && ok; w.next()) {
       // the piece of this lane in tile i: whether a row sees it, and its row of the pool
       auto locate = [&](int i, bool &need, int &y) {
-        const int k0 = w.r.tile(i) * kTK + lane * prow;
+        const int k0 = w.r.tile(i) * TK + lane * prow;
         need = lane < npc && w.r.any(k0, k0 + prow);
         y = need ? paged_page(p, w.b, k0) * p.page + (k0 & (p.page - 1)) : 0;
       };
@@ -117,10 +133,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       int y, y_next = 0;
       locate(w.i0, need, y);
       for (int i = w.i0; i < w.i1 && ok; ++i, ++it, need = need_next, y = y_next) {
-        const int t0 = w.r.tile(i) * kTK, s = it % ST;
+        const int t0 = w.r.tile(i) * TK, s = it % ST;
         if (i + 1 < w.i1) locate(i + 1, need_next, y_next);  // its table entry loads under this tile's waits
         const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, need)) * prow * 128);
-        const bool whole = (t0 + kTK <= w.r.hi && t0 >= w.r.lo) || t0 + kTK <= w.r.sink_end;
+        const bool whole = (t0 + TK <= w.r.hi && t0 >= w.r.lo) || t0 + TK <= w.r.sink_end;
         if (it >= ST) ok = mbar_wait(&empty[s], (uint32_t)((it / ST) - 1) & 1u, p.status);
         ok = __all_sync(kFull, ok);
         if (!ok) break;
@@ -152,12 +168,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     int it = 0;
     for (; w.valid() && ok; w.next()) {
       for (int i = w.i0; i < w.i1 && ok; ++i, ++it) {
-        const int t0 = w.r.tile(i) * kTK, s = it % ST;
-        if ((t0 + kTK <= w.r.hi && t0 >= w.r.lo) || t0 + kTK <= w.r.sink_end) continue;
+        const int t0 = w.r.tile(i) * TK, s = it % ST;
+        if ((t0 + TK <= w.r.hi && t0 >= w.r.lo) || t0 + TK <= w.r.sink_end) continue;
         ok = __all_sync(kFull, mbar_wait(&zbar[s], phases >> s & 1u, p.status));
         phases ^= 1u << s;
         unsigned char *tile = ring + (size_t)s * L::TILE;
-        for (int x = lane; x < kTK * 8; x += 32)
+        for (int x = lane; x < TK * 8; x += 32)
           if (!w.r.sees(t0 + (x >> 3)))
 #pragma unroll
             for (int hb = 0; hb < NB; ++hb)
@@ -173,14 +189,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       for (int seg = 0; w.valid(); w.next(), ++seg) {
         if (seg > 0 && !mbar_wait(q_empty, (uint32_t)(seg - 1) & 1u, p.status)) break;
         mbar_arrive_expect_tx(q_full, (uint32_t)(NB * p.tpb * p.G * 128));
-        for (int x = 0; x < NB; ++x) tma_3d(qbuf + x * L::BLK, &sp.mq, 64 * x, w.h * p.G, w.s.row0 + w.t0, q_full);
+        for (int x = 0; x < NB; ++x) tma_3d(qbuf + x * L::QBLK, &sp.mq, 64 * x, w.h * p.G, w.s.row0 + w.t0, q_full);
       }
     }
     __syncwarp();
   } else if (warp == kIssuer) {
     // -------------------------------------------------- matrix products
     // The whole warp walks and waits, one elected lane issues (paged_attn_tc.cu).
-    constexpr uint32_t id_s = idesc_bf16_f32(64, kTK), id_o = idesc_bf16_f32(128, R / 2) | (1u << 16);
+    constexpr uint32_t id_s = idesc_bf16_f32(64, TK), id_o = idesc_bf16_f32(128, R / 2) | (1u << 16);
     const uint32_t tm = __shfl_sync(kFull, tmem, 0);
     const uint64_t qd = sw128_kmajor_desc(smem_u32(qbuf)), kd = sw128_kmajor_desc(smem_u32(ring)),
                    vd = sw128_mnmajor_desc(smem_u32(ring), L::BLK);
@@ -209,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
               for (int x = 3 * g; x < 3 * g + 3 && x < NB; ++x)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const uint64_t off = (uint64_t)((x * L::BLK + k * 32) >> 4);
-                  mma_bf16(d, qd + off, kk + off, id_s, x > 0 || k > 0);
+                  mma_bf16(d, qd + (uint64_t)((x * L::QBLK + k * 32) >> 4), kk + (uint64_t)((x * L::BLK + k * 32) >> 4), id_s,
+                           x > 0 || k > 0);
                 }
             }
           }
@@ -234,8 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int k = 0; k < kTK / 16; ++k)
-                mma_ts(tm, tm + L::P(j & 1) + 32 * h + 8 * k, v + (uint64_t)((h * (R / 128) * L::BLK + k * 2048) >> 4), id_o,
+              for (int k = 0; k < TK / 16; ++k)
+                mma_ts(tm, tm + L::P(j & 1) + TK / 2 * h + 8 * k, v + (uint64_t)((h * (R / 128) * L::BLK + k * 2048) >> 4), id_o,
                        h > 0 || k > 0 || i > 1);
             mma_commit(&empty[s]);
             mma_commit(&o_done[j & 1]);
@@ -248,10 +264,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     __syncwarp();
     mbar_wait(drain, 0, p.status);
   } else {
-    // -------------------------------------------------- softmax: two threads a row, 32 keys each
+    // -------------------------------------------------- softmax: two threads a row, half of the keys each
     const uint32_t lanebase = (uint32_t)(warp * 32) << 16;
     const uint32_t to = tmem + lanebase;
     const int row = 16 * warp + (lane & 15), half = lane >> 4;
+    constexpr int KH = TK / 2;  // keys of a thread
     int it = 0;
     for (; w.valid(); w.next()) {
       const int ntok = w.t1() - w.t0;
@@ -263,32 +280,23 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       const int all_lo = p.window > 0 ? max(0, w.s.ctx + w.t1() - 1 - p.window + 1) : 0;
       float m = -INFINITY, l = 0.f;  // of the row; the sum of this thread's keys
       for (int i = w.i0; i < w.i1; ++i, ++it) {
-        const int k0 = w.r.tile(i) * kTK;
-        const bool whole = k0 + kTK <= all_hi && (k0 >= all_lo || k0 + kTK <= min(p.sinks, all_hi));
+        const int k0 = w.r.tile(i) * TK;
+        const bool whole = k0 + TK <= all_hi && (k0 >= all_lo || k0 + TK <= min(p.sinks, all_hi));
         if (ok) ok = mbar_wait(&s_full[it & 1], (uint32_t)(it >> 1) & 1u, p.status);
         __syncwarp();
         tc_fence_after();
-        uint32_t s[32], t[32];
-        tmem_ld32_async(tmem + lanebase + L::S(it & 1), s);
-        tmem_ld32_async(tmem + lanebase + L::S(it & 1) + 32, t);
-        tmem_wait_ld();
-        pin32(s);
-        pin32(t);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const uint32_t v = __shfl_sync(kFull, t[e], lane & 15);
-          if (half) s[e] = v;
-        }
+        uint32_t s[KH];
+        load_scores<KH>(tmem + lanebase + L::S(it & 1), s, lane);
         if (!whole) {
-          const int b = k0 + 32 * half;  // the row's view of 32 keys as bits
+          const int b = k0 + KH * half;  // the row's view of its keys as bits
           const uint32_t see = below(rhi - b) & (~below(rlo - b) | below(p.sinks - b));
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
+          for (int e = 0; e < KH; ++e)
             if (!(see >> e & 1u)) s[e] = 0xff800000u;
         }
         float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 32; e += 2)
+        for (int e = 0; e < KH; e += 2)
           x[(e >> 1) & 3] = max3(x[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16)) * p.scale_log2;
@@ -319,25 +327,26 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
         const float u = m == -INFINITY ? 0.f : m;
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nu2 = make_float2(-u, -u);
         float2 sum = make_float2(0.f, 0.f);
-        uint32_t pk[32];  // the row's weights, in key order
+        uint32_t pk[KH];  // the row's weights, in key order
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < KH / 2; ++e) {
           float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), sc2, nu2);
           y.x = ex2_approx(y.x);
           y.y = ex2_approx(y.y);
           sum = add2(sum, y);
           const uint32_t mine = pack2(y.x, y.y), other = __shfl_xor_sync(kFull, mine, 16);
           pk[e] = half ? other : mine;
-          pk[16 + e] = half ? mine : other;
+          pk[KH / 2 + e] = half ? mine : other;
         }
         l += sum.x + sum.y;
-        uint32_t z[32];
+        // [P; 0], then [0; P]
 #pragma unroll
-        for (int e = 0; e < 32; ++e) z[e] = half ? 0u : pk[e];
-        tmem_st32(tmem + lanebase + L::P(it & 1), z);
+        for (int c = 0; c < TK / 32; ++c) {
+          uint32_t z[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) z[e] = half ? pk[e] : 0u;
-        tmem_st32(tmem + lanebase + L::P(it & 1) + 32, z);
+          for (int e = 0; e < 32; ++e) z[e] = ((32 * c + e) / KH == half) ? pk[(32 * c + e) % KH] : 0u;
+          tmem_st32(tmem + lanebase + L::P(it & 1) + 32 * c, z);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -433,6 +442,8 @@ void block_shape(int B, int n_rows, int H, int *G, int *hb) {
 
 template <int R>
 cudaError_t launch(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl) {
+  cudaError_t e = launch_paged_plan<Lay<R>::TK>(sp, ctas, s, pdl);
+  if (e) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
@@ -444,7 +455,7 @@ cudaError_t launch(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl) 
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   note_launch();
-  cudaError_t e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<R>, sp);
+  e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<R>, sp);
   if (e) return e;
   cfg.gridDim = dim3(3 * ctas);
   cfg.blockDim = dim3(kCombineThreads);
@@ -474,16 +485,15 @@ cudaError_t launch_latent_attn(const LatentAttnArgs &la, void *scratch, int sms,
   a = la.a;
   block_shape(a.B, a.n_rows, a.Hq, &a.G, &a.Hkv);
   a.tpb = kRows / a.G;
-  a.min_tiles = 4;
-  sp.item_cost = kItemCost;
+  const int tk = a.Dh == 512 ? Lay<512>::TK : Lay<256>::TK;
+  a.min_tiles = 256 / tk;
+  sp.item_cost = 256 / tk;
   char *base = static_cast<char *>(scratch);
   bind_region(a, base, n, kRows);
   paged_tc_bind_plan(sp, base + region_bytes(kPagedMaxCtas, kRows, a.Dh));
-  if (!make_rows_map(&sp.mk, la.pages, w, (uint64_t)a.n_pages * a.page, w, a.page < kTK ? a.page : kTK) ||
+  if (!make_rows_map(&sp.mk, la.pages, w, (uint64_t)a.n_pages * a.page, w, a.page < tk ? a.page : tk) ||
       !make_query_map(&sp.mq, a.q, w, a.Hq, a.n_rows, a.ldq, a.G, a.tpb))
     return cudaErrorNotSupported;
-  cudaError_t e = launch_paged_plan<kTK>(sp, n, s, pdl);
-  if (e) return e;
   return a.Dh == 512 ? launch<512>(sp, n, s, pdl) : launch<256>(sp, n, s, pdl);
 }
 

@@ -612,6 +612,7 @@ cudaError_t launch_paged_plan(const PagedTcParams &sp, int ctas, cudaStream_t s,
   note_launch();
   return cudaLaunchKernelEx(&cfg, paged_tc_plan_kernel<TK>, sp, ctas);
 }
+template cudaError_t launch_paged_plan<32>(const PagedTcParams &, int, cudaStream_t, bool);
 template cudaError_t launch_paged_plan<64>(const PagedTcParams &, int, cudaStream_t, bool);
 template cudaError_t launch_paged_plan<128>(const PagedTcParams &, int, cudaStream_t, bool);
 

@@ -99,7 +99,7 @@ cudaError_t paged_tc_set_attributes();
 bool paged_tc_items_ok(int B, int n_rows, int tpb, int Hkv);  // the plan counts items in 31 bits
 size_t paged_tc_plan_bytes(int B, int n_rows, int tpb, int Hkv);
 void paged_tc_bind_plan(PagedTcParams &sp, char *base);
-// The plan of shares for `ctas` CTAs (or pairs), with tiles of TK keys (64 or 128).
+// The plan of shares for `ctas` CTAs (or pairs), with tiles of TK keys (32, 64 or 128).
 template <int TK>
 cudaError_t launch_paged_plan(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_attn_tc(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl);
