@@ -67,5 +67,6 @@ size_t latent_prefill_scratch_bytes(int B, int n_rows, int H, int Dv);
 cudaError_t launch_latent_prefill(const LatentPrefillArgs &lp, void *scratch, int sms, cudaStream_t s, bool pdl);
 
 cudaError_t latent_set_attributes();
+cudaError_t latent_prefill_set_attributes();
 
 }  // namespace mtp

@@ -26,10 +26,6 @@
 
 namespace mtp {
 
-// tensor maps (tc.cu): a pool's rows as [rows, width], boxes of box_rows x 64; queries as
-// [n_rows, Hq, Dh], boxes of tokens x G x 64; 128-byte swizzle
-bool make_rows_map(CUtensorMap *m, const void *base, uint64_t width, uint64_t rows, uint64_t ld, uint32_t box_rows);
-
 namespace {
 
 constexpr int kRows = 64;  // packed rows of a block
@@ -502,6 +498,7 @@ cudaError_t latent_set_attributes() {
       cudaFuncSetAttribute(latent_attn_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<512>::SMEM);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(latent_attn_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<256>::SMEM);
+  if (e == cudaSuccess) e = latent_prefill_set_attributes();
   return e;
 }
 

@@ -1,43 +1,493 @@
-// Attention of a prompt's rows over keys and values of each head.
+// Attention of a prompt's rows over keys and values of each head, on the tensor cores.
+//
+// A head's key is its Dn plain elements beside the Dr rotated ones that all heads
+// share; the two lie in different arrays and meet in shared memory only, so that no
+// array of whole keys is ever written.  The frame is paged_attn_tc.cu's: a CTA holds
+// two groups of 128 query rows of one head that take turns on the tensor core, the
+// items are dealt out by its plan,
+//   S_g = Q_g K_i^T     tcgen05.mma over Dn + 64 elements (a shared part of 32 is
+//                       filled up with zeros by the copies)
+//   P_g = 2^(S_g - m)   one thread a row, P back over S as bf16
+//   O_g += P_g V_i      tcgen05.mma, P from tensor memory, V row-major (MN-major)
+// Queries of 192 elements take 96 KB of shared memory, which leaves 128: the ring is
+// of blocks of 128 keys x 64 elements, each with a barrier of its own, so that a
+// tile's scores start on its first block and each block's place is free again as soon
+// as both groups have read it.
+//
+// Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1, 128 each.  Warps 0-3 and 4-7 are
+// the groups' softmax, warp 8 brings blocks, warp 9 issues the products, warp 10 brings
+// queries, warp 11 clears rows of V that no row sees.
 #include "internal.h"
-#include "latent_rows.cuh"
+#include "latent.cuh"
+#include "paged_combine.cuh"
+#include "paged_tc.cuh"
+#include "tcgen05.cuh"
 
 namespace mtp {
 
-__global__ void __launch_bounds__(128) latent_prefill_kernel(const __grid_constant__ LatentPrefillArgs lp) {
-  const PagedArgs &p = lp.a;
+namespace {
+
+constexpr int kTK = 128;
+constexpr int kThreads = 384;
+constexpr int kItemCost = 6;
+constexpr int kProducer = 8, kIssuer = 9, kQuery = 10, kClear = 11;
+constexpr int kBlk = 128 * 128;  // bytes of a block: 128 rows of 128 bytes
+constexpr int kStages = 8;
+constexpr unsigned kFull = 0xffffffffu;
+
+template <int DN, int DV>
+struct Lay {
+  static constexpr int KB = DN / 64 + 1, VB = DV / 64;  // blocks of a tile's keys and values
+  static constexpr int NB = KB + VB;
+  static constexpr int QTILE = KB * kBlk;               // a group's queries
+  static constexpr size_t SMEM = (size_t)2 * QTILE + kStages * kBlk + 512;
+};
+
+struct PrefillParams {
+  PagedTcParams tc;  // mk: the keys' and values' rows; mv: the shared key parts; mq: the queries
+  int Dn, w;         // plain elements of a key; elements of a head in a row
+  int n_keys;
+  const int *key_start;
+};
+
+}  // namespace
+
+template <int DN, int DV>
+__global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __grid_constant__ PrefillParams pp) {
   trace_start(kTkLatentPrefill);
+  using L = Lay<DN, DV>;
+  constexpr int KB = L::KB, VB = L::VB, NB = L::NB, ST = kStages;
+  const PagedTcParams &sp = pp.tc;
+  const PagedArgs &p = sp.a;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char *qbuf = smem;  // [2 groups][blocks][128][128 B]
+  unsigned char *ring = smem + 2 * L::QTILE;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(ring + ST * kBlk);
+  uint64_t *full = bars, *empty = bars + ST, *zbar = bars + 2 * ST;
+  uint64_t *q_full = bars + 3 * ST, *q_empty = q_full + 1, *drain = q_full + 2;
+  uint64_t *s_full = q_full + 3, *p_full = s_full + 2, *o_full = s_full + 4, *o_empty = s_full + 6, *p_half = s_full + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 10);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr uint32_t kS = 0, kO = 256;  // columns of S_0 and O_0, the second group's 128 further
+
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&zbar[s], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(drain, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&s_full[g], 1);
+      mbar_init(&p_full[g], 4);
+      mbar_init(&p_half[g], 4);
+      mbar_init(&o_full[g], 1);
+      mbar_init(&o_empty[g], 4);
+    }
+    fence_barrier_init();
+  }
   grid_dep_wait();
   trace_dep(kTkLatentPrefill);
   grid_dep_launch();
-  const int row = blockIdx.x;
-  int b;
-  PagedSeq s;
-  if (!find_row(p, row, &b, &s)) return;
-  const int first = __ldcg(&lp.key_start[b]);
-  if (first < 0 || (long long)first + s.ctx + s.n > lp.n_keys) {
-    set_status(p.status, kStatusBadCtx);
+  PlanWalk<kTK> w(sp, blockIdx.x);
+  if (tid == 0) p.desc[blockIdx.x].rows = 0;
+  if (!w.valid()) {  // the same for the whole CTA
+    trace_end(kTkLatentPrefill);
     return;
   }
-  const int w = lp.Dn + lp.Dv, dk = lp.Dn + lp.Dr;
-  for (int h = threadIdx.x >> 5; h < p.Hq; h += 4) {
-    auto key = [&](int j, int e) {
-      const long long r = first + j;
-      return (uint32_t)(e < lp.Dn ? lp.kv[r * lp.ldkv + h * w + e] : lp.k_rope[r * lp.ldkr + e - lp.Dn]);
-    };
-    auto val = [&](int j, int e) { return (uint32_t)lp.kv[(long long)(first + j) * lp.ldkv + h * w + lp.Dn + e]; };
-    attend_row<192, 128>(p, s, row, h, p.q + (long long)row * p.ldq + h * dk, dk, lp.Dv, key, val);
+  if (warp == kIssuer) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+
+  // registers as in paged_attn_tc.cu: 384 x 168 = 256 x 216 + 128 x 72
+  if (warp >= kProducer) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kProducer) {
+      // ------------------------------------------------ blocks of keys and values into the ring
+      int it = 0;
+      for (; w.valid() && ok; w.next()) {
+        const int first = __ldcg(&pp.key_start[w.b]);
+        if (lane == 0 && w.starts() && (first < 0 || (long long)first + w.s.ctx + w.s.n > pp.n_keys))
+          set_status(p.status, kStatusBadCtx);
+        for (int i = w.i0; i < w.i1 && ok; ++i) {
+          const int t0 = w.r.tile(i) * kTK;
+          // past the keys, either way, the copies read zeros
+          const int y = (int)min(max((long long)first + t0, -(1ll << 30)), 1ll << 30);
+          const bool whole = (t0 + kTK <= w.r.hi && t0 >= w.r.lo) || t0 + kTK <= w.r.sink_end;
+          for (int x = 0; x < NB && ok; ++x, ++it) {
+            const int s = it % ST;
+            if (it >= ST) ok = mbar_wait(&empty[s], (uint32_t)((it / ST) - 1) & 1u, p.status);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            if (lane == 0) {
+              // a block of V with rows to clear goes to the clearing warp first
+              uint64_t *bar = x >= KB && !whole ? &zbar[s] : &full[s];
+              mbar_arrive_expect_tx(bar, kBlk);
+              if (x == KB - 1) tma_2d(ring + s * kBlk, &sp.mv, 0, y, bar);
+              else tma_2d(ring + s * kBlk, &sp.mk, w.h * pp.w + (x < KB ? 64 * x : DN + 64 * (x - KB)), y, bar);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (!ok)  // let copies still in flight land before the CTA exits
+        for (int i = max(0, it - ST); i < it; ++i)
+          if (!mbar_wait(&full[i % ST], (uint32_t)(i / ST) & 1u, p.status)) break;
+    } else if (warp == kClear) {
+      // ------------------------------------------------ rows of V that no row sees
+      uint32_t phases = 0;  // a bit a stage
+      int it = KB;
+      for (; w.valid() && ok; w.next()) {
+        for (int i = w.i0; i < w.i1 && ok; ++i, it += NB) {
+          const int t0 = w.r.tile(i) * kTK;
+          if ((t0 + kTK <= w.r.hi && t0 >= w.r.lo) || t0 + kTK <= w.r.sink_end) continue;
+          for (int v = 0; v < VB && ok; ++v) {
+            const int s = (it + v) % ST;
+            ok = __all_sync(kFull, mbar_wait(&zbar[s], phases >> s & 1u, p.status));
+            phases ^= 1u << s;
+            unsigned char *blk = ring + s * kBlk;
+            for (int x = lane; x < kTK * 8; x += 32)
+              if (!w.r.sees(t0 + (x >> 3))) *reinterpret_cast<uint4 *>(blk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+          }
+        }
+      }
+    } else if (warp == kQuery) {
+      // ------------------------------------------------ the blocks' queries
+      if (lane == 0) {
+        for (int seg = 0; w.valid(); w.next(), ++seg) {
+          const int ng = w.t1() - w.t0 > 128 ? 2 : 1;
+          if (seg > 0 && !mbar_wait(q_empty, (uint32_t)(seg - 1) & 1u, p.status)) break;
+          mbar_arrive_expect_tx(q_full, (uint32_t)(ng * KB * kBlk));
+          for (int g = 0; g < ng; ++g)
+            for (int x = 0; x < KB; ++x)
+              tma_3d(qbuf + g * L::QTILE + x * kBlk, &sp.mq, 64 * x, w.h, w.s.row0 + w.t0 + g * 128, q_full);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kIssuer) {
+      // ------------------------------------------------ matrix products
+      // The whole warp walks and waits, one elected lane issues (paged_attn_tc.cu).
+      constexpr uint32_t id_s = idesc_bf16_f32(128, 128), id_o = idesc_bf16_f32(128, DV) | (1u << 16),
+                         id_o1 = idesc_bf16_f32(128, 64) | (1u << 16);
+      const uint32_t tm = __shfl_sync(kFull, tmem, 0);
+      const uint64_t qd = sw128_kmajor_desc(smem_u32(qbuf)), kd = sw128_kmajor_desc(smem_u32(ring)),
+                     vd = sw128_mnmajor_desc(smem_u32(ring), kBlk);
+      const bool leader = elect_one();
+      // A wait that gives up flags the status; the waits after it are skipped and
+      // the rest is issued on whatever is there, so that no barrier is left short.
+      auto await = [&](uint64_t *bar, uint32_t parity) {
+        if (ok) ok = mbar_wait(bar, parity, p.status);
+      };
+      int kb = 0, vb = 0, seg = 0;  // the tile's first block of keys, and of the values of the tile before
+      uint32_t pph[2] = {0, 0}, oph[2] = {1, 1};
+      for (; __shfl_sync(kFull, w.valid(), 0); w.next(), ++seg) {
+        const int ng = __shfl_sync(kFull, w.t1() - w.t0 > 128 ? 2 : 1, 0), nt = __shfl_sync(kFull, w.i1 - w.i0, 0);
+        await(q_full, (uint32_t)seg & 1u);
+        for (int i = 0; i <= nt; ++i) {
+          const int vs = vb % ST;
+          if (i > 0)
+#pragma unroll
+            for (int v = 0; v < VB; ++v) await(&full[(vb + v) % ST], (uint32_t)((vb + v) / ST) & 1u);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (g >= ng) break;
+            if (i > 0) {
+              // k-steps [k0, k1) of the product with V, whose blocks may part at the ring's end
+              auto product = [&](int k0, int k1) {
+                const uint64_t v = vd + (uint64_t)(vs * (kBlk >> 4));
+                if (VB == 1 || vs + 1 < ST) {
+                  for (int k = k0; k < k1; ++k)
+                    mma_ts(tm + kO + 128 * g, tm + kS + 128 * g + 8 * k, v + (uint64_t)(k * (2048 >> 4)), id_o, k > 0 || i > 1);
+                } else {
+                  for (int k = k0; k < k1; ++k) {
+                    mma_ts(tm + kO + 128 * g, tm + kS + 128 * g + 8 * k, v + (uint64_t)(k * (2048 >> 4)), id_o1, k > 0 || i > 1);
+                    mma_ts(tm + kO + 128 * g + 64, tm + kS + 128 * g + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), id_o1,
+                           k > 0 || i > 1);
+                  }
+                }
+              };
+              if (i == 1) {
+                await(&o_empty[g], oph[g]);
+                oph[g] ^= 1u;
+              }
+              await(&p_half[g], pph[g]);
+              tc_fence_after();
+              if (leader) product(0, kTK / 32);
+              await(&p_full[g], pph[g]);
+              pph[g] ^= 1u;
+              tc_fence_after();
+              if (leader) {
+                product(kTK / 32, kTK / 16);
+                if (i == nt) mma_commit(&o_full[g]);
+              }
+            }
+            if (i < nt) {
+              const uint64_t q = qd + (uint64_t)(g * (L::QTILE >> 4));
+#pragma unroll
+              for (int x = 0; x < KB; ++x) {
+                const int s = (kb + x) % ST;
+                if (g == 0) await(&full[s], (uint32_t)((kb + x) / ST) & 1u);
+                tc_fence_after();
+                if (leader) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    mma_bf16(tm + kS + 128 * g, q + (uint64_t)((x * kBlk + k * 32) >> 4),
+                             kd + (uint64_t)((s * kBlk + k * 32) >> 4), id_s, x > 0 || k > 0);
+                }
+              }
+              if (leader) mma_commit(&s_full[g]);
+            }
+          }
+          if (leader) {
+            if (i > 0)
+#pragma unroll
+              for (int v = 0; v < VB; ++v) mma_commit(&empty[(vb + v) % ST]);
+            if (i < nt)
+#pragma unroll
+              for (int x = 0; x < KB; ++x) mma_commit(&empty[(kb + x) % ST]);
+            if (i == nt - 1) mma_commit(q_empty);  // the block's last scores
+          }
+          __syncwarp();
+          vb = kb + KB;
+          if (i < nt) kb += NB;
+        }
+      }
+      if (leader) mma_commit(drain);  // nothing of this CTA is in flight when it frees its tensor memory
+      __syncwarp();
+      mbar_wait(drain, 0, p.status);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // ------------------------------------------------ softmax: a thread a row
+    const int g = warp >> 2, row = tid & 127;
+    const uint32_t lanebase = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanebase + kS + 128 * g, to = tmem + lanebase + kO + 128 * g;
+    int ns = 0, nseg = 0;
+    for (; w.valid(); w.next()) {
+      const int ntok = w.t1() - w.t0;
+      if (g == 1 && ntok <= 128) continue;
+      const int tg0 = w.t0 + g * 128, tg1 = min(w.t1(), tg0 + 128);  // the group's rows
+      const int tok = min(tg0 + row, tg1 - 1);
+      const bool live = tg0 + row < tg1;
+      const int pos = w.s.ctx + tok;
+      const int rhi = min(pos + 1, p.cap), rlo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      const int all_hi = min(w.s.ctx + tg0 + 1, p.cap);
+      const int all_lo = p.window > 0 ? max(0, w.s.ctx + tg1 - 1 - p.window + 1) : 0;
+      float m = -INFINITY, l = 0.f;
+      for (int i = w.i0; i < w.i1; ++i) {
+        const int k0 = w.r.tile(i) * kTK;
+        const bool whole = k0 + kTK <= all_hi && (k0 >= all_lo || k0 + kTK <= min(p.sinks, all_hi));
+        if (ok) ok = mbar_wait(&s_full[g], (uint32_t)(ns++) & 1u, p.status);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_async(ts + 32 * c, s + 32 * c);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) pin32(s + 32 * c);
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int b = k0 + 32 * c;  // the row's view of 32 keys as bits
+            const uint32_t see = below(rhi - b) & (~below(rlo - b) | below(p.sinks - b));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(see >> e & 1u)) s[32 * c + e] = 0xff800000u;
+          }
+        }
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 128; e += 2)
+          x[(e >> 1) & 3] = max3(x[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+        const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
+        if (__any_sync(kFull, live && mx > m + 8.f)) {
+          const float n = fmaxf(m, mx);
+          const float f = n == m ? 1.f : exp2f(m - n);
+          m = n;
+          l *= f;
+          if (i > w.i0) {
+#pragma unroll 1
+            for (int c = 0; c < DV / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32_async(to + 32 * c, o);
+              tmem_wait_ld();
+              pin32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(to + 32 * c, o);
+            }
+          }
+        }
+        const float u = m == -INFINITY ? 0.f : m;
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nu2 = make_float2(-u, -u);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float2 sc = make_float2(__uint_as_float(s[64 * c + 2 * e]), __uint_as_float(s[64 * c + 2 * e + 1]));
+            float2 y = fma2(sc, sc2, nu2);
+            y.x = ex2_approx(y.x);
+            y.y = ex2_approx(y.y);
+            sum[e & 1] = add2(sum[e & 1], y);
+            pk[e] = pack2(y.x, y.y);
+          }
+          tmem_st32(ts + 32 * c, pk);
+          // the product over the first half of the keys starts under the second half's exponentials
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(c == 0 ? &p_half[g] : &p_full[g]);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      }
+      // ---- the block's output, or this segment's state
+      if (ok) ok = mbar_wait(&o_full[g], (uint32_t)(nseg++) & 1u, p.status);
+      __syncwarp();
+      tc_fence_after();
+      const bool whole_item = w.starts() && w.ends();
+      const int slot = w.starts() ? 1 : 0;
+      const int qrow = w.s.row0 + tok;
+      const bool mine = live && in_bounds(qrow < p.n_rows, p.status);
+      const float inv = paged_inverse(l);
+      const size_t pr = ((size_t)blockIdx.x * 2 + slot) * kPagedTcRows + g * 128 + row;
+#pragma unroll 1
+      for (int c = 0; c < DV / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32_async(to + 32 * c, o);
+        tmem_wait_ld();
+        pin32(o);
+        if (!whole_item) {
+          uint4 v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          store_quads<8>(v, mine ? p.part_o + pr * DV + 32 * c : nullptr, lane);
+        } else {
+          uint16_t *d = static_cast<uint16_t *>(p.out) + (long long)qrow * p.ldo + w.h * DV + 32 * c;
+          uint4 v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              y[j] = pack2(__uint_as_float(o[8 * e + 2 * j]) * inv, __uint_as_float(o[8 * e + 2 * j + 1]) * inv);
+            v[e] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+          store_quads<4>(v, mine ? d : nullptr, lane);
+        }
+      }
+      if (mine) {
+        if (!whole_item) {
+          p.part_ml[pr * 2] = m;
+          p.part_ml[pr * 2 + 1] = l;
+        } else if (p.lse) {
+          p.lse[(size_t)qrow * p.Hq + w.h] = paged_lse(m, l);
+        }
+      }
+      if (tid == 0 && w.starts() && !w.ends()) {
+        PagedDesc d;
+        d.row0 = w.s.row0 + w.t0;
+        d.rows = ntok;
+        d.h = w.h;
+        d.last_cta = w.last_cta();
+        p.desc[blockIdx.x] = d;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_empty[g]);
+    }
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssuer) tmem_dealloc(tmem, 512);
   trace_end(kTkLatentPrefill);
 }
 
-bool latent_prefill_items_ok(int, int, int) { return true; }
-size_t latent_prefill_scratch_bytes(int, int, int, int) { return 256; }
+// ---------------------------------------------------------------- host side
 
-cudaError_t launch_latent_prefill(const LatentPrefillArgs &lp, void *, int, cudaStream_t s, bool) {
+namespace {
+
+constexpr int kTpb = 2 * 128;
+
+cudaLaunchConfig_t config(int ctas, int threads, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr, bool pdl) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cfg;
+}
+
+template <int DN, int DV>
+cudaError_t launch(const PrefillParams &pp, int ctas, cudaStream_t s, bool pdl) {
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config(ctas, kThreads, Lay<DN, DV>::SMEM, s, attr, pdl);
   note_launch();
-  latent_prefill_kernel<<<lp.a.n_rows, 128, 0, s>>>(lp);
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, latent_prefill_kernel<DN, DV>, pp);
+}
+
+template <int DN, int DV>
+cudaError_t set_smem() {
+  return cudaFuncSetAttribute(latent_prefill_kernel<DN, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)Lay<DN, DV>::SMEM);
+}
+
+}  // namespace
+
+bool latent_prefill_items_ok(int B, int n_rows, int H) { return paged_tc_items_ok(B, n_rows, kTpb, H); }
+
+size_t latent_prefill_scratch_bytes(int B, int n_rows, int H, int Dv) {
+  return region_bytes(kPagedMaxCtas, kPagedTcRows, Dv) + paged_tc_plan_bytes(B, n_rows, kTpb, H);
+}
+
+cudaError_t launch_latent_prefill(const LatentPrefillArgs &lp, void *scratch, int sms, cudaStream_t s, bool pdl) {
+  const int n = sms < kPagedMaxCtas ? sms : kPagedMaxCtas;
+  PrefillParams pp{};
+  PagedArgs &a = pp.tc.a;
+  a = lp.a;
+  a.tpb = kTpb;
+  a.min_tiles = 2;
+  pp.tc.item_cost = kItemCost;
+  pp.Dn = lp.Dn;
+  pp.w = lp.Dn + lp.Dv;
+  pp.n_keys = lp.n_keys;
+  pp.key_start = lp.key_start;
+  char *base = static_cast<char *>(scratch);
+  bind_region(a, base, n, kPagedTcRows);
+  paged_tc_bind_plan(pp.tc, base + region_bytes(kPagedMaxCtas, kPagedTcRows, a.Dh));
+  if (!make_rows_map(&pp.tc.mk, lp.kv, (uint64_t)a.Hq * pp.w, lp.n_keys, lp.ldkv, kTK) ||
+      !make_rows_map(&pp.tc.mv, lp.k_rope, lp.Dr, lp.n_keys, lp.ldkr, kTK) ||
+      !make_query_map(&pp.tc.mq, a.q, lp.Dn + lp.Dr, a.Hq, a.n_rows, a.ldq, 1, 128))
+    return cudaErrorNotSupported;
+  cudaError_t e = launch_paged_plan<kTK>(pp.tc, n, s, pdl);
+  if (e) return e;
+  if (lp.Dn == 128) e = lp.Dv == 128 ? launch<128, 128>(pp, n, s, pdl) : launch<128, 64>(pp, n, s, pdl);
+  else e = lp.Dv == 128 ? launch<64, 128>(pp, n, s, pdl) : launch<64, 64>(pp, n, s, pdl);
+  if (e) return e;
+  return launch_paged_combine(a, n, s, pdl);
+}
+
+cudaError_t latent_prefill_set_attributes() {
+  cudaError_t e = set_smem<128, 128>();
+  if (e == cudaSuccess) e = set_smem<128, 64>();
+  if (e == cudaSuccess) e = set_smem<64, 128>();
+  if (e == cudaSuccess) e = set_smem<64, 64>();
+  return e;
 }
 
 MTP_TRACE_COLLECTOR(latent_prefill)

@@ -94,6 +94,8 @@ struct PlanWalk {
 
 // Queries as a 3-D map, boxes of `tokens` x G x 64 elements, 128-byte swizzle (tc.cu).
 bool make_query_map(CUtensorMap *m, const void *q, int Dh, int Hq, int n_rows, long long ldq, int G, int tokens);
+// Rows of `width` elements, ld apart, boxes of box_rows x 64, 128-byte swizzle (tc.cu).
+bool make_rows_map(CUtensorMap *m, const void *base, uint64_t width, uint64_t rows, uint64_t ld, uint32_t box_rows);
 cudaError_t paged_tc_set_attributes();
 // tpb: tokens of a block
 bool paged_tc_items_ok(int B, int n_rows, int tpb, int Hkv);  // the plan counts items in 31 bits
@@ -102,6 +104,8 @@ void paged_tc_bind_plan(PagedTcParams &sp, char *base);
 // The plan of shares for `ctas` CTAs (or pairs), with tiles of TK keys (32, 64 or 128).
 template <int TK>
 cudaError_t launch_paged_plan(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl);
+// Joins the partial states of blocks of kPagedTcRows rows, heads of 64 or 128 (paged_attn.cu).
+cudaError_t launch_paged_combine(const PagedArgs &a, int ctas, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_attn_tc(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl);
 
 }  // namespace mtp
