@@ -68,5 +68,6 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &lp, void *scratch, in
 
 cudaError_t latent_set_attributes();
 cudaError_t latent_prefill_set_attributes();
+cudaError_t latent_heads_set_attributes();
 
 }  // namespace mtp

@@ -499,6 +499,7 @@ cudaError_t latent_set_attributes() {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(latent_attn_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<256>::SMEM);
   if (e == cudaSuccess) e = latent_prefill_set_attributes();
+  if (e == cudaSuccess) e = latent_heads_set_attributes();
   return e;
 }
 

@@ -1,63 +1,298 @@
-// A product a head: y[n, h, :] = W[h] x[n, h, :], from an array of rows or from the
-// pages of a latent cache (then the rows are the cached positions of the sequences
-// and every head reads the same one).
+// A product a head on the tensor cores: y[n, h, :] = W[h] x[n, h, :], from an array of
+// rows or from the pages of a latent cache (then the rows are the first positions of
+// the sequences and every head reads the same ones).
+//
+// One CTA an SM walks tiles of 128 rows x NT outputs of a head, the row tiles of one
+// weight tile next to each other so that the weights come from memory once.  x and W
+// arrive by TMA in blocks of 64 along K, W as it lies: rows along K ([N, K], the
+// K-major form of the operand) or along N ([K, N], the MN-major one).  Two accumulators in
+// tensor memory: a tile's output is written under the next one's products.
+//
+// Tiles of cached rows never cross a sequence, since page pieces start on whole pages.
+// The number of tiles is the device's to know: each CTA sums up the sequences' tiles
+// at its start (a run of sequences a thread) and searches that table for each tile.
 #include "internal.h"
 #include "latent.cuh"
+#include "paged_tc.cuh"
+#include "tcgen05.cuh"
 
 namespace mtp {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 320;  // warps 0-7 write outputs, 8 brings blocks, 9 issues the products
+constexpr int kProducer = 8, kIssuer = 9, kOutThreads = 256;
+constexpr int kABytes = 128 * 128, kBBytes = 256 * 128;  // a stage: 64 of K
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kStages = 4;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr size_t kSmem = (size_t)kStages * kStageBytes + 256;
+
+struct HeadsParams {
+  CUtensorMap mx, mw;
+  LatentHeadsArgs a;
+  int NT, n_tiles, m_tiles;  // outputs of a tile; tiles along N and (from an array) along the rows
+  int kbs, pieces;           // blocks of 64 along K; pieces of a transposed weight block
+};
+
+// A tile of rows: of sequence b (from pages), or of the array.
+struct RowTile {
+  int b, j0, row0, rows;  // sequence, first position, first output row, rows
+};
+
+// The sequences' row tiles before each thread's run of sequences.
+struct TileTable {
+  int before[kThreads + 1];
+  int sums[kThreads / 32];
+};
+
+// Rows of sequence b that are expanded; flags what is out of range.
+__device__ __forceinline__ int seq_rows(const LatentHeadsArgs &p, int b, int *start, bool flag) {
+  const int s = __ldcg(&p.key_start[b]), e = __ldcg(&p.key_start[b + 1]);
+  *start = s;
+  if (s < 0 || e < s || e > p.n_rows) {
+    if (flag) set_status(p.status, kStatusBadRows);
+    return 0;
+  }
+  if (e - s > p.cap && flag) set_status(p.status, kStatusBadCtx);
+  return min(e - s, p.cap);
+}
+
+__device__ __forceinline__ RowTile find_tile(const LatentHeadsArgs &p, const TileTable &t, int m) {
+  RowTile r;
+  if (!p.pages) {
+    r.b = 0;
+    r.j0 = 0;
+    r.row0 = m * 128;
+    r.rows = min(128, p.n_rows - r.row0);
+    return r;
+  }
+  int lo = 0, hi = kThreads;  // before[lo] <= m < before[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (t.before[mid] <= m) lo = mid;
+    else hi = mid;
+  }
+  const int per = (p.B + kThreads - 1) / kThreads;
+  int left = m - t.before[lo];
+  for (int b = lo * per;; ++b) {
+    int s;
+    const int n = seq_rows(p, b, &s, false), k = (n + 127) / 128;
+    if (left < k) {
+      r.b = b;
+      r.j0 = left * 128;
+      r.row0 = s + r.j0;
+      r.rows = min(128, n - r.j0);
+      return r;
+    }
+    left -= k;
+  }
+}
+
+// The page of position j of sequence b; page 0 for an entry outside the pool.
+__device__ __forceinline__ int page_of(const LatentHeadsArgs &p, int b, int j) {
+  const int id = __ldg(&p.page_table[(size_t)b * p.max_pages + (j >> p.page_shift)]);
+  if (id < 0 || id >= p.n_pages) {
+    set_status(p.status, kStatusBadPage);
+    return 0;
+  }
+  return id;
+}
 
 }  // namespace
 
-__global__ void __launch_bounds__(kThreads) latent_heads_kernel(const __grid_constant__ LatentHeadsArgs p) {
+template <bool TRANS>
+__global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_constant__ HeadsParams hp) {
   trace_start(kTkLatentHeads);
+  const LatentHeadsArgs &p = hp.a;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes);
+  uint64_t *empty = full + kStages, *done = empty + kStages, *tfree = done + 2, *drain = tfree + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  __shared__ TileTable table;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&done[b], 1);
+      mbar_init(&tfree[b], kOutThreads / 32);
+    }
+    mbar_init(drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == kIssuer) tmem_alloc(tmem_slot, 512);
   grid_dep_wait();
   trace_dep(kTkLatentHeads);
   grid_dep_launch();
-  const int row = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
-  const uint16_t *x = p.x + (long long)row * p.ldx + h * p.hsx;
+  int m_tiles = hp.m_tiles;
   if (p.pages) {
-    bool bad = false;
-    if (row == 0 && h == 0)
-      for (int i = threadIdx.x; i < p.B; i += kThreads) {
-        const int s = __ldcg(&p.key_start[i]), e = __ldcg(&p.key_start[i + 1]);
-        bad |= s < 0 || e < s || e > p.n_rows;
+    const int per = (p.B + kThreads - 1) / kThreads;
+    int mine = 0;
+    for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
+      int s;
+      mine += (seq_rows(p, b, &s, blockIdx.x == 0) + 127) / 128;
+    }
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) table.sums[warp] = inc;
+    __syncthreads();
+    int before = inc - mine;
+    for (int v = 0; v < warp; ++v) before += table.sums[v];
+    table.before[tid] = before;
+    if (tid == kThreads - 1) table.before[kThreads] = before + mine;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (p.pages) m_tiles = table.before[kThreads];
+  const uint32_t tmem = *tmem_slot;
+  const long long items = (long long)p.H * hp.n_tiles * m_tiles;
+  bool ok = true;
+
+  if (warp == kProducer) {
+    const int prow = p.pages ? min(p.page, 128) : 128, npc = 128 / prow;
+    const uint32_t bbytes = TRANS ? (uint32_t)hp.pieces * 64 * 128 : (uint32_t)hp.NT * 128;
+    uint32_t i = 0;
+    for (long long u = blockIdx.x; u < items && ok; u += gridDim.x) {
+      const int m = (int)(u % m_tiles), hn = (int)(u / m_tiles), h = hn / hp.n_tiles, n0 = (hn % hp.n_tiles) * hp.NT;
+      const RowTile r = find_tile(p, table, m);
+      const bool need = lane < npc && lane * prow < r.rows;
+      const int y = p.pages && need ? page_of(p, r.b, r.j0 + lane * prow) * p.page : 0;
+      const uint32_t abytes = (uint32_t)(__popc(__ballot_sync(kFull, need)) * prow * 128);
+      for (int kb = 0; kb < hp.kbs && ok; ++kb, ++i) {
+        const int s = (int)(i % kStages);
+        if (i >= (uint32_t)kStages) ok = mbar_wait(&empty[s], ((i / kStages) - 1u) & 1u, p.status);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        unsigned char *st = smem + s * kStageBytes;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[s], abytes + bbytes);
+          if (TRANS)
+            for (int x = 0; x < hp.pieces; ++x) tma_3d(st + kABytes + x * 64 * 128, &hp.mw, n0 + 64 * x, kb * 64, h, &full[s]);
+          else
+            tma_3d(st + kABytes, &hp.mw, kb * 64, n0, h, &full[s]);
+        }
+        __syncwarp();
+        if (need) {
+          if (p.pages) tma_2d(st + lane * prow * 128, &hp.mx, kb * 64, y, &full[s]);
+          else tma_3d(st, &hp.mx, kb * 64, h, r.row0, &full[s]);
+        }
       }
-    if (bad) set_status(p.status, kStatusBadRows);
-    const int b = starts_upto(p.key_start, p.B, row, lane) - 1;
-    if (b < 0) return;
-    const int s = __ldcg(&p.key_start[b]), e = __ldcg(&p.key_start[b + 1]), j = row - s;
-    if (row >= e || s < 0) return;
-    if (j >= p.cap) {
-      set_status(p.status, kStatusBadCtx);
-      return;
     }
-    int page = __ldg(&p.page_table[(size_t)b * p.max_pages + (j >> p.page_shift)]);
-    if (page < 0 || page >= p.n_pages) {
-      set_status(p.status, kStatusBadPage);
-      page = 0;
+    if (!ok)  // let copies still in flight land before the CTA exits
+      for (uint32_t q = i > (uint32_t)kStages ? i - kStages : 0u; q < i; ++q)
+        if (!mbar_wait(&full[q % kStages], (q / kStages) & 1u, p.status)) break;
+  } else if (warp == kIssuer) {
+    const uint32_t idesc = idesc_bf16_f32(128, 256) - ((uint32_t)(256 - hp.NT) >> 3 << 17) + (TRANS ? 1u << 16 : 0u);
+    const bool leader = elect_one();
+    const uint64_t ad = sw128_kmajor_desc(smem_u32(smem)),
+                   bd = TRANS ? sw128_mnmajor_desc(smem_u32(smem + kABytes), 64 * 128) : sw128_kmajor_desc(smem_u32(smem + kABytes));
+    uint32_t i = 0, n = 0;
+    for (long long u = blockIdx.x; u < items && ok; u += gridDim.x, ++n) {
+      const uint32_t buf = n & 1u;
+      if (n >= 2) ok = mbar_wait(&tfree[buf], ((n >> 1) - 1u) & 1u, p.status);
+      ok = __all_sync(kFull, ok);
+      if (!ok) break;
+      for (int kb = 0; kb < hp.kbs && ok; ++kb, ++i) {
+        const int s = (int)(i % kStages);
+        ok = __all_sync(kFull, mbar_wait(&full[s], (i / kStages) & 1u, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t so = (uint64_t)(s * (kStageBytes >> 4));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_bf16(tmem + 256 * buf, ad + so + 2 * k, bd + so + (TRANS ? 128 : 2) * k, idesc, (kb | k) != 0);
+          mma_commit(&empty[s]);
+          if (kb == hp.kbs - 1) mma_commit(&done[buf]);
+        }
+        __syncwarp();
+      }
     }
-    x = p.pages + ((size_t)page * p.page + (j & (p.page - 1))) * (size_t)(p.K + p.Dr);
-    if (h == 0 && threadIdx.x < p.Dr) p.k_rope[(long long)row * p.ldkr + threadIdx.x] = x[p.K + threadIdx.x];
+    if (leader) mma_commit(drain);  // nothing of this CTA is in flight when it frees its tensor memory
+    __syncwarp();
+    mbar_wait(drain, 0, p.status);
+  } else {
+    // a thread a row: the warp's lanes of tensor memory, every other 64 outputs
+    const int q = warp & 3;
+    const uint32_t lanebase = (uint32_t)(q * 32) << 16;
+    uint32_t n = 0;
+    for (long long u = blockIdx.x; u < items; u += gridDim.x, ++n) {
+      const int m = (int)(u % m_tiles), hn = (int)(u / m_tiles), h = hn / hp.n_tiles, n0 = (hn % hp.n_tiles) * hp.NT;
+      const RowTile r = find_tile(p, table, m);
+      const uint32_t buf = n & 1u;
+      const int row = q * 32 + lane;
+      const bool real = row < r.rows;
+      if (p.pages && hn == 0 && warp < 4 && real) {
+        // the shared key part of the tile's positions
+        const int j = r.j0 + row;
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            p.pages + ((size_t)page_of(p, r.b, j) * p.page + (j & (p.page - 1))) * (size_t)(p.K + p.Dr) + p.K);
+        uint4 *dst = reinterpret_cast<uint4 *>(p.k_rope + (long long)(r.row0 + row) * p.ldkr);
+        for (int e = 0; e < p.Dr / 8; ++e) dst[e] = __ldg(src + e);
+      }
+      ok = __all_sync(kFull, ok && mbar_wait(&done[buf], (n >> 1) & 1u, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      uint16_t *y = p.y + (long long)(r.row0 + row) * p.ldy + h * p.hsy + n0;
+      const int cols = min(hp.NT, p.N - n0);
+      for (int c = 64 * (warp >> 2); c < cols; c += 128) {
+        uint32_t o[64];
+        tmem_ld32_async(tmem + lanebase + 256 * buf + c, o);
+        tmem_ld32_async(tmem + lanebase + 256 * buf + c + 32, o + 32);
+        tmem_wait_ld();
+        pin32(o);
+        pin32(o + 32);
+        uint4 v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint32_t x[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = pack2(__uint_as_float(o[8 * e + 2 * j]), __uint_as_float(o[8 * e + 2 * j + 1]));
+          v[e] = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+        store_quads<8>(v, real ? y + c : nullptr, lane, (cols - c) / 8);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tfree[buf]);
+    }
   }
-  for (int n = threadIdx.x; n < p.N; n += kThreads) {
-    float acc = 0.f;
-    for (int k = 0; k < p.K; ++k) {
-      const uint16_t *w = p.w + h * p.hsw + (p.transposed ? k * p.ldw + n : n * p.ldw + k);
-      acc = fmaf(bf16_lo(x[k]), bf16_lo(*w), acc);
-    }
-    reinterpret_cast<__nv_bfloat16 *>(p.y)[(long long)row * p.ldy + h * p.hsy + n] = __float2bfloat16_rn(acc);
-  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssuer) tmem_dealloc(tmem, 512);
   trace_end(kTkLatentHeads);
 }
 
-cudaError_t launch_latent_heads(const LatentHeadsArgs &a, int, cudaStream_t s, bool pdl) {
+// ---------------------------------------------------------------- host side
+
+cudaError_t launch_latent_heads(const LatentHeadsArgs &a, int sms, cudaStream_t s, bool pdl) {
+  HeadsParams hp{};
+  hp.a = a;
+  hp.kbs = (a.K + 63) / 64;
+  hp.m_tiles = (a.n_rows + 127) / 128;
+  hp.NT = a.N >= 256 ? 256 : (a.N + 15) / 16 * 16;
+  hp.n_tiles = (a.N + hp.NT - 1) / hp.NT;
+  hp.pieces = (hp.NT + 63) / 64;
+  const bool x_ok = a.pages ? make_rows_map(&hp.mx, a.pages, a.K + a.Dr, (uint64_t)a.n_pages * a.page, a.K + a.Dr, a.page)
+                            : make_heads_map(&hp.mx, a.x, a.K, a.H, a.n_rows, a.hsx, a.ldx, 1, 128);
+  const bool w_ok = a.transposed ? make_heads_map(&hp.mw, a.w, a.N, a.K, a.H, a.ldw, a.hsw, 64, 1)
+                                 : make_heads_map(&hp.mw, a.w, a.K, a.N, a.H, a.ldw, a.hsw, hp.NT, 1);
+  if (!x_ok || !w_ok) return cudaErrorNotSupported;
+  // from pages the device knows how many tiles there are: one more a sequence at most
+  const long long most = (long long)a.H * hp.n_tiles * (a.pages ? hp.m_tiles + a.B : hp.m_tiles);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.n_rows, a.H);
+  cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -65,7 +300,16 @@ cudaError_t launch_latent_heads(const LatentHeadsArgs &a, int, cudaStream_t s, b
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   note_launch();
-  return cudaLaunchKernelEx(&cfg, latent_heads_kernel, a);
+  return a.transposed ? cudaLaunchKernelEx(&cfg, latent_heads_kernel<true>, hp)
+                      : cudaLaunchKernelEx(&cfg, latent_heads_kernel<false>, hp);
+}
+
+cudaError_t latent_heads_set_attributes() {
+  cudaError_t e =
+      cudaFuncSetAttribute(latent_heads_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(latent_heads_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  return e;
 }
 
 MTP_TRACE_COLLECTOR(latent_heads)

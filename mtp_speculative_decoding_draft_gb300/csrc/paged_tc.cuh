@@ -96,6 +96,9 @@ struct PlanWalk {
 bool make_query_map(CUtensorMap *m, const void *q, int Dh, int Hq, int n_rows, long long ldq, int G, int tokens);
 // Rows of `width` elements, ld apart, boxes of box_rows x 64, 128-byte swizzle (tc.cu).
 bool make_rows_map(CUtensorMap *m, const void *base, uint64_t width, uint64_t rows, uint64_t ld, uint32_t box_rows);
+// [d2, d1, d0] with strides s2, s1 (elements), boxes of b2 x b1 x 64 (tc.cu).
+bool make_heads_map(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
+                    uint32_t b1, uint32_t b2);
 cudaError_t paged_tc_set_attributes();
 // tpb: tokens of a block
 bool paged_tc_items_ok(int B, int n_rows, int tpb, int Hkv);  // the plan counts items in 31 bits

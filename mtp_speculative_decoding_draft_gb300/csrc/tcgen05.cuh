@@ -212,14 +212,14 @@ __device__ __forceinline__ void transpose_quads(uint4 (&q)[N], int lane) {
   }
 }
 
-// Stores N quads of each lane's row at the lane's address (null: none).
+// Stores the first n of N quads of each lane's row at the lane's address (null: none).
 template <int N>
-__device__ __forceinline__ void store_quads(uint4 (&q)[N], void *at, int lane) {
+__device__ __forceinline__ void store_quads(uint4 (&q)[N], void *at, int lane, int n = N) {
   transpose_quads<N>(q, lane);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const unsigned long long a = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), (lane & ~(N - 1)) + i);
-    if (a) reinterpret_cast<uint4 *>(a)[lane & (N - 1)] = q[i];
+    if (a && (lane & (N - 1)) < n) reinterpret_cast<uint4 *>(a)[lane & (N - 1)] = q[i];
   }
 }
 
