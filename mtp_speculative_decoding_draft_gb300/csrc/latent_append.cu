@@ -59,7 +59,7 @@ __device__ __forceinline__ typename Bf<VEC>::T pack(const float (&x)[VEC]) {
 }  // namespace
 
 template <int VEC, int U>
-__global__ void __launch_bounds__(32 * kAppWarps) latent_append_kernel(const __grid_constant__ LatentAppendArgs p) {
+__global__ void __launch_bounds__(32 * kAppWarps, U == 1 ? 1 : 5) latent_append_kernel(const __grid_constant__ LatentAppendArgs p) {
   trace_start(kTkLatentAppend);
   using T = typename Bf<VEC>::T;
   __shared__ float2 cs_all[kAppWarps][32];  // rot / 2 <= 32
@@ -265,7 +265,9 @@ cudaError_t launch_latent_append(const LatentAppendArgs &a, cudaStream_t s, bool
   // 16-byte accesses need the pairs' halves in whole vectors
   const bool wide = a.rot % 16 == 0;
   const int items = ((a.q ? a.Hq : 0) + 1) * a.Dr / (wide ? 16 : 8);
-  return wide ? launch_append<8, 1>(a, items, s, pdl) : launch_append<4, 1>(a, items, s, pdl);
+  if ((long long)a.n_rows * items < 152ll * 256)
+    return wide ? launch_append<8, 1>(a, items, s, pdl) : launch_append<4, 1>(a, items, s, pdl);
+  return wide ? launch_append<8, 2>(a, items, s, pdl) : launch_append<4, 2>(a, items, s, pdl);
 }
 
 MTP_TRACE_COLLECTOR(latent_append)

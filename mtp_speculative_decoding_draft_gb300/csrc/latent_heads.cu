@@ -40,10 +40,14 @@ struct RowTile {
   int b, j0, row0, rows;  // sequence, first position, first output row, rows
 };
 
-// The sequences' row tiles before each thread's run of sequences.
+// The sequences' row tiles before each thread's run of sequences, and the first kNear
+// tiles themselves: looked up through the row starts, a tile's place took two round trips
+// of the producer, which its ring of four stages does not cover.
+constexpr int kNear = 1024;
 struct TileTable {
   int before[kThreads + 1];
   int sums[kThreads / 32];
+  RowTile near[kNear];
 };
 
 // Rows of sequence b that are expanded; flags what is out of range.
@@ -67,6 +71,7 @@ __device__ __forceinline__ RowTile find_tile(const LatentHeadsArgs &p, const Til
     r.rows = min(128, p.n_rows - r.row0);
     return r;
   }
+  if (m < kNear) return t.near[m];
   int lo = 0, hi = kThreads;  // before[lo] <= m < before[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -89,9 +94,12 @@ __device__ __forceinline__ RowTile find_tile(const LatentHeadsArgs &p, const Til
   }
 }
 
-// The page of position j of sequence b; page 0 for an entry outside the pool.
-__device__ __forceinline__ int page_of(const LatentHeadsArgs &p, int b, int j) {
-  const int id = __ldg(&p.page_table[(size_t)b * p.max_pages + (j >> p.page_shift)]);
+__device__ __forceinline__ int page_entry(const LatentHeadsArgs &p, int b, int j) {
+  return __ldg(&p.page_table[(size_t)b * p.max_pages + (j >> p.page_shift)]);
+}
+
+// The page of a table's entry; page 0 for one outside the pool.
+__device__ __forceinline__ int page_of(const LatentHeadsArgs &p, int id) {
   if (id < 0 || id >= p.n_pages) {
     set_status(p.status, kStatusBadPage);
     return 0;
@@ -147,6 +155,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
     for (int v = 0; v < warp; ++v) before += table.sums[v];
     table.before[tid] = before;
     if (tid == kThreads - 1) table.before[kThreads] = before + mine;
+    for (int b = tid * per; b < min(p.B, (tid + 1) * per) && before < kNear; ++b) {
+      int s;
+      const int n = seq_rows(p, b, &s, false);
+      for (int j = 0; j < n && before < kNear; j += 128) table.near[before++] = {b, j, s + j, min(128, n - j)};
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -160,12 +173,22 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
     const int prow = p.pages ? min(p.page, 128) : 128, npc = 128 / prow;
     const uint32_t bbytes = TRANS ? (uint32_t)hp.pieces * 64 * 128 : (uint32_t)hp.NT * 128;
     uint32_t i = 0;
+    // a tile's rows and this lane's entry of the page table, one tile ahead
+    RowTile r, r_next;
+    int id = 0, id_next = 0;
+    auto locate = [&](long long u, RowTile &t, int &e) {
+      t = find_tile(p, table, (int)(u % m_tiles));
+      if (p.pages && lane < npc && lane * prow < t.rows) e = page_entry(p, t.b, t.j0 + lane * prow);
+    };
+    if (blockIdx.x < items) locate(blockIdx.x, r_next, id_next);
     for (long long u = blockIdx.x; u < items && ok; u += gridDim.x) {
-      const int m = (int)(u % m_tiles), hn = (int)(u / m_tiles), h = hn / hp.n_tiles, n0 = (hn % hp.n_tiles) * hp.NT;
-      const RowTile r = find_tile(p, table, m);
+      const int hn = (int)(u / m_tiles), h = hn / hp.n_tiles, n0 = (hn % hp.n_tiles) * hp.NT;
+      r = r_next;
+      id = id_next;
       const bool need = lane < npc && lane * prow < r.rows;
-      const int y = p.pages && need ? page_of(p, r.b, r.j0 + lane * prow) * p.page : 0;
+      const int y = p.pages && need ? page_of(p, id) * p.page : 0;
       const uint32_t abytes = (uint32_t)(__popc(__ballot_sync(kFull, need)) * prow * 128);
+      if (u + gridDim.x < items) locate(u + gridDim.x, r_next, id_next);
       for (int kb = 0; kb < hp.kbs && ok; ++kb, ++i) {
         const int s = (int)(i % kStages);
         if (i >= (uint32_t)kStages) ok = mbar_wait(&empty[s], ((i / kStages) - 1u) & 1u, p.status);
@@ -234,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
         // the shared key part of the tile's positions
         const int j = r.j0 + row;
         const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.pages + ((size_t)page_of(p, r.b, j) * p.page + (j & (p.page - 1))) * (size_t)(p.K + p.Dr) + p.K);
+            p.pages + ((size_t)page_of(p, page_entry(p, r.b, j)) * p.page + (j & (p.page - 1))) * (size_t)(p.K + p.Dr) + p.K);
         uint4 *dst = reinterpret_cast<uint4 *>(p.k_rope + (long long)(r.row0 + row) * p.ldkr);
         for (int e = 0; e < p.Dr / 8; ++e) dst[e] = __ldg(src + e);
       }

@@ -30,10 +30,13 @@ constexpr int kCombineThreads = 256;
 constexpr int kMaxDescs = 256;  // CTAs at most
 
 template <int DH, int ROWS>
-__global__ void __launch_bounds__(kCombineThreads, DH > 128 ? 3 : 6)
+__global__ void __launch_bounds__(kCombineThreads, DH > 128 ? 2 : 6)
     paged_combine_tc_kernel(const __grid_constant__ PagedArgs p, int ctas) {
   trace_start(kTkPagedCombine);
-  constexpr int PER = DH / 32, kBatch = 2, NW = kCombineThreads / 32;
+  constexpr int PER = DH / 32, kBatch = DH > 128 ? 4 : 2, NW = kCombineThreads / 32;
+  // a lane's elements: vectors of VEC, 32 VEC apart
+  constexpr int VEC = PER < 4 ? PER : 4;
+  auto place = [](int lane, int e) { return e / VEC * (32 * VEC) + lane * VEC + e % VEC; };
   __shared__ PagedDesc desc[kMaxDescs];
   __shared__ int before[kMaxDescs + 1], sums[NW];
   __shared__ float part[NW][DH + 2];
@@ -98,11 +101,11 @@ __global__ void __launch_bounds__(kCombineThreads, DH > 128 ? 3 : 6)
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
         if (i0 + i < my) {
-          const float *x = p.part_o + seg(i0 + i) * DH + lane * PER;
+          const float *x = p.part_o + seg(i0 + i) * DH + lane * VEC;
           if (PER >= 4) {
 #pragma unroll
             for (int e = 0; e < PER / 4; ++e) {
-              const float4 y = __ldcg(reinterpret_cast<const float4 *>(x) + e);
+              const float4 y = __ldcg(reinterpret_cast<const float4 *>(x) + 32 * e);
               v[i][4 * e] = y.x;
               v[i][(4 * e + 1) % PER] = y.y;
               v[i][(4 * e + 2) % PER] = y.z;
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kCombineThreads, DH > 128 ? 3 : 6)
     if (wpr > 1) {  // uniform over the block
       float *mem = part[warp];
 #pragma unroll
-      for (int e = 0; e < PER; ++e) mem[lane * PER + e] = a[e];
+      for (int e = 0; e < PER; ++e) mem[place(lane, e)] = a[e];
       if (lane == 0) {
         mem[DH] = M;
         mem[DH + 1] = S;
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(kCombineThreads, DH > 128 ? 3 : 6)
           const float f = y[DH] == -INFINITY ? 0.f : exp2f(y[DH] - N);
           S = fmaf(y[DH + 1], f, S);
 #pragma unroll
-          for (int e = 0; e < PER; ++e) a[e] = fmaf(y[lane * PER + e], f, a[e]);
+          for (int e = 0; e < PER; ++e) a[e] = fmaf(y[place(lane, e)], f, a[e]);
         }
         M = N;
       }
@@ -168,20 +171,19 @@ __global__ void __launch_bounds__(kCombineThreads, DH > 128 ? 3 : 6)
     }
     const float inv = paged_inverse(S);
     const int row = d.row0 + r / p.G, hq = d.h * p.G + r % p.G;
-    const long long at = (long long)row * p.ldo + hq * DH + lane * PER;
     // (a block of heads may hold fewer than G at the end)
     if (mine && q == 0 && hq < p.Hq && in_bounds(row < p.n_rows, p.status)) {
-      if constexpr (PER >= 8) {
+      __nv_bfloat16 *at = static_cast<__nv_bfloat16 *>(p.out) + (long long)row * p.ldo + hq * DH;
 #pragma unroll
-        for (int e = 0; e < PER; e += 8) {
-          __nv_bfloat162 w[4];
+      for (int e = 0; e < PER; e += VEC) {
+        if constexpr (VEC == 4) {
+          const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(a[e] * inv, a[e + 1] * inv),
+                                       __floats2bfloat162_rn(a[e + 2] * inv, a[e + 3] * inv)};
+          *reinterpret_cast<uint2 *>(at + place(lane, e)) = *reinterpret_cast<const uint2 *>(w);
+        } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = __floats2bfloat162_rn(a[e + 2 * j] * inv, a[e + 2 * j + 1] * inv);
-          *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at + e) = *reinterpret_cast<const uint4 *>(w);
+          for (int j = 0; j < VEC; ++j) at[place(lane, e + j)] = __float2bfloat16_rn(a[e + j] * inv);
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < PER; ++e) static_cast<__nv_bfloat16 *>(p.out)[at + e] = __float2bfloat16_rn(a[e] * inv);
       }
       if (lane == 0 && p.lse) p.lse[(size_t)row * p.Hq + hq] = paged_lse(M, S);
     }
