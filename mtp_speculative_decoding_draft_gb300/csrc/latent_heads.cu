@@ -2,8 +2,12 @@
 // rows or from the pages of a latent cache (then the rows are the first positions of
 // the sequences and every head reads the same ones).
 //
-// One CTA an SM walks tiles of 128 rows x NT outputs of a head, the row tiles of one
-// weight tile next to each other so that the weights come from memory once.  x and W
+// Pairs of CTAs walk tiles of 2 x 128 rows x NT outputs of a head, the row tiles of one
+// weight tile next to each other so that the weights come from memory once.  A pair's
+// product (cta_group::2) reads each CTA's rows and half of the weight tile: alone, a CTA
+// would bring 48 KB and read 48 KB of shared memory for every 512 cycles of products, at
+// 128 bytes a cycle 768; in pairs it is 32 and 32 KB.  With one tile of rows there is no
+// pair to make, and CTAs walk alone.  x and W
 // arrive by TMA in blocks of 64 along K, W as it lies: rows along K ([N, K], the
 // K-major form of the operand) or along N ([K, N], the MN-major one).  Two accumulators in
 // tensor memory: a tile's output is written under the next one's products.
@@ -22,11 +26,15 @@ namespace {
 
 constexpr int kThreads = 320;  // warps 0-7 write outputs, 8 brings blocks, 9 issues the products
 constexpr int kProducer = 8, kIssuer = 9, kOutThreads = 256;
-constexpr int kABytes = 128 * 128, kBBytes = 256 * 128;  // a stage: 64 of K
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 4;
+constexpr int kABytes = 128 * 128;  // of a stage: 64 of K
 constexpr unsigned kFull = 0xffffffffu;
-constexpr size_t kSmem = (size_t)kStages * kStageBytes + 256;
+
+template <bool PAIR>
+struct Lay {
+  static constexpr int STAGE = kABytes + (PAIR ? 128 : 256) * 128;  // rows, and a CTA's part of the weights
+  static constexpr int STAGES = PAIR ? 6 : 4;
+  static constexpr size_t SMEM = (size_t)STAGES * STAGE + 256;
+};
 
 struct HeadsParams {
   CUtensorMap mx, mw;
@@ -68,9 +76,10 @@ __device__ __forceinline__ RowTile find_tile(const LatentHeadsArgs &p, const Til
     r.b = 0;
     r.j0 = 0;
     r.row0 = m * 128;
-    r.rows = min(128, p.n_rows - r.row0);
+    r.rows = max(0, min(128, p.n_rows - r.row0));
     return r;
   }
+  if (m >= t.before[kThreads]) return {0, 0, 0, 0};  // the second of a last, odd pair
   if (m < kNear) return t.near[m];
   int lo = 0, hi = kThreads;  // before[lo] <= m < before[hi]
   while (hi - lo > 1) {
@@ -109,10 +118,14 @@ __device__ __forceinline__ int page_of(const LatentHeadsArgs &p, int id) {
 
 }  // namespace
 
-template <bool TRANS>
+template <bool TRANS, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_constant__ HeadsParams hp) {
   trace_start(kTkLatentHeads);
+  using L = Lay<PAIR>;
+  constexpr int kStages = L::STAGES, kStageBytes = L::STAGE, CTAS = PAIR ? 2 : 1;
   const LatentHeadsArgs &p = hp.a;
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
+  const unsigned walker = blockIdx.x / CTAS, walkers = gridDim.x / CTAS;
   extern __shared__ __align__(1024) unsigned char smem[];
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes);
   uint64_t *empty = full + kStages, *done = empty + kStages, *tfree = done + 2, *drain = tfree + 2;
@@ -121,17 +134,20 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], CTAS);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&done[b], 1);
-      mbar_init(&tfree[b], kOutThreads / 32);
+      mbar_init(&tfree[b], CTAS * kOutThreads / 32);
     }
     mbar_init(drain, 1);
     fence_barrier_init();
   }
-  if (warp == kIssuer) tmem_alloc(tmem_slot, 512);
+  if (warp == kIssuer) {
+    if constexpr (PAIR) tmem_alloc_pair(tmem_slot, 512);
+    else tmem_alloc(tmem_slot, 512);
+  }
   grid_dep_wait();
   trace_dep(kTkLatentHeads);
   grid_dep_launch();
@@ -162,94 +178,124 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // the barriers of both CTAs are set up
+  else __syncthreads();
   tc_fence_after();
   if (p.pages) m_tiles = table.before[kThreads];
+  m_tiles = (m_tiles + CTAS - 1) / CTAS;  // of all the walker's rows
   const uint32_t tmem = *tmem_slot;
   const long long items = (long long)p.H * hp.n_tiles * m_tiles;
   bool ok = true;
 
   if (warp == kProducer) {
     const int prow = p.pages ? min(p.page, 128) : 128, npc = 128 / prow;
-    const uint32_t bbytes = TRANS ? (uint32_t)hp.pieces * 64 * 128 : (uint32_t)hp.NT * 128;
+    const uint32_t bbytes = TRANS ? (uint32_t)hp.pieces * 64 * 128 : (uint32_t)(hp.NT / CTAS) * 128;
     uint32_t i = 0;
     // a tile's rows and this lane's entry of the page table, one tile ahead
     RowTile r, r_next;
     int id = 0, id_next = 0;
     auto locate = [&](long long u, RowTile &t, int &e) {
-      t = find_tile(p, table, (int)(u % m_tiles));
+      t = find_tile(p, table, (int)(u % m_tiles) * CTAS + rank);
       if (p.pages && lane < npc && lane * prow < t.rows) e = page_entry(p, t.b, t.j0 + lane * prow);
     };
-    if (blockIdx.x < items) locate(blockIdx.x, r_next, id_next);
-    for (long long u = blockIdx.x; u < items && ok; u += gridDim.x) {
+    if (walker < items) locate(walker, r_next, id_next);
+    for (long long u = walker; u < items && ok; u += walkers) {
       const int hn = (int)(u / m_tiles), h = hn / hp.n_tiles, n0 = (hn % hp.n_tiles) * hp.NT;
       r = r_next;
       id = id_next;
       const bool need = lane < npc && lane * prow < r.rows;
       const int y = p.pages && need ? page_of(p, id) * p.page : 0;
       const uint32_t abytes = (uint32_t)(__popc(__ballot_sync(kFull, need)) * prow * 128);
-      if (u + gridDim.x < items) locate(u + gridDim.x, r_next, id_next);
+      if (u + walkers < items) locate(u + walkers, r_next, id_next);
       for (int kb = 0; kb < hp.kbs && ok; ++kb, ++i) {
         const int s = (int)(i % kStages);
         if (i >= (uint32_t)kStages) ok = mbar_wait(&empty[s], ((i / kStages) - 1u) & 1u, p.status);
         ok = __all_sync(kFull, ok);
         if (!ok) break;
         unsigned char *st = smem + s * kStageBytes;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&full[s], abytes + bbytes);
-          if (TRANS)
-            for (int x = 0; x < hp.pieces; ++x) tma_3d(st + kABytes + x * 64 * 128, &hp.mw, n0 + 64 * x, kb * 64, h, &full[s]);
-          else
-            tma_3d(st + kABytes, &hp.mw, kb * 64, n0, h, &full[s]);
-        }
-        __syncwarp();
-        if (need) {
-          if (p.pages) tma_2d(st + lane * prow * 128, &hp.mx, kb * 64, y, &full[s]);
-          else tma_3d(st, &hp.mx, kb * 64, h, r.row0, &full[s]);
+        if constexpr (PAIR) {
+          // both CTAs' copies complete on the first one's barrier, each CTA adding its bytes
+          const uint32_t bar = dsmem_addr(&full[s], 0);
+          if (lane == 0) {
+            expect_tx_cluster(bar, abytes + bbytes);
+            if (TRANS)
+              for (int x = 0; x < hp.pieces; ++x)
+                tma_3d_pair(st + kABytes + x * 64 * 128, &hp.mw, n0 + 64 * (rank * hp.pieces + x), kb * 64, h, bar);
+            else
+              tma_3d_pair(st + kABytes, &hp.mw, kb * 64, n0 + rank * (hp.NT / 2), h, bar);
+          }
+          __syncwarp();
+          if (need) {
+            if (p.pages) tma_2d_pair(st + lane * prow * 128, &hp.mx, kb * 64, y, bar);
+            else tma_3d_pair(st, &hp.mx, kb * 64, h, r.row0, bar);
+          }
+        } else {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&full[s], abytes + bbytes);
+            if (TRANS)
+              for (int x = 0; x < hp.pieces; ++x)
+                tma_3d(st + kABytes + x * 64 * 128, &hp.mw, n0 + 64 * x, kb * 64, h, &full[s]);
+            else
+              tma_3d(st + kABytes, &hp.mw, kb * 64, n0, h, &full[s]);
+          }
+          __syncwarp();
+          if (need) {
+            if (p.pages) tma_2d(st + lane * prow * 128, &hp.mx, kb * 64, y, &full[s]);
+            else tma_3d(st, &hp.mx, kb * 64, h, r.row0, &full[s]);
+          }
         }
       }
     }
-    if (!ok)  // let copies still in flight land before the CTA exits
+    if (!ok && rank == 0)  // let copies still in flight land before the CTAs exit
       for (uint32_t q = i > (uint32_t)kStages ? i - kStages : 0u; q < i; ++q)
         if (!mbar_wait(&full[q % kStages], (q / kStages) & 1u, p.status)) break;
   } else if (warp == kIssuer) {
-    const uint32_t idesc = idesc_bf16_f32(128, 256) - ((uint32_t)(256 - hp.NT) >> 3 << 17) + (TRANS ? 1u << 16 : 0u);
-    const bool leader = elect_one();
-    const uint64_t ad = sw128_kmajor_desc(smem_u32(smem)),
-                   bd = TRANS ? sw128_mnmajor_desc(smem_u32(smem + kABytes), 64 * 128) : sw128_kmajor_desc(smem_u32(smem + kABytes));
-    uint32_t i = 0, n = 0;
-    for (long long u = blockIdx.x; u < items && ok; u += gridDim.x, ++n) {
-      const uint32_t buf = n & 1u;
-      if (n >= 2) ok = mbar_wait(&tfree[buf], ((n >> 1) - 1u) & 1u, p.status);
-      ok = __all_sync(kFull, ok);
-      if (!ok) break;
-      for (int kb = 0; kb < hp.kbs && ok; ++kb, ++i) {
-        const int s = (int)(i % kStages);
-        ok = __all_sync(kFull, mbar_wait(&full[s], (i / kStages) & 1u, p.status));
+    if (rank == 0) {
+      const uint32_t idesc = idesc_bf16_f32(128 * CTAS, 256) - ((uint32_t)(256 - hp.NT) >> 3 << 17) + (TRANS ? 1u << 16 : 0u);
+      const bool leader = elect_one();
+      const uint64_t ad = sw128_kmajor_desc(smem_u32(smem)),
+                     bd = TRANS ? sw128_mnmajor_desc(smem_u32(smem + kABytes), 64 * 128) : sw128_kmajor_desc(smem_u32(smem + kABytes));
+      auto commit = [](uint64_t *bar) {
+        if constexpr (PAIR) mma_commit_pair(bar);
+        else mma_commit(bar);
+      };
+      uint32_t i = 0, n = 0;
+      for (long long u = walker; u < items && ok; u += walkers, ++n) {
+        const uint32_t buf = n & 1u;
+        if (n >= 2) ok = mbar_wait(&tfree[buf], ((n >> 1) - 1u) & 1u, p.status);
+        ok = __all_sync(kFull, ok);
         if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const uint64_t so = (uint64_t)(s * (kStageBytes >> 4));
+        for (int kb = 0; kb < hp.kbs && ok; ++kb, ++i) {
+          const int s = (int)(i % kStages);
+          ok = __all_sync(kFull, mbar_wait(&full[s], (i / kStages) & 1u, p.status));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t so = (uint64_t)(s * (kStageBytes >> 4));
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_bf16(tmem + 256 * buf, ad + so + 2 * k, bd + so + (TRANS ? 128 : 2) * k, idesc, (kb | k) != 0);
-          mma_commit(&empty[s]);
-          if (kb == hp.kbs - 1) mma_commit(&done[buf]);
+            for (int k = 0; k < 4; ++k) {
+              const uint64_t x = ad + so + 2 * k, y = bd + so + (TRANS ? 128 : 2) * k;
+              if constexpr (PAIR) mma_bf16_pair(tmem + 256 * buf, x, y, idesc, (kb | k) != 0);
+              else mma_bf16(tmem + 256 * buf, x, y, idesc, (kb | k) != 0);
+            }
+            commit(&empty[s]);
+            if (kb == hp.kbs - 1) commit(&done[buf]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
+      if (leader) commit(drain);  // nothing is in flight when the tensor memory is freed
+      __syncwarp();
     }
-    if (leader) mma_commit(drain);  // nothing of this CTA is in flight when it frees its tensor memory
-    __syncwarp();
-    mbar_wait(drain, 0, p.status);
+    mbar_sleep_wait(drain, 0, p.status);  // (a pair's second CTA waits here from the start)
   } else {
     // a thread a row: the warp's lanes of tensor memory, every other 64 outputs
     const int q = warp & 3;
     const uint32_t lanebase = (uint32_t)(q * 32) << 16;
     uint32_t n = 0;
-    for (long long u = blockIdx.x; u < items; u += gridDim.x, ++n) {
+    for (long long u = walker; u < items; u += walkers, ++n) {
       const int m = (int)(u % m_tiles), hn = (int)(u / m_tiles), h = hn / hp.n_tiles, n0 = (hn % hp.n_tiles) * hp.NT;
-      const RowTile r = find_tile(p, table, m);
+      const RowTile r = find_tile(p, table, m * CTAS + rank);
       const uint32_t buf = n & 1u;
       const int row = q * 32 + lane;
       const bool real = row < r.rows;
@@ -285,53 +331,91 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tfree[buf]);
+      if (lane == 0) {
+        // (the reads of tensor memory are complete: there is nothing to release)
+        if constexpr (PAIR) mbar_arrive_cluster_relaxed(dsmem_addr(&tfree[buf], 0));
+        else mbar_arrive(&tfree[buf]);
+      }
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // neither CTA leaves while the other may still signal it
+  else __syncthreads();
   tc_fence_after();
-  if (warp == kIssuer) tmem_dealloc(tmem, 512);
+  if (warp == kIssuer) {
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
+  }
   trace_end(kTkLatentHeads);
 }
 
 // ---------------------------------------------------------------- host side
+
+namespace {
+
+template <bool TRANS, bool PAIR>
+cudaError_t launch(const HeadsParams &hp, long long walkers, cudaStream_t s, bool pdl) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)walkers * (PAIR ? 2 : 1));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Lay<PAIR>::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (PAIR) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, latent_heads_kernel<TRANS, PAIR>, hp);
+}
+
+template <bool TRANS, bool PAIR>
+cudaError_t set_smem() {
+  return cudaFuncSetAttribute(latent_heads_kernel<TRANS, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)Lay<PAIR>::SMEM);
+}
+
+}  // namespace
 
 cudaError_t launch_latent_heads(const LatentHeadsArgs &a, int sms, cudaStream_t s, bool pdl) {
   HeadsParams hp{};
   hp.a = a;
   hp.kbs = (a.K + 63) / 64;
   hp.m_tiles = (a.n_rows + 127) / 128;
-  hp.NT = a.N >= 256 ? 256 : (a.N + 15) / 16 * 16;
+  const bool pair = hp.m_tiles > 1;
+  // a CTA of a pair holds half of a weight tile: whole pieces of 64
+  hp.NT = a.N > (pair ? 128 : 255) ? 256 : pair ? 128 : (a.N + 15) / 16 * 16;
   hp.n_tiles = (a.N + hp.NT - 1) / hp.NT;
-  hp.pieces = (hp.NT + 63) / 64;
+  const int nt = pair ? hp.NT / 2 : hp.NT;  // outputs whose weights a CTA brings
+  hp.pieces = (nt + 63) / 64;
   const bool x_ok = a.pages ? make_rows_map(&hp.mx, a.pages, a.K + a.Dr, (uint64_t)a.n_pages * a.page, a.K + a.Dr, a.page)
                             : make_heads_map(&hp.mx, a.x, a.K, a.H, a.n_rows, a.hsx, a.ldx, 1, 128);
   const bool w_ok = a.transposed ? make_heads_map(&hp.mw, a.w, a.N, a.K, a.H, a.ldw, a.hsw, 64, 1)
-                                 : make_heads_map(&hp.mw, a.w, a.K, a.N, a.H, a.ldw, a.hsw, hp.NT, 1);
+                                 : make_heads_map(&hp.mw, a.w, a.K, a.N, a.H, a.ldw, a.hsw, nt, 1);
   if (!x_ok || !w_ok) return cudaErrorNotSupported;
   // from pages the device knows how many tiles there are: one more a sequence at most
-  const long long most = (long long)a.H * hp.n_tiles * (a.pages ? hp.m_tiles + a.B : hp.m_tiles);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  note_launch();
-  return a.transposed ? cudaLaunchKernelEx(&cfg, latent_heads_kernel<true>, hp)
-                      : cudaLaunchKernelEx(&cfg, latent_heads_kernel<false>, hp);
+  const long long tiles = a.pages ? (long long)hp.m_tiles + a.B : hp.m_tiles, most = (long long)a.H * hp.n_tiles * tiles;
+  const int places = pair ? sms / 2 : sms;
+  const long long walkers = most < places ? most : places;
+  if (a.transposed) return pair ? launch<true, true>(hp, walkers, s, pdl) : launch<true, false>(hp, walkers, s, pdl);
+  return pair ? launch<false, true>(hp, walkers, s, pdl) : launch<false, false>(hp, walkers, s, pdl);
 }
 
 cudaError_t latent_heads_set_attributes() {
-  cudaError_t e =
-      cudaFuncSetAttribute(latent_heads_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(latent_heads_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  cudaError_t e = set_smem<true, true>();
+  if (e == cudaSuccess) e = set_smem<true, false>();
+  if (e == cudaSuccess) e = set_smem<false, true>();
+  if (e == cudaSuccess) e = set_smem<false, false>();
   return e;
 }
 
