@@ -41,7 +41,8 @@ def library_path(variant=None):
     return VARIANTS[v][1]
 SOURCES = ("api.cu", "draft.cu", "verify.cu", "verify_split.cu", "tc.cu", "attn_tc.cu", "diag.cu", "fused.cu",
            "chain.cu", "paged_attn.cu", "paged_attn_tc.cu", "cache_append.cu", "logits.cu",
-           "latent_append.cu", "latent_heads.cu", "latent_attn.cu", "latent_prefill.cu")
+           "latent_append.cu", "latent_heads.cu", "latent_attn.cu", "latent_attn_pair.cu",
+           "latent_prefill.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -661,6 +661,7 @@ int trace_collect_logits(TraceRec *, int);
 int trace_collect_latent_append(TraceRec *, int);
 int trace_collect_latent_heads(TraceRec *, int);
 int trace_collect_latent_attn(TraceRec *, int);
+int trace_collect_latent_attn_pair(TraceRec *, int);
 int trace_collect_latent_prefill(TraceRec *, int);
 
 }  // namespace mtp
@@ -1466,7 +1467,8 @@ int mtp_trace_read(MtpTraceEntry *entries, int max_entries) {
                                          mtp::trace_collect_paged_attn_tc,
                                          mtp::trace_collect_cache_append, mtp::trace_collect_logits,
                                          mtp::trace_collect_latent_append, mtp::trace_collect_latent_heads,
-                                         mtp::trace_collect_latent_attn, mtp::trace_collect_latent_prefill};
+                                         mtp::trace_collect_latent_attn, mtp::trace_collect_latent_attn_pair,
+                                         mtp::trace_collect_latent_prefill};
   static mtp::TraceRec recs[mtp::kTraceSlots];
   int n = 0;
   for (Collector col : collectors) {

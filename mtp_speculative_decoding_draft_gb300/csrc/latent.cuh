@@ -66,6 +66,12 @@ bool latent_prefill_items_ok(int B, int n_rows, int H);
 size_t latent_prefill_scratch_bytes(int B, int n_rows, int H, int Dv);
 cudaError_t launch_latent_prefill(const LatentPrefillArgs &lp, void *scratch, int sms, cudaStream_t s, bool pdl);
 
+// The same on pairs of CTAs (latent_attn_pair.cu).
+bool latent_pair_items_ok(int B, int n_rows, int H);
+size_t latent_pair_scratch_bytes(int B, int n_rows, int H);
+cudaError_t launch_latent_attn_pair(const LatentAttnArgs &la, void *scratch, int sms, cudaStream_t s, bool pdl);
+cudaError_t latent_pair_set_attributes();
+
 cudaError_t latent_set_attributes();
 cudaError_t latent_prefill_set_attributes();
 cudaError_t latent_heads_set_attributes();

@@ -462,19 +462,26 @@ cudaError_t launch(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl) 
 
 }  // namespace
 
+// More packed rows than two blocks hold, at the mean number of rows a sequence, go to
+// pairs of CTAs.
+static bool wants_pair(int B, int n_rows, int H) { return (long long)((n_rows + B - 1) / B) * H > 128; }
+
 bool latent_attn_items_ok(int B, int n_rows, int H) {
+  if (wants_pair(B, n_rows, H)) return latent_pair_items_ok(B, n_rows, H);
   int G, hb;
   block_shape(B, n_rows, H, &G, &hb);
   return paged_tc_items_ok(B, n_rows, kRows / G, hb);
 }
 
 size_t latent_attn_scratch_bytes(int B, int n_rows, int H, int R) {
+  if (wants_pair(B, n_rows, H)) return latent_pair_scratch_bytes(B, n_rows, H);
   int G, hb;
   block_shape(B, n_rows, H, &G, &hb);
   return region_bytes(kPagedMaxCtas, kRows, R) + paged_tc_plan_bytes(B, n_rows, kRows / G, hb);
 }
 
 cudaError_t launch_latent_attn(const LatentAttnArgs &la, void *scratch, int sms, cudaStream_t s, bool pdl) {
+  if (wants_pair(la.a.B, la.a.n_rows, la.a.Hq)) return launch_latent_attn_pair(la, scratch, sms, s, pdl);
   const int n = sms < kPagedMaxCtas ? sms : kPagedMaxCtas, w = la.a.Dh + la.Dr;
   PagedTcParams sp{};
   PagedArgs &a = sp.a;
@@ -498,6 +505,7 @@ cudaError_t latent_set_attributes() {
       cudaFuncSetAttribute(latent_attn_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<512>::SMEM);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(latent_attn_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<256>::SMEM);
+  if (e == cudaSuccess) e = latent_pair_set_attributes();
   if (e == cudaSuccess) e = latent_prefill_set_attributes();
   if (e == cudaSuccess) e = latent_heads_set_attributes();
   return e;

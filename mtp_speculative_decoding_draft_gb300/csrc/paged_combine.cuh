@@ -29,7 +29,8 @@ inline void bind_region(PagedArgs &a, char *base, int ctas, int rows) {
 constexpr int kCombineThreads = 256;
 constexpr int kMaxDescs = 256;  // CTAs at most
 
-template <int DH, int ROWS>
+// HALVES: an item is one of so many parts (of DH elements) of its heads' outputs.
+template <int DH, int ROWS, int HALVES = 1>
 __global__ void __launch_bounds__(kCombineThreads, DH > 128 ? 2 : 6)
     paged_combine_tc_kernel(const __grid_constant__ PagedArgs p, int ctas) {
   trace_start(kTkPagedCombine);
@@ -170,10 +171,10 @@ __global__ void __launch_bounds__(kCombineThreads, DH > 128 ? 2 : 6)
       __syncthreads();
     }
     const float inv = paged_inverse(S);
-    const int row = d.row0 + r / p.G, hq = d.h * p.G + r % p.G;
+    const int row = d.row0 + r / p.G, hq = d.h / HALVES * p.G + r % p.G, half = d.h % HALVES;
     // (a block of heads may hold fewer than G at the end)
     if (mine && q == 0 && hq < p.Hq && in_bounds(row < p.n_rows, p.status)) {
-      __nv_bfloat16 *at = static_cast<__nv_bfloat16 *>(p.out) + (long long)row * p.ldo + hq * DH;
+      __nv_bfloat16 *at = static_cast<__nv_bfloat16 *>(p.out) + (long long)row * p.ldo + (hq * HALVES + half) * DH;
 #pragma unroll
       for (int e = 0; e < PER; e += VEC) {
         if constexpr (VEC == 4) {
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kCombineThreads, DH > 128 ? 2 : 6)
           for (int j = 0; j < VEC; ++j) at[place(lane, e + j)] = __float2bfloat16_rn(a[e + j] * inv);
         }
       }
-      if (lane == 0 && p.lse) p.lse[(size_t)row * p.Hq + hq] = paged_lse(M, S);
+      if (lane == 0 && p.lse && half == 0) p.lse[(size_t)row * p.Hq + hq] = paged_lse(M, S);
     }
   }
   trace_end(kTkPagedCombine);
