@@ -747,7 +747,8 @@ int64_t mtp_launch_count(void);
  * launch; 0 where the kernel does not record it), when the last CTA reached
  * each of up to four intermediate points of the kernel (the GEMV: activations
  * loaded, last weight piece used, epilogue done; tensor-core attention: query
- * staged, last tile done, CTA merged, cluster combined) and when the last CTA
+ * staged, last tile done, CTA merged, cluster combined; latent attention: a first
+ * tile's scores there, last tile done, output written) and when the last CTA
  * finished.  Unlike the event profiler above it leaves the launch chain
  * intact, so it shows the live overlap of the chained kernels.
  *

@@ -20,9 +20,8 @@
 // products, warp 6 brings the next block's queries, warp 7 clears rows that no row sees.
 #include "internal.h"
 #include "latent.cuh"
-#include "paged_combine.cuh"
 #include "paged_tc.cuh"
-#include "tcgen05.cuh"
+#include "latent_combine.cuh"
 
 namespace mtp {
 
@@ -42,7 +41,7 @@ struct Lay {
   static constexpr int QBLK = kRows * 128, QTILE = NB * QBLK;
   static constexpr int STAGES = 4;
   static constexpr int NG = (NB + 2) / 3;        // groups of up to three blocks that arrive together
-  static constexpr size_t SMEM = (size_t)QTILE + STAGES * TILE + 512;
+  static constexpr size_t SMEM = (size_t)QTILE + STAGES * TILE + 512 + kNearItems * sizeof(PagedItem);
   __host__ __device__ static constexpr uint32_t S(int b) { return 256u + TK * b; }
   __host__ __device__ static constexpr uint32_t P(int b) { return 384u + TK * b; }
 };
@@ -101,12 +100,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   grid_dep_wait();
   trace_dep(kTkLatentAttn);
   grid_dep_launch();
-  PlanWalk<TK> w(sp, blockIdx.x);
+  PagedItem *near = reinterpret_cast<PagedItem *>(smem + L::SMEM - kNearItems * sizeof(PagedItem));
+  PlanWalk<TK, true> w(sp, blockIdx.x, near);
   if (tid == 0) p.desc[blockIdx.x].rows = 0;
   if (!w.valid()) {  // the same for the whole CTA
     trace_end(kTkLatentAttn);
     return;
   }
+  w.copy_near(sp, blockIdx.x, near);
   if (warp == kIssuer) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
@@ -280,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
         const bool whole = k0 + TK <= all_hi && (k0 >= all_lo || k0 + TK <= min(p.sinks, all_hi));
         if (ok) ok = mbar_wait(&s_full[it & 1], (uint32_t)(it >> 1) & 1u, p.status);
         __syncwarp();
+        if (i == w.i0) trace_mark(kTkLatentAttn, 0);
         tc_fence_after();
         uint32_t s[KH];
         load_scores<KH>(tmem + lanebase + L::S(it & 1), s, lane);
@@ -308,16 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
             if (ok) ok = mbar_wait(&o_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u, p.status);
             __syncwarp();
             tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < R / 64; ++c) {
-              uint32_t o[32];
-              tmem_ld32_async(to + 32 * c, o);
-              tmem_wait_ld();
-              pin32(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(to + 32 * c, o);
-            }
+            rescale_columns<R / 64>(to, f);
           }
         }
         const float u = m == -INFINITY ? 0.f : m;
@@ -353,42 +346,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       if (ok) ok = mbar_wait(&o_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u, p.status);
       __syncwarp();
       tc_fence_after();
+      trace_mark(kTkLatentAttn, 1);
       const bool whole_item = w.starts() && w.ends();
       const int slot = w.starts() ? 1 : 0;
       const int qrow = w.s.row0 + tok;
       const bool mine = live && in_bounds(qrow < p.n_rows, p.status);
       const float inv = paged_inverse(l);
-      const size_t pr = ((size_t)blockIdx.x * 2 + slot) * kRows + row;
-#pragma unroll 1
-      for (int c = 0; c < R / 64; ++c) {
-        uint32_t o[32];
-        tmem_ld32_async(to + 32 * c, o);
-        tmem_wait_ld();
-        pin32(o);
-        const int e0 = half * (R / 2) + 32 * c;
-        if (!whole_item) {
-          uint4 v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          store_quads<8>(v, mine ? p.part_o + pr * R + e0 : nullptr, lane);
-        } else {
-          uint16_t *d = static_cast<uint16_t *>(p.out) + (long long)qrow * p.ldo + hq * R + e0;
-          uint4 v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              y[j] = pack2(__uint_as_float(o[8 * e + 2 * j]) * inv, __uint_as_float(o[8 * e + 2 * j + 1]) * inv);
-            v[e] = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-          store_quads<4>(v, mine ? d : nullptr, lane);
-        }
-      }
+      const size_t block = (size_t)blockIdx.x * 2 + slot;
+      write_row<R / 64, kRows>(to, half * (R / 2), whole_item,
+                               mine ? static_cast<uint16_t *>(p.out) + (long long)qrow * p.ldo + hq * R : nullptr, inv,
+                               p.part_o + block * kRows * R, mine ? row : -1, lane);
       if (mine && half == 0) {
         if (!whole_item) {
-          p.part_ml[pr * 2] = m;
-          p.part_ml[pr * 2 + 1] = l;
+          reinterpret_cast<float2 *>(p.part_ml)[block * kRows + row] = make_float2(m, l);
         } else if (p.lse) {
           p.lse[(size_t)qrow * p.Hq + hq] = paged_lse(m, l);
         }
@@ -401,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
         d.last_cta = w.last_cta();
         p.desc[blockIdx.x] = d;
       }
+      trace_mark(kTkLatentAttn, 2);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_empty);
@@ -453,11 +424,7 @@ cudaError_t launch(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl) 
   note_launch();
   e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<R>, sp);
   if (e) return e;
-  cfg.gridDim = dim3(3 * ctas);
-  cfg.blockDim = dim3(kCombineThreads);
-  cfg.dynamicSmemBytes = 0;
-  note_launch();
-  return cudaLaunchKernelEx(&cfg, paged_combine_tc_kernel<R, kRows>, sp.a, ctas);
+  return launch_latent_combine<R, kRows, 1>(sp, ctas, ctas, s, pdl);
 }
 
 }  // namespace

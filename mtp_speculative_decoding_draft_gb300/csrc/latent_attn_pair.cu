@@ -22,9 +22,8 @@
 // waits for lie in the first CTA and count both; those that products complete lie in both.
 #include "internal.h"
 #include "latent.cuh"
-#include "paged_combine.cuh"
 #include "paged_tc.cuh"
-#include "tcgen05.cuh"
+#include "latent_combine.cuh"
 
 namespace mtp {
 
@@ -46,7 +45,7 @@ struct Lay {
   static constexpr int KST = R == 512 ? 6 : 9;
   static constexpr int VGRP = kTK * 128, VTILE = 2 * VGRP;  // 64 elements of 128 values; a CTA's 128 elements
   static constexpr int VST = R == 512 ? 1 : 2;
-  static constexpr size_t SMEM = (size_t)QTILE + KST * KBLK + VST * VTILE + 512;
+  static constexpr size_t SMEM = (size_t)QTILE + KST * KBLK + VST * VTILE + 512 + kNearItems * sizeof(PagedItem);
   __host__ __device__ static constexpr uint32_t S(int b) { return 256u + 128u * b; }
 };
 
@@ -93,12 +92,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   trace_dep(kTkLatentAttn);
   grid_dep_launch();
-  PlanWalk<kTK> w(sp, pair);
+  PagedItem *near = reinterpret_cast<PagedItem *>(smem + L::SMEM - kNearItems * sizeof(PagedItem));
+  PlanWalk<kTK, true> w(sp, pair, near);
   if (tid == 0 && rank == 0) p.desc[pair].rows = 0;
   if (!w.valid()) {  // the same for the whole pair
     trace_end(kTkLatentAttn);
     return;
   }
+  w.copy_near(sp, pair, near);
   if (warp == kIssuer) tmem_alloc_pair(tmem_slot, 512);
   tc_fence_before();
   cluster_sync();
@@ -313,6 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + lanebase + L::S(it & 1);
         if (ok) ok = mbar_wait(&s_full[it & 1], (uint32_t)(it >> 1) & 1u, p.status);
         __syncwarp();
+        if (i == w.i0) trace_mark(kTkLatentAttn, 0);
         tc_fence_after();
         uint32_t s[128];
 #pragma unroll
@@ -347,16 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (ok) ok = mbar_wait(&o_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u, p.status);
             __syncwarp();
             tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < kDV / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32_async(to + 32 * c, o);
-              tmem_wait_ld();
-              pin32(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(to + 32 * c, o);
-            }
+            rescale_columns<kDV / 32>(to, f);
           }
         }
         const float u = m == -INFINITY ? 0.f : m;
@@ -385,41 +378,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (ok) ok = mbar_wait(&o_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u, p.status);
       __syncwarp();
       tc_fence_after();
+      trace_mark(kTkLatentAttn, 1);
       const bool whole_item = w.starts() && w.ends();
       const int slot = w.starts() ? 1 : 0;
       const int qrow = w.s.row0 + tok;
       const bool mine = live && in_bounds(qrow < p.n_rows, p.status);
       const float inv = paged_inverse(l);
-      const size_t pr = ((size_t)pair * 2 + slot) * (2 * kRows) + rank * tpg * p.G + row;
-#pragma unroll 1
-      for (int c = 0; c < kDV / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32_async(to + 32 * c, o);
-        tmem_wait_ld();
-        pin32(o);
-        if (!whole_item) {
-          uint4 v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          store_quads<8>(v, mine ? p.part_o + pr * kDV + 32 * c : nullptr, lane);
-        } else {
-          uint16_t *d = static_cast<uint16_t *>(p.out) + (long long)qrow * p.ldo + hq * R + vh * kDV + 32 * c;
-          uint4 v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              y[j] = pack2(__uint_as_float(o[8 * e + 2 * j]) * inv, __uint_as_float(o[8 * e + 2 * j + 1]) * inv);
-            v[e] = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-          store_quads<4>(v, mine ? d : nullptr, lane);
-        }
-      }
+      const size_t block = (size_t)pair * 2 + slot;
+      const int srow = rank * tpg * p.G + row;  // in the pair's block
+      write_row<kDV / 32, 2 * kRows>(
+          to, 0, whole_item, mine ? static_cast<uint16_t *>(p.out) + (long long)qrow * p.ldo + hq * R + vh * kDV : nullptr, inv,
+          p.part_o + block * (2 * kRows) * kDV, mine ? srow : -1, lane);
       if (mine) {
         if (!whole_item) {
-          p.part_ml[pr * 2] = m;
-          p.part_ml[pr * 2 + 1] = l;
+          reinterpret_cast<float2 *>(p.part_ml)[block * (2 * kRows) + srow] = make_float2(m, l);
         } else if (p.lse && vh == 0) {
           p.lse[(size_t)qrow * p.Hq + hq] = paged_lse(m, l);
         }
@@ -432,6 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         d.last_cta = w.last_cta();
         p.desc[pair] = d;
       }
+      trace_mark(kTkLatentAttn, 2);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(dsmem_addr(o_empty, 0));
@@ -483,11 +456,7 @@ cudaError_t launch(const PagedTcParams &sp, int pairs, cudaStream_t s, bool pdl)
   note_launch();
   e = cudaLaunchKernelEx(&cfg, latent_attn_pair_kernel<R>, sp);
   if (e) return e;
-  cfg.gridDim = dim3(2 * 2 * pairs);
-  cfg.blockDim = dim3(kCombineThreads);
-  cfg.dynamicSmemBytes = 0;
-  note_launch();
-  return cudaLaunchKernelEx(&cfg, paged_combine_tc_kernel<kDV, 2 * kRows, Lay<R>::VH>, sp.a, pairs);
+  return launch_latent_combine<kDV, 2 * kRows, Lay<R>::VH>(sp, pairs, 2 * pairs, s, pdl);
 }
 
 }  // namespace

@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
   tc_fence_after();
   if (p.pages) m_tiles = table.before[kThreads];
   m_tiles = (m_tiles + CTAS - 1) / CTAS;  // of all the walker's rows
+  trace_mark(kTkLatentHeads, 0);
   const uint32_t tmem = *tmem_slot;
   const long long items = (long long)p.H * hp.n_tiles * m_tiles;
   bool ok = true;
@@ -310,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
       ok = __all_sync(kFull, ok && mbar_wait(&done[buf], (n >> 1) & 1u, p.status));
       if (!ok) break;
       tc_fence_after();
+      if (n == 0) trace_mark(kTkLatentHeads, 1);
       uint16_t *y = p.y + (long long)(r.row0 + row) * p.ldy + h * p.hsy + n0;
       const int cols = min(hp.NT, p.N - n0);
       for (int c = 64 * (warp >> 2); c < cols; c += 128) {
@@ -338,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
       }
     }
   }
+  trace_mark(kTkLatentHeads, 2);
   tc_fence_before();
   if constexpr (PAIR) cluster_sync();  // neither CTA leaves while the other may still signal it
   else __syncthreads();

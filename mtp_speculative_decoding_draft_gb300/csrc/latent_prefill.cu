@@ -19,9 +19,8 @@
 // queries, warp 11 clears rows of V that no row sees.
 #include "internal.h"
 #include "latent.cuh"
-#include "paged_combine.cuh"
 #include "paged_tc.cuh"
-#include "tcgen05.cuh"
+#include "latent_combine.cuh"
 
 namespace mtp {
 
@@ -40,7 +39,7 @@ struct Lay {
   static constexpr int KB = DN / 64 + 1, VB = DV / 64;  // blocks of a tile's keys and values
   static constexpr int NB = KB + VB;
   static constexpr int QTILE = KB * kBlk;               // a group's queries
-  static constexpr size_t SMEM = (size_t)2 * QTILE + kStages * kBlk + 512;
+  static constexpr size_t SMEM = (size_t)2 * QTILE + kStages * kBlk + 512 + kNearItems * sizeof(PagedItem);
 };
 
 struct PrefillParams {
@@ -91,12 +90,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
   grid_dep_wait();
   trace_dep(kTkLatentPrefill);
   grid_dep_launch();
-  PlanWalk<kTK> w(sp, blockIdx.x);
+  PagedItem *near = reinterpret_cast<PagedItem *>(smem + L::SMEM - kNearItems * sizeof(PagedItem));
+  PlanWalk<kTK, true> w(sp, blockIdx.x, near);
   if (tid == 0) p.desc[blockIdx.x].rows = 0;
   if (!w.valid()) {  // the same for the whole CTA
     trace_end(kTkLatentPrefill);
     return;
   }
+  w.copy_near(sp, blockIdx.x, near);
   if (warp == kIssuer) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
@@ -282,11 +283,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
       const int all_hi = min(w.s.ctx + tg0 + 1, p.cap);
       const int all_lo = p.window > 0 ? max(0, w.s.ctx + tg1 - 1 - p.window + 1) : 0;
       float m = -INFINITY, l = 0.f;
-      for (int i = w.i0; i < w.i1; ++i) {
+            for (int i = w.i0; i < w.i1; ++i) {
         const int k0 = w.r.tile(i) * kTK;
         const bool whole = k0 + kTK <= all_hi && (k0 >= all_lo || k0 + kTK <= min(p.sinks, all_hi));
         if (ok) ok = mbar_wait(&s_full[g], (uint32_t)(ns++) & 1u, p.status);
         __syncwarp();
+        if (i == w.i0) trace_mark(kTkLatentPrefill, 0);
         tc_fence_after();
         uint32_t s[128];
 #pragma unroll
@@ -315,16 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
           m = n;
           l *= f;
           if (i > w.i0) {
-#pragma unroll 1
-            for (int c = 0; c < DV / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32_async(to + 32 * c, o);
-              tmem_wait_ld();
-              pin32(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(to + 32 * c, o);
-            }
+            rescale_columns<DV / 32>(to, f);
           }
         }
         const float u = m == -INFINITY ? 0.f : m;
@@ -355,41 +348,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
       if (ok) ok = mbar_wait(&o_full[g], (uint32_t)(nseg++) & 1u, p.status);
       __syncwarp();
       tc_fence_after();
+      trace_mark(kTkLatentPrefill, 1);
       const bool whole_item = w.starts() && w.ends();
       const int slot = w.starts() ? 1 : 0;
       const int qrow = w.s.row0 + tok;
       const bool mine = live && in_bounds(qrow < p.n_rows, p.status);
       const float inv = paged_inverse(l);
-      const size_t pr = ((size_t)blockIdx.x * 2 + slot) * kPagedTcRows + g * 128 + row;
-#pragma unroll 1
-      for (int c = 0; c < DV / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32_async(to + 32 * c, o);
-        tmem_wait_ld();
-        pin32(o);
-        if (!whole_item) {
-          uint4 v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          store_quads<8>(v, mine ? p.part_o + pr * DV + 32 * c : nullptr, lane);
-        } else {
-          uint16_t *d = static_cast<uint16_t *>(p.out) + (long long)qrow * p.ldo + w.h * DV + 32 * c;
-          uint4 v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              y[j] = pack2(__uint_as_float(o[8 * e + 2 * j]) * inv, __uint_as_float(o[8 * e + 2 * j + 1]) * inv);
-            v[e] = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-          store_quads<4>(v, mine ? d : nullptr, lane);
-        }
-      }
+      const size_t block = (size_t)blockIdx.x * 2 + slot;
+      write_row<DV / 32, kPagedTcRows>(
+          to, 0, whole_item, mine ? static_cast<uint16_t *>(p.out) + (long long)qrow * p.ldo + w.h * DV : nullptr, inv,
+          p.part_o + block * kPagedTcRows * DV, mine ? g * 128 + row : -1, lane);
       if (mine) {
         if (!whole_item) {
-          p.part_ml[pr * 2] = m;
-          p.part_ml[pr * 2 + 1] = l;
+          reinterpret_cast<float2 *>(p.part_ml)[block * kPagedTcRows + g * 128 + row] = make_float2(m, l);
         } else if (p.lse) {
           p.lse[(size_t)qrow * p.Hq + w.h] = paged_lse(m, l);
         }
@@ -402,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
         d.last_cta = w.last_cta();
         p.desc[blockIdx.x] = d;
       }
+      trace_mark(kTkLatentPrefill, 2);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_empty[g]);
@@ -479,7 +451,8 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &lp, void *scratch, in
   if (lp.Dn == 128) e = lp.Dv == 128 ? launch<128, 128>(pp, n, s, pdl) : launch<128, 64>(pp, n, s, pdl);
   else e = lp.Dv == 128 ? launch<64, 128>(pp, n, s, pdl) : launch<64, 64>(pp, n, s, pdl);
   if (e) return e;
-  return launch_paged_combine(a, n, s, pdl);
+  return lp.Dv == 128 ? launch_latent_combine<128, kPagedTcRows, 1>(pp.tc, n, n, s, pdl)
+                      : launch_latent_combine<64, kPagedTcRows, 1>(pp.tc, n, n, s, pdl);
 }
 
 cudaError_t latent_prefill_set_attributes() {

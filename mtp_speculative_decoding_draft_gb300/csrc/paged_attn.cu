@@ -621,15 +621,6 @@ size_t paged_attn_scratch_bytes(int B, int Hkv, int n_rows, int max_rows, int G,
   return region_bytes(kMaxSms, kPagedTcRows, Dh) + paged_tc_plan_bytes(B, n_rows, 2 * (128 / G), Hkv);
 }
 
-cudaError_t launch_paged_combine(const PagedArgs &a, int ctas, cudaStream_t s, bool pdl) {
-  static_assert(kMaxSms <= kMaxDescs, "a description a CTA");
-  cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = config(dim3(6 * ctas), kCombineThreads, 0, s, attr, pdl);
-  note_launch();
-  return a.Dh == 64 ? cudaLaunchKernelEx(&cfg, paged_combine_tc_kernel<64, kPagedTcRows>, a, ctas)
-                    : cudaLaunchKernelEx(&cfg, paged_combine_tc_kernel<128, kPagedTcRows>, a, ctas);
-}
-
 cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const void *v_pages, int max_rows, void *scratch,
                               int sms, cudaStream_t s, bool pdl) {
   const long long packed = packed_rows(args.n_rows, max_rows, args.G);
@@ -650,7 +641,12 @@ cudaError_t launch_paged_attn(const PagedArgs &args, const void *k_pages, const 
         !make_query_map(&tp.mq, args.q, args.Dh, args.Hq, args.n_rows, args.ldq, args.G, 128 / args.G))
       return cudaErrorNotSupported;
     if ((e = launch_paged_attn_tc(tp, n, s, pdl))) return e;
-    return launch_paged_combine(tp.a, n, s, pdl);
+    static_assert(kMaxSms <= kMaxDescs, "a description a CTA");
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = config(dim3(6 * n), kCombineThreads, 0, s, attr, pdl);
+    note_launch();
+    return args.Dh == 64 ? cudaLaunchKernelEx(&cfg, paged_combine_tc_kernel<64, kPagedTcRows>, tp.a, n)
+                         : cudaLaunchKernelEx(&cfg, paged_combine_tc_kernel<128, kPagedTcRows>, tp.a, n);
   }
   StreamParams sp;
   sp.a = args;

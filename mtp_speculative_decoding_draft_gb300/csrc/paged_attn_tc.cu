@@ -585,6 +585,7 @@ size_t paged_tc_plan_bytes(int B, int n_rows, int tpb, int Hkv) {
 }
 
 void paged_tc_bind_plan(PagedTcParams &sp, char *base) {
+  sp.n_items = (int)plan_items(sp.a.B, sp.a.n_rows, sp.a.tpb, sp.a.Hkv);
   sp.start = reinterpret_cast<PagedStart *>(base);
   base += up256((size_t)kPagedMaxCtas * sizeof(PagedStart));
   sp.blocks = reinterpret_cast<int *>(base);

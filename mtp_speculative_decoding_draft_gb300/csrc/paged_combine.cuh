@@ -1,5 +1,5 @@
 // The kernel that joins the partial states of the tensor-core attention kernels
-// (paged_attn_tc.cu, latent_attn.cu, latent_prefill.cu) in key order.
+// (paged_attn_tc.cu) in key order.
 #pragma once
 
 #include "paged.cuh"
@@ -29,12 +29,11 @@ inline void bind_region(PagedArgs &a, char *base, int ctas, int rows) {
 constexpr int kCombineThreads = 256;
 constexpr int kMaxDescs = 256;  // CTAs at most
 
-// HALVES: an item is one of so many parts (of DH elements) of its heads' outputs.
-template <int DH, int ROWS, int HALVES = 1>
-__global__ void __launch_bounds__(kCombineThreads, DH > 128 ? 2 : 6)
+template <int DH, int ROWS>
+__global__ void __launch_bounds__(kCombineThreads, 6)
     paged_combine_tc_kernel(const __grid_constant__ PagedArgs p, int ctas) {
   trace_start(kTkPagedCombine);
-  constexpr int PER = DH / 32, kBatch = DH > 128 ? 4 : 2, NW = kCombineThreads / 32;
+  constexpr int PER = DH / 32, kBatch = 2, NW = kCombineThreads / 32;
   // a lane's elements: vectors of VEC, 32 VEC apart
   constexpr int VEC = PER < 4 ? PER : 4;
   auto place = [](int lane, int e) { return e / VEC * (32 * VEC) + lane * VEC + e % VEC; };
@@ -171,10 +170,9 @@ __global__ void __launch_bounds__(kCombineThreads, DH > 128 ? 2 : 6)
       __syncthreads();
     }
     const float inv = paged_inverse(S);
-    const int row = d.row0 + r / p.G, hq = d.h / HALVES * p.G + r % p.G, half = d.h % HALVES;
-    // (a block of heads may hold fewer than G at the end)
-    if (mine && q == 0 && hq < p.Hq && in_bounds(row < p.n_rows, p.status)) {
-      __nv_bfloat16 *at = static_cast<__nv_bfloat16 *>(p.out) + (long long)row * p.ldo + (hq * HALVES + half) * DH;
+    const int row = d.row0 + r / p.G, hq = d.h * p.G + r % p.G;
+    if (mine && q == 0 && in_bounds(row < p.n_rows, p.status)) {
+      __nv_bfloat16 *at = static_cast<__nv_bfloat16 *>(p.out) + (long long)row * p.ldo + hq * DH;
 #pragma unroll
       for (int e = 0; e < PER; e += VEC) {
         if constexpr (VEC == 4) {
@@ -186,7 +184,7 @@ __global__ void __launch_bounds__(kCombineThreads, DH > 128 ? 2 : 6)
           for (int j = 0; j < VEC; ++j) at[place(lane, e + j)] = __float2bfloat16_rn(a[e + j] * inv);
         }
       }
-      if (lane == 0 && p.lse && half == 0) p.lse[(size_t)row * p.Hq + hq] = paged_lse(M, S);
+      if (lane == 0 && p.lse) p.lse[(size_t)row * p.Hq + hq] = paged_lse(M, S);
     }
   }
   trace_end(kTkPagedCombine);

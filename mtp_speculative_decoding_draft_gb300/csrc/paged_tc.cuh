@@ -34,12 +34,17 @@ struct PagedTcParams {
   PagedStart *start;  // [CTAs]
   PagedItem *items;   // the line's items
   int item_cost;      // tiles that an item counts for besides its own
+  int n_items;        // places of the line
 };
+
+// A share's first items, copied into shared memory: a step to the next item costs two
+// round trips of L2 otherwise, with every warp waiting.
+constexpr int kNearItems = 16;
 
 // Walks a share's items in the plan's order, one segment at a time; the interface
 // of PagedWalk.  On the line an item is item_cost tiles, which stand for what a
 // segment costs besides its tiles (queries, first scores, output), then its tiles.
-template <int TK>
+template <int TK, bool NEAR = false>
 struct PlanWalk {
   const PagedTcParams &sp;
   const PagedArgs &p;
@@ -48,11 +53,14 @@ struct PlanWalk {
   PagedSeq s;
   PagedRange r;
   int i0, i1;
+  const PagedItem *near;  // items base .. base + kNearItems - 1
+  int base;
 
-  __device__ __forceinline__ explicit PlanWalk(const PagedTcParams &x, int share) : sp(x), p(x.a), i0(0), i1(0) {
+  __device__ __forceinline__ explicit PlanWalk(const PagedTcParams &x, int share, const PagedItem *copies = nullptr)
+      : sp(x), p(x.a), i0(0), i1(0), near(copies) {
     const PagedStart *st = &sp.start[share];
     const longlong2 e = __ldcg(reinterpret_cast<const longlong2 *>(&st->end));
-    i = __ldcg(&st->i);
+    i = base = __ldcg(&st->i);
     load(&st->item);
     end = e.x;
     per = e.y;
@@ -85,10 +93,36 @@ struct PlanWalk {
   __device__ __forceinline__ void next() {
     i0 = i1 = 0;
     if (first + sp.item_cost + r.count >= end) return;
+    if (NEAR) {
+      for (++i; i < base + kNearItems; ++i)
+        if (near[i - base].count != 0) {
+          take(near[i - base]);
+          cut();
+          return;
+        }
+      --i;
+    }
     do ++i;
     while (__ldcg(&sp.items[i].count) == 0);  // the line goes on: an item follows
     load(&sp.items[i]);
     cut();
+  }
+  __device__ __forceinline__ void take(const PagedItem &it) {
+    first = it.first;
+    b = it.b;
+    h = it.h;
+    t0 = it.t0;
+    s.row0 = it.row0;
+    s.n = it.n;
+    s.ctx = it.ctx;
+    r = paged_range<TK>(p, s, t0, t1());
+  }
+  // Executed by the whole CTA (a barrier follows): the copies of share's first items.
+  __device__ __forceinline__ static void copy_near(const PagedTcParams &sp, int share, PagedItem *copies) {
+    constexpr int kQuads = sizeof(PagedItem) / 16;
+    const int k = threadIdx.x / kQuads, e = threadIdx.x % kQuads, at = __ldcg(&sp.start[share].i) + k;
+    if (k < kNearItems && at < sp.n_items)
+      reinterpret_cast<int4 *>(copies + k)[e] = __ldcg(reinterpret_cast<const int4 *>(sp.items + at) + e);
   }
 };
 
@@ -107,8 +141,6 @@ void paged_tc_bind_plan(PagedTcParams &sp, char *base);
 // The plan of shares for `ctas` CTAs (or pairs), with tiles of TK keys (32, 64 or 128).
 template <int TK>
 cudaError_t launch_paged_plan(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl);
-// Joins the partial states of blocks of kPagedTcRows rows, heads of 64 or 128 (paged_attn.cu).
-cudaError_t launch_paged_combine(const PagedArgs &a, int ctas, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_attn_tc(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl);
 
 }  // namespace mtp
