@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   unsigned char *qbuf = smem, *ring = smem + L::QTILE;
   uint64_t *full = reinterpret_cast<uint64_t *>(ring + ST * L::TILE);  // [stages][groups]
   uint64_t *empty = full + ST * NG, *zbar = empty + ST;
-  uint64_t *q_full = zbar + ST, *q_empty = q_full + 1, *drain = q_full + 2;
-  uint64_t *s_full = q_full + 3, *p_full = s_full + 2, *o_done = s_full + 4, *o_empty = s_full + 6;
+  uint64_t *q_full = zbar + ST, *q_empty = q_full + NG, *drain = q_empty + 1;
+  uint64_t *s_full = drain + 1, *p_full = s_full + 2, *o_done = s_full + 4, *o_empty = s_full + 6;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 7);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
       mbar_init(&empty[s], 1);
       mbar_init(&zbar[s], 1);
     }
-    mbar_init(q_full, 1);
+    for (int g = 0; g < NG; ++g) mbar_init(&q_full[g], 1);
     mbar_init(q_empty, 1);
     mbar_init(drain, 1);
     for (int b = 0; b < 2; ++b) {
@@ -97,22 +97,21 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     mbar_init(o_empty, 4);
     fence_barrier_init();
   }
-  grid_dep_wait();
-  trace_dep(kTkLatentAttn);
-  grid_dep_launch();
-  PagedItem *near = reinterpret_cast<PagedItem *>(smem + L::SMEM - kNearItems * sizeof(PagedItem));
-  PlanWalk<TK, true> w(sp, blockIdx.x, near);
-  if (tid == 0) p.desc[blockIdx.x].rows = 0;
-  if (!w.valid()) {  // the same for the whole CTA
-    trace_end(kTkLatentAttn);
-    return;
-  }
-  w.copy_near(sp, blockIdx.x, near);
   if (warp == kIssuer) tmem_alloc(tmem_slot, 512);
+  if (warp == kProducer && lane == 0) prefetch_map(&sp.mk);
+  if (warp == kQuery && lane == 0) prefetch_map(&sp.mq);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();
+  trace_dep(kTkLatentAttn);
+  grid_dep_launch();
+  PagedItem *near = reinterpret_cast<PagedItem *>(smem + L::SMEM - kNearItems * sizeof(PagedItem));
+  PlanWalk<TK, true> w(sp, blockIdx.x, near);  // (no share, no segment)
+  if (tid == 0) p.desc[blockIdx.x].rows = 0;
+  if (w.valid()) w.copy_near(sp, blockIdx.x, near);
+  __syncthreads();
   bool ok = true;
 
   if (warp == kProducer) {
@@ -185,8 +184,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     if (lane == 0) {
       for (int seg = 0; w.valid(); w.next(), ++seg) {
         if (seg > 0 && !mbar_wait(q_empty, (uint32_t)(seg - 1) & 1u, p.status)) break;
-        mbar_arrive_expect_tx(q_full, (uint32_t)(NB * p.tpb * p.G * 128));
-        for (int x = 0; x < NB; ++x) tma_3d(qbuf + x * L::QBLK, &sp.mq, 64 * x, w.h * p.G, w.s.row0 + w.t0, q_full);
+        for (int x = 0; x < NB; ++x) {
+          if (x % 3 == 0) mbar_arrive_expect_tx(&q_full[x / 3], (uint32_t)(min(3, NB - x) * p.tpb * p.G * 128));
+          tma_3d(qbuf + x * L::QBLK, &sp.mq, 64 * x, w.h * p.G, w.s.row0 + w.t0, &q_full[x / 3]);
+        }
       }
     }
     __syncwarp();
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
     uint32_t oph = 1;
     for (; __shfl_sync(kFull, w.valid(), 0); w.next(), ++seg) {
       const int nt = __shfl_sync(kFull, w.i1 - w.i0, 0);
-      await(q_full, (uint32_t)seg & 1u);
+      for (int g = 0; g < NG; ++g) await(&q_full[g], (uint32_t)seg & 1u);
       for (int i = 0; i <= nt; ++i) {
         if (i < nt) {
           const int s = it % ST;

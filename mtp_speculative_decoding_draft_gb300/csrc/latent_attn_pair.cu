@@ -39,6 +39,7 @@ constexpr unsigned kFull = 0xffffffffu;
 template <int R>
 struct Lay {
   static constexpr int NB = R / 64 + 1;             // 64-element blocks of a row, the rotary one last
+  static constexpr int NG = (NB + 2) / 3;           // groups of blocks of the queries
   static constexpr int VH = R / kDV;                // items a block of rows
   static constexpr int QBLK = kRows * 128, QTILE = NB * QBLK;
   static constexpr int KBLK = 64 * 128;             // a block of keys: 64 rows of 128 bytes
@@ -56,14 +57,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     latent_attn_pair_kernel(const __grid_constant__ PagedTcParams sp) {
   trace_start(kTkLatentAttn);
   using L = Lay<R>;
-  constexpr int NB = L::NB, KST = L::KST, VST = L::VST, VH = L::VH;
+  constexpr int NB = L::NB, KST = L::KST, VST = L::VST, VH = L::VH, NG = L::NG;
   const PagedArgs &p = sp.a;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char *qbuf = smem, *kring = smem + L::QTILE, *vring = kring + KST * L::KBLK;
   uint64_t *k_full = reinterpret_cast<uint64_t *>(vring + VST * L::VTILE);
   uint64_t *k_empty = k_full + KST, *v_full = k_empty + KST, *v_empty = v_full + VST, *zbar = v_empty + VST;
-  uint64_t *q_full = zbar + VST, *q_empty = q_full + 1, *drain = q_full + 2, *o_empty = q_full + 3;
-  uint64_t *s_full = q_full + 4, *p_full = s_full + 2, *o_done = s_full + 4;
+  uint64_t *q_full = zbar + VST, *q_empty = q_full + NG, *drain = q_empty + 1, *o_empty = q_empty + 2;
+  uint64_t *s_full = q_empty + 3, *p_full = s_full + 2, *o_done = s_full + 4;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 6);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1;
@@ -78,7 +79,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&v_empty[s], 1);
       mbar_init(&zbar[s], 1);
     }
-    mbar_init(q_full, 2);
+    for (int g = 0; g < NG; ++g) mbar_init(&q_full[g], 2);
     mbar_init(q_empty, 1);
     mbar_init(drain, 1);
     mbar_init(o_empty, 8);
@@ -89,22 +90,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     fence_barrier_init();
   }
+  if (warp == kIssuer) tmem_alloc_pair(tmem_slot, 512);
+  if (warp == kKeys && lane == 0) prefetch_map(&sp.mk);
+  if (warp == kValues && lane == 0) prefetch_map(&sp.mv);
+  if (warp == kQuery && lane == 0) prefetch_map(&sp.mq);
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers are set up
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   grid_dep_wait();
   trace_dep(kTkLatentAttn);
   grid_dep_launch();
   PagedItem *near = reinterpret_cast<PagedItem *>(smem + L::SMEM - kNearItems * sizeof(PagedItem));
-  PlanWalk<kTK, true> w(sp, pair, near);
+  PlanWalk<kTK, true> w(sp, pair, near);  // (no share, no segment)
   if (tid == 0 && rank == 0) p.desc[pair].rows = 0;
-  if (!w.valid()) {  // the same for the whole pair
-    trace_end(kTkLatentAttn);
-    return;
-  }
-  w.copy_near(sp, pair, near);
-  if (warp == kIssuer) tmem_alloc_pair(tmem_slot, 512);
-  tc_fence_before();
-  cluster_sync();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  if (w.valid()) w.copy_near(sp, pair, near);
+  __syncthreads();
   const int tpg = kRows / p.G;  // tokens of a CTA
   bool ok = true;
 
@@ -210,12 +211,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int seg = 0; w.valid(); w.next(), ++seg) {
         if (seg > 0 && !mbar_wait(q_empty, (uint32_t)(seg - 1) & 1u, p.status)) break;
         const int t = w.t0 + rank * tpg;
-        const uint32_t bar = dsmem_addr(q_full, 0);
         const bool any = t < w.t1();  // else this CTA's rows are none: whatever lies there
-        expect_tx_cluster(bar, any ? (uint32_t)(NB * tpg * p.G * 128) : 0u);
-        if (any)
-          for (int x = 0; x < NB; ++x)
-            tma_3d_pair(qbuf + x * L::QBLK, &sp.mq, 64 * x, w.h / VH * p.G, w.s.row0 + t, bar);
+        for (int x = 0; x < NB; ++x) {
+          const uint32_t bar = dsmem_addr(&q_full[x / 3], 0);
+          if (x % 3 == 0) expect_tx_cluster(bar, any ? (uint32_t)(min(3, NB - x) * tpg * p.G * 128) : 0u);
+          if (any) tma_3d_pair(qbuf + x * L::QBLK, &sp.mq, 64 * x, w.h / VH * p.G, w.s.row0 + t, bar);
+        }
       }
     }
     __syncwarp();
@@ -237,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t kph = 0, vph = 0, oph = 1;
       for (; __shfl_sync(kFull, w.valid(), 0); w.next(), ++seg) {
         const int nt = __shfl_sync(kFull, w.i1 - w.i0, 0);
-        await(q_full, (uint32_t)seg & 1u);
+        for (int g = 0; g < NG; ++g) await(&q_full[g], (uint32_t)seg & 1u);
         for (int i = 0; i <= nt; ++i) {
           if (i < nt) {
             const uint32_t d = tm + L::S(it & 1);

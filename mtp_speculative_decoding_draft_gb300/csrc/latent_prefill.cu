@@ -9,13 +9,16 @@
 //                       filled up with zeros by the copies)
 //   P_g = 2^(S_g - m)   one thread a row, P back over S as bf16
 //   O_g += P_g V_i      tcgen05.mma, P from tensor memory, V row-major (MN-major)
-// Queries of 192 elements take 96 KB of shared memory, which leaves 128: the ring is
-// of blocks of 128 keys x 64 elements, each with a barrier of its own, so that a
-// tile's scores start on its first block and each block's place is free again as soon
-// as both groups have read it.
+// Queries of 192 elements take 96 KB of shared memory, which leaves 128 for 80 KB a tile.
+// Three places of two blocks (128 keys x 128 elements) go round: K_i's plain part is in
+// place i mod 3, V_i where K_{i-1}'s was; the shared parts have two places of their own.
+// So K_i waits for V_{i-2} and V_i for K_{i-1}, and every operand lies in one piece: with
+// blocks in a common ring, whose end parted a V tile now and then, the branches between the
+// products cost the issuing warp 160 cycles an instruction of 64.  The scores begin with the
+// shared part, which comes earlier.
 //
 // Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1, 128 each.  Warps 0-3 and 4-7 are
-// the groups' softmax, warp 8 brings blocks, warp 9 issues the products, warp 10 brings
+// the groups' softmax, warp 8 brings keys and values, warp 9 issues the products, warp 10 brings
 // queries, warp 11 clears rows of V that no row sees.
 #include "internal.h"
 #include "latent.cuh"
@@ -31,15 +34,14 @@ constexpr int kThreads = 384;
 constexpr int kItemCost = 6;
 constexpr int kProducer = 8, kIssuer = 9, kQuery = 10, kClear = 11;
 constexpr int kBlk = 128 * 128;  // bytes of a block: 128 rows of 128 bytes
-constexpr int kStages = 8;
 constexpr unsigned kFull = 0xffffffffu;
 
 template <int DN, int DV>
 struct Lay {
   static constexpr int KB = DN / 64 + 1, VB = DV / 64;  // blocks of a tile's keys and values
-  static constexpr int NB = KB + VB;
   static constexpr int QTILE = KB * kBlk;               // a group's queries
-  static constexpr size_t SMEM = (size_t)2 * QTILE + kStages * kBlk + 512 + kNearItems * sizeof(PagedItem);
+  static constexpr int PLACE = (DN > DV ? DN : DV) / 64 * kBlk;
+  static constexpr size_t SMEM = (size_t)2 * QTILE + 3 * PLACE + 2 * kBlk + 512 + kNearItems * sizeof(PagedItem);
 };
 
 struct PrefillParams {
@@ -55,26 +57,23 @@ template <int DN, int DV>
 __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __grid_constant__ PrefillParams pp) {
   trace_start(kTkLatentPrefill);
   using L = Lay<DN, DV>;
-  constexpr int KB = L::KB, VB = L::VB, NB = L::NB, ST = kStages;
+  constexpr int KB = L::KB, VB = L::VB;
   const PagedTcParams &sp = pp.tc;
   const PagedArgs &p = sp.a;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char *qbuf = smem;  // [2 groups][blocks][128][128 B]
-  unsigned char *ring = smem + 2 * L::QTILE;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(ring + ST * kBlk);
-  uint64_t *full = bars, *empty = bars + ST, *zbar = bars + 2 * ST;
-  uint64_t *q_full = bars + 3 * ST, *q_empty = q_full + 1, *drain = q_full + 2;
+  unsigned char *places = smem + 2 * L::QTILE, *shared = places + 3 * L::PLACE;
+  // of odd and even tiles: keys and values there, read, values to clear, shared parts there
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(shared + 2 * kBlk), *k_empty = k_full + 2, *v_full = k_full + 4,
+           *v_empty = k_full + 6, *zbar = k_full + 8, *r_full = k_full + 10;
+  uint64_t *q_full = r_full + 2, *q_empty = q_full + 1, *drain = q_full + 2;
   uint64_t *s_full = q_full + 3, *p_full = s_full + 2, *o_full = s_full + 4, *o_empty = s_full + 6, *p_half = s_full + 8;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 10);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr uint32_t kS = 0, kO = 256;  // columns of S_0 and O_0, the second group's 128 further
 
   if (tid == 0) {
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-      mbar_init(&zbar[s], 1);
-    }
+    for (int s = 0; s < 12; ++s) mbar_init(&k_full[s], 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     mbar_init(drain, 1);
@@ -87,77 +86,94 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
     }
     fence_barrier_init();
   }
-  grid_dep_wait();
-  trace_dep(kTkLatentPrefill);
-  grid_dep_launch();
-  PagedItem *near = reinterpret_cast<PagedItem *>(smem + L::SMEM - kNearItems * sizeof(PagedItem));
-  PlanWalk<kTK, true> w(sp, blockIdx.x, near);
-  if (tid == 0) p.desc[blockIdx.x].rows = 0;
-  if (!w.valid()) {  // the same for the whole CTA
-    trace_end(kTkLatentPrefill);
-    return;
-  }
-  w.copy_near(sp, blockIdx.x, near);
   if (warp == kIssuer) tmem_alloc(tmem_slot, 512);
+  if (warp == kProducer && lane == 0) {
+    prefetch_map(&sp.mk);
+    prefetch_map(&sp.mv);
+  }
+  if (warp == kQuery && lane == 0) prefetch_map(&sp.mq);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();
+  trace_dep(kTkLatentPrefill);
+  grid_dep_launch();
+  PagedItem *near = reinterpret_cast<PagedItem *>(smem + L::SMEM - kNearItems * sizeof(PagedItem));
+  PlanWalk<kTK, true> w(sp, blockIdx.x, near);  // (no share, no segment)
+  if (tid == 0) p.desc[blockIdx.x].rows = 0;
+  if (w.valid()) w.copy_near(sp, blockIdx.x, near);
+  __syncthreads();
   bool ok = true;
 
   // registers as in paged_attn_tc.cu: 384 x 168 = 256 x 216 + 128 x 72
   if (warp >= kProducer) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kProducer) {
-      // ------------------------------------------------ blocks of keys and values into the ring
+      // ------------------------------------------------ tiles of keys and values
       int it = 0;
       for (; w.valid() && ok; w.next()) {
         const int first = __ldcg(&pp.key_start[w.b]);
         if (lane == 0 && w.starts() && (first < 0 || (long long)first + w.s.ctx + w.s.n > pp.n_keys))
           set_status(p.status, kStatusBadCtx);
-        for (int i = w.i0; i < w.i1 && ok; ++i) {
+        for (int i = w.i0; i < w.i1 && ok; ++i, ++it) {
           const int t0 = w.r.tile(i) * kTK;
           // past the keys, either way, the copies read zeros
           const int y = (int)min(max((long long)first + t0, -(1ll << 30)), 1ll << 30);
           const bool whole = (t0 + kTK <= w.r.hi && t0 >= w.r.lo) || t0 + kTK <= w.r.sink_end;
-          for (int x = 0; x < NB && ok; ++x, ++it) {
-            const int s = it % ST;
-            if (it >= ST) ok = mbar_wait(&empty[s], (uint32_t)((it / ST) - 1) & 1u, p.status);
-            ok = __all_sync(kFull, ok);
-            if (!ok) break;
-            if (lane == 0) {
-              // a block of V with rows to clear goes to the clearing warp first
-              uint64_t *bar = x >= KB && !whole ? &zbar[s] : &full[s];
-              mbar_arrive_expect_tx(bar, kBlk);
-              if (x == KB - 1) tma_2d(ring + s * kBlk, &sp.mv, 0, y, bar);
-              else tma_2d(ring + s * kBlk, &sp.mk, w.h * pp.w + (x < KB ? 64 * x : DN + 64 * (x - KB)), y, bar);
-            }
-            __syncwarp();
+          const int odd = it & 1, place = it % 3;
+          if (lane == 0) {  // (V_{it-1} has waited for the scores of tile it - 2)
+            mbar_arrive_expect_tx(&r_full[odd], kBlk);
+            tma_2d(shared + odd * kBlk, &sp.mv, 0, y, &r_full[odd]);
           }
+          __syncwarp();
+          if (it >= 2) ok = mbar_wait(&v_empty[odd], (uint32_t)((it >> 1) - 1) & 1u, p.status);
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&k_full[odd], (KB - 1) * kBlk);
+#pragma unroll
+            for (int x = 0; x < KB - 1; ++x)
+              tma_2d(places + place * L::PLACE + x * kBlk, &sp.mk, w.h * pp.w + 64 * x, y, &k_full[odd]);
+          }
+          __syncwarp();
+          if (it >= 1) ok = mbar_wait(&k_empty[odd ^ 1], (uint32_t)((it - 1) >> 1) & 1u, p.status);
+          ok = __all_sync(kFull, ok);
+          if (lane == 0 && ok) {
+            // a tile of V with rows to clear goes to the clearing warp first
+            uint64_t *bar = whole ? &v_full[odd] : &zbar[odd];
+            mbar_arrive_expect_tx(bar, VB * kBlk);
+#pragma unroll
+            for (int x = 0; x < VB; ++x)
+              tma_2d(places + (it + 2) % 3 * L::PLACE + x * kBlk, &sp.mk, w.h * pp.w + DN + 64 * x, y, bar);
+          }
+          __syncwarp();
         }
       }
       if (!ok)  // let copies still in flight land before the CTA exits
-        for (int i = max(0, it - ST); i < it; ++i)
-          if (!mbar_wait(&full[i % ST], (uint32_t)(i / ST) & 1u, p.status)) break;
+        for (int i = max(0, it - 2); i <= it; ++i) {
+          if (!mbar_wait(&r_full[i & 1], (uint32_t)(i >> 1) & 1u, p.status)) break;
+          if (!mbar_wait(&k_full[i & 1], (uint32_t)(i >> 1) & 1u, p.status)) break;
+          if (i < it && !mbar_wait(&v_full[i & 1], (uint32_t)(i >> 1) & 1u, p.status)) break;
+        }
     } else if (warp == kClear) {
       // ------------------------------------------------ rows of V that no row sees
-      uint32_t phases = 0;  // a bit a stage
-      int it = KB;
+      uint32_t phases = 0;  // of odd and even tiles
+      int it = 0;
       for (; w.valid() && ok; w.next()) {
-        for (int i = w.i0; i < w.i1 && ok; ++i, it += NB) {
-          const int t0 = w.r.tile(i) * kTK;
+        for (int i = w.i0; i < w.i1 && ok; ++i, ++it) {
+          const int t0 = w.r.tile(i) * kTK, odd = it & 1;
           if ((t0 + kTK <= w.r.hi && t0 >= w.r.lo) || t0 + kTK <= w.r.sink_end) continue;
-          for (int v = 0; v < VB && ok; ++v) {
-            const int s = (it + v) % ST;
-            ok = __all_sync(kFull, mbar_wait(&zbar[s], phases >> s & 1u, p.status));
-            phases ^= 1u << s;
-            unsigned char *blk = ring + s * kBlk;
-            for (int x = lane; x < kTK * 8; x += 32)
-              if (!w.r.sees(t0 + (x >> 3))) *reinterpret_cast<uint4 *>(blk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[s]);
-          }
+          ok = __all_sync(kFull, mbar_wait(&zbar[odd], phases >> odd & 1u, p.status));
+          phases ^= 1u << odd;
+          unsigned char *tile = places + (it + 2) % 3 * L::PLACE;
+          for (int x = lane; x < kTK * 8; x += 32)
+            if (!w.r.sees(t0 + (x >> 3)))
+#pragma unroll
+              for (int v = 0; v < VB; ++v) *reinterpret_cast<uint4 *>(tile + v * kBlk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_full[odd]);
         }
       }
     } else if (warp == kQuery) {
@@ -176,89 +192,89 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
     } else if (warp == kIssuer) {
       // ------------------------------------------------ matrix products
       // The whole warp walks and waits, one elected lane issues (paged_attn_tc.cu).
-      constexpr uint32_t id_s = idesc_bf16_f32(128, 128), id_o = idesc_bf16_f32(128, DV) | (1u << 16),
-                         id_o1 = idesc_bf16_f32(128, 64) | (1u << 16);
+      constexpr uint32_t id_s = idesc_bf16_f32(128, 128), id_o = idesc_bf16_f32(128, DV) | (1u << 16);
       const uint32_t tm = __shfl_sync(kFull, tmem, 0);
-      const uint64_t qd = sw128_kmajor_desc(smem_u32(qbuf)), kd = sw128_kmajor_desc(smem_u32(ring)),
-                     vd = sw128_mnmajor_desc(smem_u32(ring), kBlk);
+      const uint64_t qd = sw128_kmajor_desc(smem_u32(qbuf)), kd = sw128_kmajor_desc(smem_u32(places)),
+                     rd = sw128_kmajor_desc(smem_u32(shared)), vd = sw128_mnmajor_desc(smem_u32(places), kBlk);
       const bool leader = elect_one();
       // A wait that gives up flags the status; the waits after it are skipped and
       // the rest is issued on whatever is there, so that no barrier is left short.
       auto await = [&](uint64_t *bar, uint32_t parity) {
         if (ok) ok = mbar_wait(bar, parity, p.status);
       };
-      int kb = 0, vb = 0, seg = 0;  // the tile's first block of keys, and of the values of the tile before
-      uint32_t pph[2] = {0, 0}, oph[2] = {1, 1};
+      int place = 0, seg = 0;  // K_i's place; V_{i-1} is in the second before it
+      uint32_t n = 0, pph[2] = {0, 0}, oph[2] = {1, 1};  // (n: tiles whose scores were issued)
       for (; __shfl_sync(kFull, w.valid(), 0); w.next(), ++seg) {
         const int ng = __shfl_sync(kFull, w.t1() - w.t0 > 128 ? 2 : 1, 0), nt = __shfl_sync(kFull, w.i1 - w.i0, 0);
         await(q_full, (uint32_t)seg & 1u);
         for (int i = 0; i <= nt; ++i) {
-          const int vs = vb % ST;
-          if (i > 0)
-#pragma unroll
-            for (int v = 0; v < VB; ++v) await(&full[(vb + v) % ST], (uint32_t)((vb + v) / ST) & 1u);
+          const uint32_t odd = n & 1u, last = n - 1u;  // K_n, V_{n-1}
+          if (i > 0) await(&v_full[odd ^ 1u], (last >> 1) & 1u);
+          const int vplace = place == 2 ? 0 : place + 1;  // (n - 1 + 2) mod 3
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             if (g >= ng) break;
             if (i > 0) {
-              // k-steps [k0, k1) of the product with V, whose blocks may part at the ring's end
-              auto product = [&](int k0, int k1) {
-                const uint64_t v = vd + (uint64_t)(vs * (kBlk >> 4));
-                if (VB == 1 || vs + 1 < ST) {
-                  for (int k = k0; k < k1; ++k)
-                    mma_ts(tm + kO + 128 * g, tm + kS + 128 * g + 8 * k, v + (uint64_t)(k * (2048 >> 4)), id_o, k > 0 || i > 1);
-                } else {
-                  for (int k = k0; k < k1; ++k) {
-                    mma_ts(tm + kO + 128 * g, tm + kS + 128 * g + 8 * k, v + (uint64_t)(k * (2048 >> 4)), id_o1, k > 0 || i > 1);
-                    mma_ts(tm + kO + 128 * g + 64, tm + kS + 128 * g + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), id_o1,
-                           k > 0 || i > 1);
-                  }
-                }
-              };
+              const uint64_t v = vd + (uint64_t)(vplace * (L::PLACE >> 4));
               if (i == 1) {
                 await(&o_empty[g], oph[g]);
                 oph[g] ^= 1u;
               }
               await(&p_half[g], pph[g]);
               tc_fence_after();
-              if (leader) product(0, kTK / 32);
+              if (leader) {
+#pragma unroll
+                for (int k = 0; k < kTK / 32; ++k)
+                  mma_ts(tm + kO + 128 * g, tm + kS + 128 * g + 8 * k, v + (uint64_t)(k * (2048 >> 4)), id_o, k > 0 || i > 1);
+              }
               await(&p_full[g], pph[g]);
               pph[g] ^= 1u;
               tc_fence_after();
               if (leader) {
-                product(kTK / 32, kTK / 16);
+#pragma unroll
+                for (int k = kTK / 32; k < kTK / 16; ++k)
+                  mma_ts(tm + kO + 128 * g, tm + kS + 128 * g + 8 * k, v + (uint64_t)(k * (2048 >> 4)), id_o, 1u);
                 if (i == nt) mma_commit(&o_full[g]);
+                if (g == ng - 1) mma_commit(&v_empty[odd ^ 1u]);
               }
             }
             if (i < nt) {
-              const uint64_t q = qd + (uint64_t)(g * (L::QTILE >> 4));
-#pragma unroll
-              for (int x = 0; x < KB; ++x) {
-                const int s = (kb + x) % ST;
-                if (g == 0) await(&full[s], (uint32_t)((kb + x) / ST) & 1u);
+              const uint64_t q = qd + (uint64_t)(g * (L::QTILE >> 4)), kk = kd + (uint64_t)(place * (L::PLACE >> 4)),
+                             rr = rd + (uint64_t)(odd * (kBlk >> 4));
+              if (g == 0) {
+                await(&r_full[odd], (n >> 1) & 1u);
                 tc_fence_after();
-                if (leader) {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    mma_bf16(tm + kS + 128 * g, q + (uint64_t)((x * kBlk + k * 32) >> 4),
-                             kd + (uint64_t)((s * kBlk + k * 32) >> 4), id_s, x > 0 || k > 0);
-                }
               }
-              if (leader) mma_commit(&s_full[g]);
+              if (leader) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_bf16(tm + kS + 128 * g, q + (uint64_t)(((KB - 1) * kBlk + k * 32) >> 4), rr + 2 * k, id_s, k > 0);
+              }
+              if (g == 0) {
+                await(&k_full[odd], (n >> 1) & 1u);
+                tc_fence_after();
+              }
+              if (leader) {
+#pragma unroll
+                for (int x = 0; x < KB - 1; ++x)
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const uint64_t off = (uint64_t)((x * kBlk + k * 32) >> 4);
+                    mma_bf16(tm + kS + 128 * g, q + off, kk + off, id_s, 1u);
+                  }
+                mma_commit(&s_full[g]);
+              }
             }
           }
           if (leader) {
-            if (i > 0)
-#pragma unroll
-              for (int v = 0; v < VB; ++v) mma_commit(&empty[(vb + v) % ST]);
-            if (i < nt)
-#pragma unroll
-              for (int x = 0; x < KB; ++x) mma_commit(&empty[(kb + x) % ST]);
+            if (i < nt) mma_commit(&k_empty[odd]);
             if (i == nt - 1) mma_commit(q_empty);  // the block's last scores
           }
           __syncwarp();
-          vb = kb + KB;
-          if (i < nt) kb += NB;
+          if (i < nt) {
+            ++n;
+            place = vplace;
+          }
         }
       }
       if (leader) mma_commit(drain);  // nothing of this CTA is in flight when it frees its tensor memory
@@ -301,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
           for (int c = 0; c < 4; ++c) {
             const int b = k0 + 32 * c;  // the row's view of 32 keys as bits
             const uint32_t see = below(rhi - b) & (~below(rlo - b) | below(p.sinks - b));
+            if (__all_sync(kFull, see == 0xffffffffu)) continue;  // on the diagonal half of them
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!(see >> e & 1u)) s[32 * c + e] = 0xff800000u;

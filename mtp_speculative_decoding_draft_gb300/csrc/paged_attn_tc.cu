@@ -92,14 +92,19 @@ __device__ __forceinline__ long long block_scan(long long v, long long *incl, lo
 
 }  // namespace
 
-// One CTA: the items of the batch, their order, and where each share starts.
+// One CTA: the items of the batch, their order, and where each share starts.  One item may
+// hold the starts of many shares (one user's few blocks over all CTAs), so that the shares
+// look for their items and not the other way round: a thread that wrote 19 starts in turn
+// took 2.2 of a plan's 4.9 us.
 template <int TK>
 __global__ void __launch_bounds__(kPlanThreads)
     paged_tc_plan_kernel(const __grid_constant__ PagedTcParams sp, int ctas) {
   trace_start(kTkPagedPlan);
-  constexpr int kNear = 1024;  // sequences whose blocks are kept in shared memory
+  constexpr int kNear = 1024;  // sequences that are kept in shared memory
   __shared__ long long scratch[kPlanThreads / 32];
   __shared__ int near_blocks[kNear + 1];
+  __shared__ PagedSeq near_seq[kNear];
+  __shared__ PagedItem round_items[kPlanThreads];
   const PagedArgs &p = sp.a;
   const int tid = threadIdx.x;
   const bool near = p.B <= kNear;
@@ -117,6 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       const PagedSeq s = paged_seq(p, b, true, &back);
       c = paged_cost<TK>(p, s, &u);
       nb = paged_blocks(p, s.n);
+      if (near) near_seq[b] = s;
     }
     const long long sum = block_scan(nb, &incl, scratch);
     if (b < p.B) {
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         if (first_item(mid) <= m) lo = mid;
         else hi = mid;
       }
-      const PagedSeq s = paged_seq(p, lo, false);
+      const PagedSeq s = near ? near_seq[lo] : paged_seq(p, lo, false);
       const int nb = paged_blocks(p, s.n), off = (int)(m - first_item(lo));
       it.b = lo;
       it.h = off / nb;
@@ -170,20 +176,28 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int len = it.count > 0 ? sp.item_cost + it.count : 0;  // on the line
     const long long sum = block_scan(len, &incl, scratch);
     it.first = before + incl - len;
-    before += sum;
-    if (i < places) {
-      sp.items[i] = it;
-      // the shares that start inside this item
-      if (it.count > 0)
-        for (long long c = (it.first + per - 1) / per; c * per < it.first + len && c < ctas; ++c) {
-          PagedStart st{};
-          st.item = it;
-          st.end = min(total, (c + 1) * per);
-          st.per = per;
-          st.i = (int)i;
-          sp.start[c] = st;
-        }
+    round_items[tid] = it;
+    if (i < places) sp.items[i] = it;
+    __syncthreads();
+    // ---- the shares that start inside this round's items
+    for (int c = tid; c < ctas; c += kPlanThreads) {
+      const long long at = c * per;
+      if (at < before || at >= before + sum) continue;
+      int lo = 0, hi = kPlanThreads;  // the last item that starts at or before it (gaps start where their next item does)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (round_items[mid].first <= at) lo = mid;
+        else hi = mid;
+      }
+      PagedStart st{};
+      st.item = round_items[lo];
+      st.end = min(total, at + per);
+      st.per = per;
+      st.i = (int)(base + lo);
+      sp.start[c] = st;
     }
+    before += sum;
+    __syncthreads();  // the round's items are read
   }
   trace_end(kTkPagedPlan);
 }

@@ -250,6 +250,11 @@ __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *m, int x, i
       : "memory");
 }
 
+// Fetches a tensor map ahead of its first use.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 // ---------------------------------------------------------------- pairs of CTAs
 //
 // In a cluster of two, one thread of the first CTA issues products of both: each CTA's
