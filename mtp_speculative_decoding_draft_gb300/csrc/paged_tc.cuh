@@ -103,7 +103,8 @@ struct PlanWalk {
       --i;
     }
     do ++i;
-    while (__ldcg(&sp.items[i].count) == 0);  // the line goes on: an item follows
+    while ((!NEAR || i < sp.n_items) && __ldcg(&sp.items[i].count) == 0);  // the line goes on: an item follows
+    if (NEAR && i >= sp.n_items) return;  // (only if the workspace was overwritten meanwhile)
     load(&sp.items[i]);
     cut();
   }
