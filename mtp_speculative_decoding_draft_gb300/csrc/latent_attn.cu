@@ -108,9 +108,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const __grid_c
   trace_dep(kTkLatentAttn);
   grid_dep_launch();
   PagedItem *near = reinterpret_cast<PagedItem *>(smem + L::SMEM - kNearItems * sizeof(PagedItem));
-  PlanWalk<TK, true> w(sp, blockIdx.x, near);  // (no share, no segment)
+  SmallPlan *plan = reinterpret_cast<SmallPlan *>(ring);  // (before the first copy)
+  if (sp.small) plan_share<TK, kThreads>(sp, sp.shares, blockIdx.x, plan, near);
+  PlanWalk<TK, true> w = sp.small ? PlanWalk<TK, true>(sp, blockIdx.x, plan->start, near) : PlanWalk<TK, true>(sp, blockIdx.x, near);
+  // (no share, no segment)
   if (tid == 0) p.desc[blockIdx.x].rows = 0;
-  if (w.valid()) w.copy_near(sp, blockIdx.x, near);
+  if (!sp.small && w.valid()) w.copy_near(sp, blockIdx.x, near);
+  fence_proxy_async_smem();  // the plan's memory is the copies' next
   __syncthreads();
   bool ok = true;
 
@@ -410,7 +414,7 @@ void block_shape(int B, int n_rows, int H, int *G, int *hb) {
 
 template <int R>
 cudaError_t launch(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl) {
-  cudaError_t e = launch_paged_plan<Lay<R>::TK>(sp, ctas, s, pdl);
+  cudaError_t e = sp.small ? cudaSuccess : launch_paged_plan<Lay<R>::TK>(sp, ctas, s, pdl);
   if (e) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
@@ -462,6 +466,7 @@ cudaError_t launch_latent_attn(const LatentAttnArgs &la, void *scratch, int sms,
   char *base = static_cast<char *>(scratch);
   bind_region(a, base, n, kRows);
   paged_tc_bind_plan(sp, base + region_bytes(kPagedMaxCtas, kRows, a.Dh));
+  paged_small_plan(sp, n);
   if (!make_rows_map(&sp.mk, la.pages, w, (uint64_t)a.n_pages * a.page, w, a.page < tk ? a.page : tk) ||
       !make_query_map(&sp.mq, a.q, w, a.Hq, a.n_rows, a.ldq, a.G, a.tpb))
     return cudaErrorNotSupported;

@@ -102,9 +102,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   trace_dep(kTkLatentAttn);
   grid_dep_launch();
   PagedItem *near = reinterpret_cast<PagedItem *>(smem + L::SMEM - kNearItems * sizeof(PagedItem));
-  PlanWalk<kTK, true> w(sp, pair, near);  // (no share, no segment)
+  SmallPlan *plan = reinterpret_cast<SmallPlan *>(kring);  // (before the first copy)
+  if (sp.small) plan_share<kTK, kThreads>(sp, sp.shares, pair, plan, near);
+  PlanWalk<kTK, true> w = sp.small ? PlanWalk<kTK, true>(sp, pair, plan->start, near) : PlanWalk<kTK, true>(sp, pair, near);
+  // (no share, no segment)
   if (tid == 0 && rank == 0) p.desc[pair].rows = 0;
-  if (w.valid()) w.copy_near(sp, pair, near);
+  if (!sp.small && w.valid()) w.copy_near(sp, pair, near);
+  fence_proxy_async_smem();  // the plan's memory is the copies' next
   __syncthreads();
   const int tpg = kRows / p.G;  // tokens of a CTA
   bool ok = true;
@@ -442,7 +446,7 @@ void block_shape(int B, int n_rows, int H, int *G, int *hb) {
 
 template <int R>
 cudaError_t launch(const PagedTcParams &sp, int pairs, cudaStream_t s, bool pdl) {
-  cudaError_t e = launch_paged_plan<kTK>(sp, pairs, s, pdl);
+  cudaError_t e = sp.small ? cudaSuccess : launch_paged_plan<kTK>(sp, pairs, s, pdl);
   if (e) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(2 * pairs);
@@ -488,6 +492,7 @@ cudaError_t launch_latent_attn_pair(const LatentAttnArgs &la, void *scratch, int
   char *base = static_cast<char *>(scratch);
   bind_region(a, base, n, 2 * kRows);
   paged_tc_bind_plan(sp, base + region_bytes(kPagedMaxCtas / 2, 2 * kRows, kDV));
+  paged_small_plan(sp, n);
   const uint64_t rows = (uint64_t)a.n_pages * a.page;
   if (!make_rows_map(&sp.mk, la.pages, w, rows, w, a.page < 64 ? a.page : 64) ||
       !make_rows_map(&sp.mv, la.pages, w, rows, w, a.page) ||

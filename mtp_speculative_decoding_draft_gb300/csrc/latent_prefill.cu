@@ -100,9 +100,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
   trace_dep(kTkLatentPrefill);
   grid_dep_launch();
   PagedItem *near = reinterpret_cast<PagedItem *>(smem + L::SMEM - kNearItems * sizeof(PagedItem));
-  PlanWalk<kTK, true> w(sp, blockIdx.x, near);  // (no share, no segment)
+  SmallPlan *plan = reinterpret_cast<SmallPlan *>(places);  // (before the first copy)
+  if (sp.small) plan_share<kTK, kThreads>(sp, sp.shares, blockIdx.x, plan, near);
+  PlanWalk<kTK, true> w = sp.small ? PlanWalk<kTK, true>(sp, blockIdx.x, plan->start, near) : PlanWalk<kTK, true>(sp, blockIdx.x, near);
+  // (no share, no segment)
   if (tid == 0) p.desc[blockIdx.x].rows = 0;
-  if (w.valid()) w.copy_near(sp, blockIdx.x, near);
+  if (!sp.small && w.valid()) w.copy_near(sp, blockIdx.x, near);
+  fence_proxy_async_smem();  // the plan's memory is the copies' next
   __syncthreads();
   bool ok = true;
 
@@ -459,11 +463,12 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &lp, void *scratch, in
   char *base = static_cast<char *>(scratch);
   bind_region(a, base, n, kPagedTcRows);
   paged_tc_bind_plan(pp.tc, base + region_bytes(kPagedMaxCtas, kPagedTcRows, a.Dh));
+  paged_small_plan(pp.tc, n);
   if (!make_rows_map(&pp.tc.mk, lp.kv, (uint64_t)a.Hq * pp.w, lp.n_keys, lp.ldkv, kTK) ||
       !make_rows_map(&pp.tc.mv, lp.k_rope, lp.Dr, lp.n_keys, lp.ldkr, kTK) ||
       !make_query_map(&pp.tc.mq, a.q, lp.Dn + lp.Dr, a.Hq, a.n_rows, a.ldq, 1, 128))
     return cudaErrorNotSupported;
-  cudaError_t e = launch_paged_plan<kTK>(pp.tc, n, s, pdl);
+  cudaError_t e = pp.tc.small ? cudaSuccess : launch_paged_plan<kTK>(pp.tc, n, s, pdl);
   if (e) return e;
   if (lp.Dn == 128) e = lp.Dv == 128 ? launch<128, 128>(pp, n, s, pdl) : launch<128, 64>(pp, n, s, pdl);
   else e = lp.Dv == 128 ? launch<64, 128>(pp, n, s, pdl) : launch<64, 64>(pp, n, s, pdl);

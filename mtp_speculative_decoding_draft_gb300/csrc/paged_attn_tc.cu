@@ -68,28 +68,6 @@ struct Lay {
 
 constexpr int kPlanThreads = 512;
 
-// Inclusive scan over the block's threads; returns the block's sum.
-__device__ __forceinline__ long long block_scan(long long v, long long *incl, long long *scratch) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(kFull, v, o);
-    if (lane >= o) v += u;
-  }
-  __syncthreads();  // scratch is free again
-  if (lane == 31) scratch[warp] = v;
-  __syncthreads();
-  long long w = lane < kPlanThreads / 32 ? scratch[lane] : 0;  // every warp scans the warps' sums
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(kFull, w, o);
-    if (lane >= o) w += u;
-  }
-  const long long before = __shfl_sync(kFull, w, (warp + 31) & 31);
-  *incl = v + (warp > 0 ? before : 0);
-  return __shfl_sync(kFull, w, 31);
-}
-
 }  // namespace
 
 // One CTA: the items of the batch, their order, and where each share starts.  One item may
@@ -124,14 +102,14 @@ __global__ void __launch_bounds__(kPlanThreads)
       nb = paged_blocks(p, s.n);
       if (near) near_seq[b] = s;
     }
-    const long long sum = block_scan(nb, &incl, scratch);
+    const long long sum = block_scan<kPlanThreads>(nb, &incl, scratch);
     if (b < p.B) {
       const int before = (int)(nblk + incl - nb);
       if (near) near_blocks[b] = before;
       else sp.blocks[b] = before;
     }
     nblk += sum;
-    total += block_scan((c + (long long)nb * sp.item_cost) * p.Hkv, &incl, scratch);
+    total += block_scan<kPlanThreads>((c + (long long)nb * sp.item_cost) * p.Hkv, &incl, scratch);
   }
   if (tid == 0) {
     if (near) near_blocks[p.B] = (int)nblk;
@@ -174,7 +152,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       it.ctx = s.ctx;
     }
     const int len = it.count > 0 ? sp.item_cost + it.count : 0;  // on the line
-    const long long sum = block_scan(len, &incl, scratch);
+    const long long sum = block_scan<kPlanThreads>(len, &incl, scratch);
     it.first = before + incl - len;
     round_items[tid] = it;
     if (i < places) sp.items[i] = it;

@@ -58,11 +58,11 @@ def sees(ctx, n, keys, window, sinks):
     return s
 
 
-def attention(q, k, v, visible, scale):
+def attention(q, k, v, visible, scale, device="cpu"):
     """One sequence in 64 bits: q [n, H, D], k [L, H or 1, D], v [L, H or 1, Dv].  Returns
     (out, lse, spread, score error): spread is sum_j p_j |v_j|, the score error how far an
     fp32 score of the row may be from the exact one."""
-    q, k, v = (x.double().cpu().transpose(0, 1) for x in (q, k, v))
+    q, k, v = (x.to(device).double().transpose(0, 1) for x in (q, k, v))
     s = scale * (q @ k.transpose(1, 2)).masked_fill(~visible[None], -math.inf)
     mag = scale * (q.abs() @ k.abs().transpose(1, 2)).masked_fill(~visible[None], 0)
     lse = torch.logsumexp(s, dim=-1)

@@ -3,8 +3,8 @@
 import pytest
 import torch
 
-from latent_helpers import (attend, check_attend, check_prefill, check_product, make_latent, make_prompt, norm_reference,
-                            prefill)
+from latent_helpers import (attend, attention, check_attend, check_prefill, check_product, check_rows, make_latent, make_prompt,
+                            norm_reference, prefill, sees)
 from paged_helpers import append_reference
 
 pytestmark = pytest.mark.gpu
@@ -287,6 +287,32 @@ def test_attend_long_contexts_split_and_joined():
     check_attend(d, *attend(d))
 
 
+@pytest.mark.parametrize("H,rows", [(16, [1] * 20), (128, [1, 0, 2, 1]), (40, [4, 4, 4, 0, 1]), (64, [2] * 9)])
+def test_attend_few_items(H, rows):
+    """Calls small enough that every CTA makes the plan for itself; and rows that end early."""
+    for R, Dr in ((512, 64), (256, 32)):
+        d = make_latent(rows, [(b * 531) % 1500 for b in range(len(rows))], H, R, Dr, 32, seed=H, pad=1)
+        out, lse = attend(d)
+        check_attend(d, out, lse)
+        assert (out[sum(rows):] == 7).all()
+
+
+@pytest.mark.parametrize("n", [12, 17])                       # the plan in every CTA, and in a kernel of its own
+def test_attend_one_long_and_many_short(n):
+    """Shares of 17 and more items: one sequence is as long as many others are short."""
+    long, H = 260000, 128
+    d = make_latent([1] * n + [2] + [1] * n, [b % 5 for b in range(n)] + [long] + [b % 7 for b in range(n)], H, 512, 64, 128, seed=3)
+    out, lse = attend(d)
+    assert torch.isfinite(out).all()
+    short = dict(d, rows=[1] * n, ctx=d["ctx"][:n], seqs=d["seqs"][:n], q=d["q"][:n], n_rows=n)
+    check_attend(short, out[:n], lse[:n])
+    short = dict(d, rows=[1] * n, ctx=d["ctx"][n + 1:], seqs=d["seqs"][n + 1:], q=d["q"][n + 2:], n_rows=n)
+    check_attend(short, out[n + 2:], lse[n + 2:])
+    k = d["seqs"][n][:, None]
+    ref = [x.cpu() for x in attention(d["q"][n:n + 2], k, k[..., :512], sees(long, 2, long + 2, 0, 0).cuda(), d["scale"], "cuda")]
+    check_rows(ref, out[n:n + 2], lse[n:n + 2], 2, long + 2)
+
+
 @pytest.mark.parametrize("B", [64, 600, 1100])
 def test_attend_large_batches(B):
     rows = [(b * 7) % 4 for b in range(B)]
@@ -362,6 +388,12 @@ def test_prefill_large_batches(B):
     rows[B // 2] = 300
     d = make_prompt(rows, ctx, 2, 64, 32, 64, seed=B, pad=3)
     check_prefill(d, *prefill(d))
+
+
+def test_prefill_few_items():
+    for rows, ctx, H in (([1, 2, 0, 1], [900, 5, 7, 0], 8), ([300], [40], 4), ([1], [0], 1), ([257, 3], [1000, 2000], 16)):
+        d = make_prompt(rows, ctx, H, 128, 64, 128, seed=H, pad=1)
+        check_prefill(d, *prefill(d))
 
 
 def test_prefill_of_fresh_prompts_takes_row_start():
