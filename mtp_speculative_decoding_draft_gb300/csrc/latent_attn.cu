@@ -461,8 +461,11 @@ cudaError_t launch_latent_attn(const LatentAttnArgs &la, void *scratch, int sms,
   block_shape(a.B, a.n_rows, a.Hq, &a.G, &a.Hkv);
   a.tpb = kRows / a.G;
   const int tk = a.Dh == 512 ? Lay<512>::TK : Lay<256>::TK;
-  a.min_tiles = 256 / tk;
-  sp.item_cost = 256 / tk;
+  // shares of at least 64 / 128 / 256 keys (us, one row of 16 heads, R 512): one sequence of 512
+  // keys 10.4 / 12.1 / 15.4, of 4096 12.8 / 13.3 / 16.0; 4 of 2048 13.0 / 13.8 / 16.7; R 256 (128 and
+  // 256): 10.1 / 11.2, 11.4 / 11.8, 11.2 / 12.2
+  a.min_tiles = 2;
+  sp.item_cost = 128 / tk;
   char *base = static_cast<char *>(scratch);
   bind_region(a, base, n, kRows);
   paged_tc_bind_plan(sp, base + region_bytes(kPagedMaxCtas, kRows, a.Dh));

@@ -217,9 +217,9 @@ __global__ void __launch_bounds__(kLatentCombineThreads, 4)
 }
 
 // Few items cut into many states: a block joins 32 rows x 16 elements, each of its warps
-// every eighth state.
+// every eighth state, three requested together (one user's 20 states in one round).
 template <int DH, int ROWS, int PARTS>
-__global__ void __launch_bounds__(kLatentCombineThreads, 3)
+__global__ void __launch_bounds__(kLatentCombineThreads, 2)
     latent_combine_many_kernel(const __grid_constant__ PagedArgs p, int shares) {
   trace_start(kTkPagedCombine);
   constexpr int NW = kLatentCombineThreads / 32, CW = 16, CU = DH / CW;
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kLatentCombineThreads, 3)
     const int c = u % CU;
     const CombineGroup g = table.find(u / CU);
     float M, S, a[CW];
-    join_states<DH, ROWS, CW, 2>(p, g, min(g.r0 + lane, g.d.rows - 1), CW * c, warp, NW, M, S, a);
+    join_states<DH, ROWS, CW, 3>(p, g, min(g.r0 + lane, g.d.rows - 1), CW * c, warp, NW, M, S, a);
 #pragma unroll
     for (int e = 0; e < CW; ++e) part[warp][e][lane] = a[e];
     stat[warp][0][lane] = M;

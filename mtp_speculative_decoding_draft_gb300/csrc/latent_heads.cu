@@ -148,6 +148,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
     if constexpr (PAIR) tmem_alloc_pair(tmem_slot, 512);
     else tmem_alloc(tmem_slot, 512);
   }
+  if (warp == kProducer && lane == 0) {
+    prefetch_map(&hp.mx);
+    prefetch_map(&hp.mw);
+  }
+  tc_fence_before();
+  if constexpr (PAIR) cluster_sync();  // the barriers of both CTAs are set up
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   grid_dep_wait();
   trace_dep(kTkLatentHeads);
   grid_dep_launch();
@@ -177,14 +186,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
       for (int j = 0; j < n && before < kNear; j += 128) table.near[before++] = {b, j, s + j, min(128, n - j)};
     }
   }
-  tc_fence_before();
-  if constexpr (PAIR) cluster_sync();  // the barriers of both CTAs are set up
-  else __syncthreads();
-  tc_fence_after();
-  if (p.pages) m_tiles = table.before[kThreads];
+  if (p.pages) {
+    __syncthreads();
+    m_tiles = table.before[kThreads];
+  }
   m_tiles = (m_tiles + CTAS - 1) / CTAS;  // of all the walker's rows
   trace_mark(kTkLatentHeads, 0);
-  const uint32_t tmem = *tmem_slot;
   const long long items = (long long)p.H * hp.n_tiles * m_tiles;
   bool ok = true;
 
