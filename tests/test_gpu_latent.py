@@ -218,6 +218,13 @@ def test_expand_sizes_of_heads():
         check_expanded(d, [70, 200], H, N)
 
 
+@pytest.mark.parametrize("R,Dr", [(256, 64), (512, 32)])
+def test_expand_of_many_row_tiles(R, Dr):
+    """More tiles of rows than there are SMs: rows are kept, given up and brought again."""
+    n = [45000, 1, 0, 1300]
+    check_expanded(make_latent(n, [0] * 4, 1, R, Dr, 128, seed=R), n, 3, 64, pad=1)
+
+
 def test_expand_of_many_sequences():
     n = [(b * 5) % 9 for b in range(700)]
     check_expanded(make_latent(n, [0] * 700, 1, 256, 32, 16, seed=1), n, 2, 64, pad=3)

@@ -4,7 +4,7 @@ then candidate rows through the absorbed one, over the same pages."""
 import pytest
 import torch
 
-from latent_helpers import attention, attend, check_attend, check_product, make_latent, make_prompt, norm_reference, prefill, sees
+from latent_helpers import attention, attend, check_attend, check_product, check_rows, make_latent, make_prompt, norm_reference, prefill, sees
 from paged_helpers import append_reference
 
 pytestmark = pytest.mark.gpu
@@ -225,3 +225,33 @@ def test_pools_past_32_bits():
     at = [(0, 100), (0, 101), (0, 102), (1, 70), (1, 71)]
     for i, (b, j) in enumerate(at):
         assert torch.equal(pool[int(d["table"][b, j // page]), j % page], rows[i])
+
+
+def test_keys_and_values_past_32_bits():
+    """Expanded keys and values of more than 2^31 elements, and prompts' rows over them."""
+    from mtp_speculative_decoding_draft_gb300 import binding as bd
+    R, Dr, H, Dn, Dv, page = 256, 32, 128, 128, 128, 128
+    total, ctx, rows = [65700, 300], [65697, 295], [3, 5]
+    d = make_latent(rows, ctx, 1, R, Dr, page, seed=8)
+    lat = [s.cuda() for s in d["seqs"]]
+    n = sum(total)
+    w, ws = torch.randn(H, Dn + Dv, R, **BF) / 16, bd.alloc_workspace(256)
+    kv, kr = torch.empty(n, H, Dn + Dv, **BF), torch.empty(n, Dr, **BF)
+    assert kv.numel() > 2 ** 31
+    starts = torch.tensor([0, total[0], n], dtype=torch.int32, device="cuda")
+    bd.mtp_latent_expand(bd.make_latent_cache(d["pages"], d["table"], Dr), starts, w, kv, kr, ws)
+    torch.cuda.synchronize()
+    assert bd.get_status(ws) == 0 and torch.equal(kr, torch.cat(lat)[:, R:])
+    check_product(lat[1][:, None, :R].expand(-1, H, -1), w, kv[total[0]:])
+    check_product(lat[0][-100:, None, :R].expand(-1, H, -1), w, kv[total[0] - 100:total[0]])
+    q = torch.randn(sum(rows), H, Dn + Dr, **BF)
+    p = dict(B=2, H=H, Dn=Dn, Dr=Dr, Dv=Dv, n_rows=sum(rows), window=0, sinks=0, scale=(Dn + Dr) ** -0.5, q=q, kv=kv, k_rope=kr,
+             row_start=d["row_start"], ctx_len=d["ctx_len"], key_start=starts)
+    out, lse = prefill(p)
+    r = 0
+    for b, m in enumerate(rows):
+        at, e, heads = slice(int(starts[b]), int(starts[b + 1])), slice(r, r + m), [0, 63, 127]
+        k = torch.cat([kv[at, heads, :Dn], kr[at, None].expand(-1, 3, -1)], dim=-1)
+        ref = attention(q[e][:, heads], k, kv[at, heads, Dn:], sees(ctx[b], m, total[b], 0, 0), p["scale"])
+        check_rows(ref, out[e][:, heads], lse[e][:, heads], m, total[b])
+        r += m
