@@ -4,7 +4,8 @@
 // as value.  A block is 64 packed rows (tokens x heads); with more heads than that, a
 // block holds part of a token's heads.  Its items are cut and dealt out by the plan of
 // paged_attn_tc.cu, a CTA an SM, tiles of 32 or 64 keys:
-//   S = Q K_i^T     64 rows, over R + 64 elements; both operands in shared memory by TMA
+//   S = Q K_i^T     64 rows, over R + 64 elements (zeros from Dr on: the cache's bytes bind);
+//                   both operands in shared memory by TMA
 //   P = 2^(S - m)   two threads a row, half of the keys each
 //   O += P V_i      V_i the first R elements of K_i as they lie in shared memory
 //                   (row-major keys: the MN-major form of operand B)
@@ -16,8 +17,9 @@
 // S of 64 rows arrives in the lanes l < 16 of each 32.
 //
 // S_{i+1} is issued ahead of O += P_i V_i, so that the softmax of one tile runs under
-// the products of another.  Tensor memory (512 columns): O 256 | S_0 S_1 128 | P_0 P_1 128.  Warps 0-3 are the softmax, warp 4 brings pages, warp 5 issues the
-// products, warp 6 brings the next block's queries, warp 7 clears rows that no row sees.
+// the products of another.  Tensor memory (512 columns): O 256 | S_0 S_1 128 | P_0 P_1 128.
+// Warps 0-3 are the softmax, warp 4 brings pages, warp 5 issues the products, warp 6 brings
+// the next block's queries, warp 7 clears rows that no row sees.
 #include "internal.h"
 #include "latent.cuh"
 #include "paged_tc.cuh"

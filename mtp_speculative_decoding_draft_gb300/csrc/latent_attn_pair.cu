@@ -3,7 +3,7 @@
 //
 // A pair (a cluster of two, tcgen05 with cta_group::2) holds a block of 256 packed rows,
 // 128 a CTA, and walks tiles of 128 keys:
-//   S = Q K_i^T     256 x 128 over R + 64 elements: each CTA brings 64 of the keys
+//   S = Q K_i^T     256 x 128 over R + Dr elements: each CTA brings 64 of the keys
 //   P = 2^(S - m)   one thread a row, P back over S as bf16
 //   O += P V_i      256 x 256: each CTA brings 128 of the 256 elements of V
 // The output of 128 rows and 512 elements would be all of tensor memory.  So an item is
@@ -253,7 +253,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (leader) {
                 const uint64_t q = qd + (uint64_t)(x * (L::QBLK >> 4)), kk = kd + (uint64_t)(ks * (L::KBLK >> 4));
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_bf16_pair(d, q + 2 * k, kk + 2 * k, id_s, x > 0 || k > 0);
+                for (int k = 0; k < 2; ++k) mma_bf16_pair(d, q + 2 * k, kk + 2 * k, id_s, x > 0 || k > 0);
+                // (the last block's second half may be zeros; 12 ragged chunks, 40 heads of 256 + 32: 361 -> 349 us)
+                if (x < NB - 1 || sp.rope > 32)
+#pragma unroll
+                  for (int k = 2; k < 4; ++k) mma_bf16_pair(d, q + 2 * k, kk + 2 * k, id_s, 1u);
                 mma_commit_pair(&k_empty[ks]);
               }
               __syncwarp();
@@ -491,6 +495,7 @@ cudaError_t launch_latent_attn_pair(const LatentAttnArgs &la, void *scratch, int
   // rows over 4096 20.2 / 20.0 / 21.1, 4 x 2 rows over 2048 22.5 / 22.5 / 22.6
   a.min_tiles = 1;
   sp.item_cost = 2;
+  sp.rope = la.Dr;
   char *base = static_cast<char *>(scratch);
   bind_region(a, base, n, 2 * kRows);
   paged_tc_bind_plan(sp, base + region_bytes(kPagedMaxCtas / 2, 2 * kRows, kDV));

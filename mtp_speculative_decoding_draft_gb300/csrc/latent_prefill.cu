@@ -5,8 +5,8 @@
 // array of whole keys is ever written.  The frame is paged_attn_tc.cu's: a CTA holds
 // two groups of 128 query rows of one head that take turns on the tensor core, the
 // items are dealt out by its plan,
-//   S_g = Q_g K_i^T     tcgen05.mma over Dn + 64 elements (a shared part of 32 is
-//                       filled up with zeros by the copies)
+//   S_g = Q_g K_i^T     tcgen05.mma over Dn + Dr elements (a shared part of 32 lies in
+//                       a block of 64, whose other half is not multiplied)
 //   P_g = 2^(S_g - m)   one thread a row, P back over S as bf16
 //   O_g += P_g V_i      tcgen05.mma, P from tensor memory, V row-major (MN-major)
 // Queries of 192 elements take 96 KB of shared memory, which leaves 128 for 80 KB a tile.
@@ -251,8 +251,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
               }
               if (leader) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 2; ++k)
                   mma_bf16(tm + kS + 128 * g, q + (uint64_t)(((KB - 1) * kBlk + k * 32) >> 4), rr + 2 * k, id_s, k > 0);
+                if (sp.rope > 32)  // (2048 rows over 10240, 16 heads of 128 + 32: 136 us with the zeros, 133 without)
+#pragma unroll
+                  for (int k = 2; k < 4; ++k)
+                    mma_bf16(tm + kS + 128 * g, q + (uint64_t)(((KB - 1) * kBlk + k * 32) >> 4), rr + 2 * k, id_s, 1u);
               }
               if (g == 0) {
                 await(&k_full[odd], (n >> 1) & 1u);
@@ -303,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
       const int all_hi = min(w.s.ctx + tg0 + 1, p.cap);
       const int all_lo = p.window > 0 ? max(0, w.s.ctx + tg1 - 1 - p.window + 1) : 0;
       float m = -INFINITY, l = 0.f;
-            for (int i = w.i0; i < w.i1; ++i) {
+      for (int i = w.i0; i < w.i1; ++i) {
         const int k0 = w.r.tile(i) * kTK;
         const bool whole = k0 + kTK <= all_hi && (k0 >= all_lo || k0 + kTK <= min(p.sinks, all_hi));
         if (ok) ok = mbar_wait(&s_full[g], (uint32_t)(ns++) & 1u, p.status);
@@ -456,6 +460,7 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &lp, void *scratch, in
   a.tpb = kTpb;
   a.min_tiles = 2;
   pp.tc.item_cost = kItemCost;
+  pp.tc.rope = lp.Dr;
   pp.Dn = lp.Dn;
   pp.w = lp.Dn + lp.Dv;
   pp.n_keys = lp.n_keys;

@@ -37,6 +37,7 @@ struct PagedTcParams {
   int n_items;        // places of the line
   int shares;         // CTAs (or pairs) of the call
   int small;          // no plan was made: plan_share
+  int rope;           // (latent attention) elements of the shared key part, 32 or 64
 };
 
 // A share's first items, copied into shared memory: a step to the next item costs two
