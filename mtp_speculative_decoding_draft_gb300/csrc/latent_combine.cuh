@@ -186,7 +186,8 @@ __device__ __forceinline__ uint16_t *joined_row(const PagedArgs &p, const Combin
   return static_cast<uint16_t *>(p.out) + (long long)row * p.ldo + (hq * PARTS + part) * DH;
 }
 
-// Items cut in two at most: a warp joins 32 rows x 8 elements, a lane a row.
+// Items cut into a few states: a warp joins 32 rows x 8 elements, a lane a row, two states
+// requested together (four: 23.4 us against 24.5 where items lie in four, 55.7 against 53.1 where in two).
 template <int DH, int ROWS, int PARTS>
 __global__ void __launch_bounds__(kLatentCombineThreads, 4)
     latent_combine_kernel(const __grid_constant__ PagedArgs p, int shares) {
@@ -273,8 +274,10 @@ cudaError_t launch_latent_combine(const PagedTcParams &sp, int shares, int sms, 
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   note_launch();
-  // (of the places of the line, kPagedMaxCtas are for gaps)
-  return 2 * (sp.n_items - kPagedMaxCtas) < shares
+  // More than eight shares an item: by blocks.  us (by blocks / by warps), R 512: one row of 16 heads,
+  // 4 of 4096 keys 14.8 / 20.4, 8 of 2048 14.5 / 16.6, 16 of 2048 19.6 / 18.7; one of 128 heads, 16 of
+  // 2048 35.6 / 28.0.  (Of the places of the line, kPagedMaxCtas are for gaps.)
+  return 8 * (sp.n_items - kPagedMaxCtas) < shares
              ? cudaLaunchKernelEx(&cfg, latent_combine_many_kernel<DH, ROWS, PARTS>, sp.a, shares)
              : cudaLaunchKernelEx(&cfg, latent_combine_kernel<DH, ROWS, PARTS>, sp.a, shares);
 }
