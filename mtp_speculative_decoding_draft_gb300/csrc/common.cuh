@@ -175,18 +175,6 @@ __device__ __forceinline__ void mbar_arrive_remote(uint64_t *local_bar, uint32_t
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(raddr) : "memory");
 }
 
-// Arrivals on a barrier of the cluster (its cluster address) that publish nothing this
-// thread wrote: a release at cluster scope would first wait for the thread's stores, about
-// 0.8 us each time.  The first adds bytes to wait for.
-__device__ __forceinline__ void expect_tx_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 // ---------------------------------------------------------------- TMA bulk copy
 
 // 1-D bulk copy global -> this CTA's shared memory, completing on `bar`.

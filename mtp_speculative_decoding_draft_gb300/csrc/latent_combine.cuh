@@ -9,7 +9,7 @@
 
 #include "paged_combine.cuh"
 #include "paged_tc.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_ops.cuh"
 
 namespace mtp {
 

@@ -25,7 +25,7 @@
 #include "internal.h"
 #include "latent.cuh"
 #include "paged_tc.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_ops.cuh"
 
 namespace mtp {
 

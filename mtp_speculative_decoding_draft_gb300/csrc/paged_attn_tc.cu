@@ -32,7 +32,7 @@
 #include "internal.h"
 #include "paged.cuh"
 #include "paged_tc.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_ops.cuh"
 
 // The order of the line (paged.cuh): with equal contiguous shares each CTA walks
 // the blocks of a few K/V heads one after another, and all heads of the batch are
