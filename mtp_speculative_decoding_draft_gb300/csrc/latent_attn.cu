@@ -16,6 +16,10 @@
 // product of 64 rows runs at half the rate of one of 128, so the zeros cost nothing.)
 // S of 64 rows arrives in the lanes l < 16 of each 32.
 //
+// Bound by the cache's bytes: 32 x 1 row of 16 heads over 16384-32749 keys (R 512) take 171 us, 907 MB
+// at 78% of the copy rate; one row of 16 heads over 512 keys takes 10 us, one over 4096 13 us,
+// in latencies (its plan 2, first scores 5, states and joining 4).
+//
 // S_{i+1} is issued ahead of O += P_i V_i, so that the softmax of one tile runs under
 // the products of another.  Tensor memory (512 columns): O 256 | S_0 S_1 128 | P_0 P_1 128.
 // Warps 0-3 are the softmax, warp 4 brings pages, warp 5 issues the products, warp 6 brings
@@ -436,8 +440,14 @@ cudaError_t launch(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl) 
 
 }  // namespace
 
-// More packed rows than two blocks hold, at the mean number of rows a sequence, go to
-// pairs of CTAs.
+// More packed rows than two blocks of 64 hold, at the mean number of rows a sequence, go to
+// pairs of CTAs.  us (64-row blocks / pairs), R 512:
+//             4 of 4096 keys   16 of 2048    48 of 1024    64 of 4096
+//   1 x 128   21.4 / 24.6      28.0 / 30.2   43.5 / 47.9   130 / 161
+//   4 x 40    25.8 / 24.6      35.3 / 32.2   55.3 / 49.1   181 / 164
+//   4 x 128   39.9 / 30.7      75.9 / 57.3   109 / 87      440 / 311
+// R 256, 1 x 128: 15.7 / 16.3, 19.0 / 21.6, 26.1 / 26.5, 65 / 60; 4 x 40: 17.5 / 17.2, 22.6 / 21.4,
+// 32.6 / 30.1, 88 / 61.  (One sequence: within 2 us.)
 static bool wants_pair(int B, int n_rows, int H) { return (long long)((n_rows + B - 1) / B) * H > 128; }
 
 bool latent_attn_items_ok(int B, int n_rows, int H) {
