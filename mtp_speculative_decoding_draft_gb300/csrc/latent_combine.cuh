@@ -265,7 +265,13 @@ template <int DH, int ROWS, int PARTS>
 cudaError_t launch_latent_combine(const PagedTcParams &sp, int shares, int sms, cudaStream_t s, bool pdl) {
   static_assert(kPagedMaxCtas <= kMaxDescs, "a description a share");
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(4 * sms);
+  // More than eight shares an item: by blocks.  us (by blocks / by warps), R 512: one row of 16 heads,
+  // 4 of 4096 keys 14.8 / 20.4, 8 of 2048 14.5 / 16.6, 16 of 2048 19.6 / 18.7; one of 128 heads, 16 of
+  // 2048 35.6 / 28.0.  (Of the places of the line, kPagedMaxCtas are for gaps.)
+  const bool many = 8 * (sp.n_items - kPagedMaxCtas) < shares;
+  // what is resident at once: with four blocks an SM of the first kind a call of two keys took 10.0
+  // us, with two 9.1; with two of the second kind 16 x 4 rows of 128 heads took 60.7, with four 55.2
+  cfg.gridDim = dim3((many ? 2 : 4) * sms);
   cfg.blockDim = dim3(kLatentCombineThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -274,12 +280,8 @@ cudaError_t launch_latent_combine(const PagedTcParams &sp, int shares, int sms, 
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   note_launch();
-  // More than eight shares an item: by blocks.  us (by blocks / by warps), R 512: one row of 16 heads,
-  // 4 of 4096 keys 14.8 / 20.4, 8 of 2048 14.5 / 16.6, 16 of 2048 19.6 / 18.7; one of 128 heads, 16 of
-  // 2048 35.6 / 28.0.  (Of the places of the line, kPagedMaxCtas are for gaps.)
-  return 8 * (sp.n_items - kPagedMaxCtas) < shares
-             ? cudaLaunchKernelEx(&cfg, latent_combine_many_kernel<DH, ROWS, PARTS>, sp.a, shares)
-             : cudaLaunchKernelEx(&cfg, latent_combine_kernel<DH, ROWS, PARTS>, sp.a, shares);
+  return many ? cudaLaunchKernelEx(&cfg, latent_combine_many_kernel<DH, ROWS, PARTS>, sp.a, shares)
+              : cudaLaunchKernelEx(&cfg, latent_combine_kernel<DH, ROWS, PARTS>, sp.a, shares);
 }
 
 }  // namespace mtp
