@@ -579,8 +579,9 @@ int mtp_latent_heads(int n_rows, int H, int K, int N, const void *x, int64_t ldx
  *   N         elements of a kv head (Dn + Dv): a multiple of 8, at most 4096
  *   w         bf16 [H, N, R], rows ldw and heads hsw elements apart
  *   kv        bf16 rows of H * N, ldkv elements apart;  k_rope  rows of Dr, ldkr apart
- * Starts out of order or outside the rows set MTP_STATUS_BAD_ROWS, positions past the
- * cache MTP_STATUS_BAD_CTX; their rows are not written.  An entry of the page table
+ * Starts outside the rows set MTP_STATUS_BAD_ROWS, positions past the cache
+ * MTP_STATUS_BAD_CTX; their rows are not written.  Starts that decrease set
+ * MTP_STATUS_BAD_ROWS, and nothing of the call is written.  An entry of the page table
  * outside the pool sets MTP_STATUS_BAD_PAGE, and page 0 is read in its place.
  */
 int mtp_latent_expand(const MtpLatentCache *cache, int B, int H, int N, int n_keys, const int32_t *key_start,

@@ -69,10 +69,12 @@ struct TileTable {
   RowTile near[kNear];
 };
 
-// Rows of sequence b that are expanded; flags what is out of range.
-__device__ __forceinline__ int seq_rows(const LatentHeadsArgs &p, int b, int *start, bool flag) {
+// Rows of sequence b that are expanded; flags what is out of range, and sets *back if the
+// rows end before they start.
+__device__ __forceinline__ int seq_rows(const LatentHeadsArgs &p, int b, int *start, bool flag, bool *back = nullptr) {
   const int s = __ldcg(&p.key_start[b]), e = __ldcg(&p.key_start[b + 1]);
   *start = s;
+  if (back) *back |= e < s;
   if (s < 0 || e < s || e > p.n_rows) {
     if (flag) set_status(p.status, kStatusBadRows);
     return 0;
@@ -181,10 +183,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
   if (p.pages) {
     const int per = (p.B + kThreads - 1) / kThreads;
     int mine = 0;
+    bool back = false;
     for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
       int s;
-      mine += (seq_rows(p, b, &s, blockIdx.x == 0) + 127) / 128;
+      mine += (seq_rows(p, b, &s, blockIdx.x == 0, &back) + 127) / 128;
     }
+    // Starts that decrease may count rows twice: two CTAs could write one row, and the tiles'
+    // number would have no bound (n_keys / 128 + B otherwise).  Nothing of such a call is expanded.
+    const bool none = __syncthreads_or(back);
+    if (none) mine = 0;
     int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -197,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
     for (int v = 0; v < warp; ++v) before += table.sums[v];
     table.before[tid] = before;
     if (tid == kThreads - 1) table.before[kThreads] = before + mine;
-    for (int b = tid * per; b < min(p.B, (tid + 1) * per) && before < kNear; ++b) {
+    for (int b = tid * per; !none && b < min(p.B, (tid + 1) * per) && before < kNear; ++b) {
       int s;
       const int n = seq_rows(p, b, &s, false);
       for (int j = 0; j < n && before < kNear; j += 128) table.near[before++] = {b, j, s + j, min(128, n - j)};
