@@ -281,11 +281,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (i > 0) {
             const int j = it - (i < nt ? 2 : 1);  // the tile before
             if (i == 1) {
-              await(o_empty, oph);
+              if (ok) ok = mbar_wait_cluster(o_empty, oph, p.status);
               oph ^= 1u;
             }
-            await(&p_full[j & 1], (uint32_t)(j >> 1) & 1u);
-            // (cluster scope: zeros that the second CTA wrote)
+            // (cluster scope: O's reads, P, a rescaled O and zeros of the second CTA)
+            if (ok) ok = mbar_wait_cluster(&p_full[j & 1], (uint32_t)(j >> 1) & 1u, p.status);
             if (ok) ok = mbar_wait_cluster(&v_full[vs], vph, p.status);
             tc_fence_after();
             if (leader) {
@@ -385,6 +385,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
+        // P and a rescaled O are handed over, all in tensor memory.  (With a release: 64 x 4 rows of
+        // 128 heads 331 -> 339 us, 12 ragged chunks of 40 heads, R 256, 345 -> 425; passed on by an idle
+        // warp of the second CTA, without stores to wait for, 339 and 393.)
         if (lane == 0) mbar_arrive_cluster_relaxed(dsmem_addr(&p_full[it & 1], 0));
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
           ++nkept;
         }
         const bool last = KEEP && (u + 1 == u1 || row_tile(u + 1) != at);
-        if (n >= 2) ok = mbar_wait(&tfree[buf], ((n >> 1) - 1u) & 1u, p.status);
+        if (n >= 2) ok = mbar_wait_cluster(&tfree[buf], ((n >> 1) - 1u) & 1u, p.status);
         ok = __all_sync(kFull, ok);
         if (!ok) break;
         for (int kb = 0; kb < hp.kbs && ok; ++kb, ++i) {

@@ -171,8 +171,17 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
 // offsets, and its tensor memory the accumulator of its rows.
 
 // Arrivals on a barrier of the cluster (its cluster address) that publish nothing this
-// thread wrote: a release at cluster scope would first wait for the thread's stores, about
-// 0.8 us each time.  The first adds bytes to wait for.
+// thread wrote to shared or global memory: a release at cluster scope would first wait for
+// the thread's stores, about 0.8 us each time.  The first adds bytes to wait for.
+//
+// The second may hand over tensor memory, whose reads and writes no release orders, but the
+// fences around the barrier do, a relaxed one too (the PTX manual's pattern for instructions
+// that are not pipelined, in different threads):
+//   tcgen05.ld or st, tcgen05.wait, tcgen05.fence::before_thread_sync, (the warp's barrier,)
+//   this arrival | a wait at cluster scope, tcgen05.fence::after_thread_sync, the product
+// The wait has to be mbar_wait_cluster: one at CTA scope, which mbar_wait is, does not
+// synchronise with an arrival from another CTA.  Shared memory written for the other CTA's
+// products takes mbar_arrive_remote.
 __device__ __forceinline__ void expect_tx_cluster(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
