@@ -596,7 +596,8 @@ int mtp_latent_expand(const MtpLatentCache *cache, int B, int H, int N, int n_ke
  *   scale  softmax scale (> 0), usually 1 / sqrt(Dn + Dr)
  *   out    bf16 rows of Hq * R, ldo apart: sum_j p_j c_j; must not overlap q
  *   lse    [n_rows, Hq] fp32, or NULL: ln sum_j exp(score)
- *   ws     mtp_latent_attn_workspace_size() bytes, 256-byte aligned
+ *   ws     mtp_latent_attn_workspace_size() bytes, 256-byte aligned: enough, too, for every
+ *          call of no more sequences and no more rows
  * Scores, statistics and sums are fp32; the softmax weights are rounded to bf16 for
  * their product with the latents.  What a row without keys gives, NaN and infinities, and
  * what unseen positions may hold are as for mtp_paged_attn.

@@ -690,6 +690,7 @@ def mtp_latent_expand(cache, key_start, w, kv, k_rope, ws, stream=None):
 
 
 def latent_attn_workspace_size(B, n_rows, Hq, R):
+    """Bytes for mtp_latent_attn of at most B sequences and n_rows rows."""
     return int(_lib().mtp_latent_attn_workspace_size(int(B), int(n_rows), int(Hq), int(R)))
 
 
@@ -710,6 +711,7 @@ def mtp_latent_attn(cache, row_start, ctx_len, q, out, lse, ws, scale, window=0,
 
 
 def latent_prefill_workspace_size(B, n_rows, H, Dv):
+    """Bytes for mtp_latent_prefill of at most B sequences and n_rows rows."""
     return int(_lib().mtp_latent_prefill_workspace_size(int(B), int(n_rows), int(H), int(Dv)))
 
 

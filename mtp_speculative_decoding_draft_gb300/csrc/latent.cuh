@@ -68,7 +68,7 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &lp, void *scratch, in
 
 // The same on pairs of CTAs (latent_attn_pair.cu).
 bool latent_pair_items_ok(int B, int n_rows, int H);
-size_t latent_pair_scratch_bytes(int B, int n_rows, int H);
+size_t latent_pair_scratch_bytes(int B, int n_rows, int H, int R);
 cudaError_t launch_latent_attn_pair(const LatentAttnArgs &la, void *scratch, int sms, cudaStream_t s, bool pdl);
 cudaError_t latent_pair_set_attributes();
 

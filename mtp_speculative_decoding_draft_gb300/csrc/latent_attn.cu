@@ -457,11 +457,19 @@ bool latent_attn_items_ok(int B, int n_rows, int H) {
   return paged_tc_items_ok(B, n_rows, kRows / G, hb);
 }
 
+// Enough for every call of at most B sequences and n_rows rows, whichever kernel and blocks its
+// mean takes: a program sizes its workspace once, and sequences finish.  Items: of N rows in B
+// sequences, n = ceil(N / B) at the mean, block_shape takes runs r of t tokens a block with
+// r ceil(n / t) <= r0 ceil(n / t0), r0 and t0 its first choice.  So
+//   r (N / t + B) <= 2 B r ceil(n / t) <= 2 r0 B ceil(n / t0) <= 2 r0 (N / t0 + B).
 size_t latent_attn_scratch_bytes(int B, int n_rows, int H, int R) {
-  if (wants_pair(B, n_rows, H)) return latent_pair_scratch_bytes(B, n_rows, H);
-  int G, hb;
-  block_shape(B, n_rows, H, &G, &hb);
-  return region_bytes(kPagedMaxCtas, kRows, R) + paged_tc_plan_bytes(B, n_rows, kRows / G, hb);
+  const int r0 = (H + kRows - 1) / kRows, G = (H + r0 - 1) / r0;
+  const long long most = (long long)B * (128 / H);  // rows that stay with this kernel
+  const size_t here = region_bytes(kPagedMaxCtas, kRows, R) +
+                      paged_tc_plan_bytes(B, most < n_rows ? (int)most : n_rows, kRows / G, 2 * r0);
+  if (!wants_pair(1, n_rows, H)) return here;  // (no call of fewer rows does)
+  const size_t pairs = latent_pair_scratch_bytes(B, n_rows, H, R);
+  return here > pairs ? here : pairs;
 }
 
 cudaError_t launch_latent_attn(const LatentAttnArgs &la, void *scratch, int sms, cudaStream_t s, bool pdl) {
