@@ -1135,6 +1135,9 @@ int check_latent(const MtpLatentCache *c) {
 
 constexpr int kMaxLatentHeads = 128;
 
+// The plans count items in 31 bits, which these limits keep them below: an absorbed call
+// has at most 4 (n_rows / 2 + B) < 1.1 x 2^30 (latent_attn_scratch_bytes), an expanded one
+// 128 (n_rows / 256 + B) = 1.5 x 2^28.
 int check_latent_rows(int B, int H, int n_rows, const int32_t *row_start, const int32_t *ctx_len) {
   if (B < 1 || n_rows < 1 || H < 1) return MTP_ERR_INVALID_ARG;
   if (B > (1 << 20) || n_rows > (1 << 29) || H > kMaxLatentHeads) return MTP_ERR_UNSUPPORTED_SHAPE;
@@ -1261,7 +1264,7 @@ int mtp_latent_expand(const MtpLatentCache *cache, int B, int H, int N, int n_ke
 
 size_t mtp_latent_attn_workspace_size(int B, int n_rows, int Hq, int R) {
   if (B < 1 || n_rows < 1 || Hq < 1 || Hq > kMaxLatentHeads || (R != 256 && R != 512)) return 0;
-  if (B > (1 << 20) || n_rows > (1 << 29) || !latent_attn_items_ok(B, n_rows, Hq)) return 0;
+  if (B > (1 << 20) || n_rows > (1 << 29)) return 0;
   return kAlign + latent_attn_scratch_bytes(B, n_rows, Hq, R);
 }
 
@@ -1274,7 +1277,6 @@ int mtp_latent_attn(const MtpLatentCache *cache, int B, int Hq, int n_rows, cons
   if (rc) return rc;
   if (!stride_ok(ldq, (long long)Hq * (cache->R + cache->Dr)) || !stride_ok(ldo, (long long)Hq * cache->R))
     return MTP_ERR_INVALID_ARG;
-  if (!latent_attn_items_ok(B, n_rows, Hq)) return MTP_ERR_UNSUPPORTED_SHAPE;
   if (!workspace_ok(ws)) return MTP_ERR_INVALID_ARG;
   if (ws_bytes < mtp_latent_attn_workspace_size(B, n_rows, Hq, cache->R)) return MTP_ERR_WORKSPACE;
   if (!tc_available()) return MTP_ERR_CUDA;
@@ -1303,7 +1305,7 @@ int mtp_latent_attn(const MtpLatentCache *cache, int B, int Hq, int n_rows, cons
 
 size_t mtp_latent_prefill_workspace_size(int B, int n_rows, int H, int Dv) {
   if (B < 1 || n_rows < 1 || H < 1 || H > kMaxLatentHeads || (Dv != 64 && Dv != 128)) return 0;
-  if (B > (1 << 20) || n_rows > (1 << 29) || !latent_prefill_items_ok(B, n_rows, H)) return 0;
+  if (B > (1 << 20) || n_rows > (1 << 29)) return 0;
   return kAlign + latent_prefill_scratch_bytes(B, n_rows, H, Dv);
 }
 
@@ -1321,7 +1323,6 @@ int mtp_latent_prefill(int B, int H, int Dn, int Dr, int Dv, int n_rows, int n_k
   if (!stride_ok(ldq, (long long)H * (Dn + Dr)) || !stride_ok(ldkv, (long long)H * (Dn + Dv)) || !stride_ok(ldkr, Dr) ||
       !stride_ok(ldo, (long long)H * Dv))
     return MTP_ERR_INVALID_ARG;
-  if (!latent_prefill_items_ok(B, n_rows, H)) return MTP_ERR_UNSUPPORTED_SHAPE;
   if (!workspace_ok(ws)) return MTP_ERR_INVALID_ARG;
   if (ws_bytes < mtp_latent_prefill_workspace_size(B, n_rows, H, Dv)) return MTP_ERR_WORKSPACE;
   if (!tc_available()) return MTP_ERR_CUDA;

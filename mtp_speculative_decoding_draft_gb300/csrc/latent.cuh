@@ -50,7 +50,6 @@ struct LatentAttnArgs {
   int Dr;
   const uint16_t *pages;
 };
-bool latent_attn_items_ok(int B, int n_rows, int H);
 size_t latent_attn_scratch_bytes(int B, int n_rows, int H, int R);
 cudaError_t launch_latent_attn(const LatentAttnArgs &la, void *scratch, int sms, cudaStream_t s, bool pdl);
 
@@ -62,12 +61,10 @@ struct LatentPrefillArgs {
   const uint16_t *kv, *k_rope;
   long long ldkv, ldkr;
 };
-bool latent_prefill_items_ok(int B, int n_rows, int H);
 size_t latent_prefill_scratch_bytes(int B, int n_rows, int H, int Dv);
 cudaError_t launch_latent_prefill(const LatentPrefillArgs &lp, void *scratch, int sms, cudaStream_t s, bool pdl);
 
 // The same on pairs of CTAs (latent_attn_pair.cu).
-bool latent_pair_items_ok(int B, int n_rows, int H);
 size_t latent_pair_scratch_bytes(int B, int n_rows, int H, int R);
 cudaError_t launch_latent_attn_pair(const LatentAttnArgs &la, void *scratch, int sms, cudaStream_t s, bool pdl);
 cudaError_t latent_pair_set_attributes();

@@ -450,13 +450,6 @@ cudaError_t launch(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl) 
 // 32.6 / 30.1, 88 / 61.  (One sequence: within 2 us.)
 static bool wants_pair(int B, int n_rows, int H) { return (long long)((n_rows + B - 1) / B) * H > 128; }
 
-bool latent_attn_items_ok(int B, int n_rows, int H) {
-  if (wants_pair(B, n_rows, H)) return latent_pair_items_ok(B, n_rows, H);
-  int G, hb;
-  block_shape(B, n_rows, H, &G, &hb);
-  return paged_tc_items_ok(B, n_rows, kRows / G, hb);
-}
-
 // Enough for every call of at most B sequences and n_rows rows, whichever kernel and blocks its
 // mean takes: a program sizes its workspace once, and sequences finish.  Items: of N rows in B
 // sequences, n = ceil(N / B) at the mean, block_shape takes runs r of t tokens a block with

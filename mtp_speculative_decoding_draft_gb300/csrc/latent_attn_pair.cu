@@ -478,12 +478,6 @@ cudaError_t launch(const PagedTcParams &sp, int pairs, cudaStream_t s, bool pdl)
 
 }  // namespace
 
-bool latent_pair_items_ok(int B, int n_rows, int H) {
-  int G, hb;
-  block_shape(B, n_rows, H, &G, &hb);
-  return paged_tc_items_ok(B, n_rows, 2 * (kRows / G), 2 * hb);
-}
-
 // The first choice of block_shape is one run (latent_attn_scratch_bytes), of R / kDV items.
 size_t latent_pair_scratch_bytes(int B, int n_rows, int H, int R) {
   return region_bytes(kPagedMaxCtas / 2, 2 * kRows, kDV) + paged_tc_plan_bytes(B, n_rows, 2 * (kRows / H), 2 * (R / kDV));

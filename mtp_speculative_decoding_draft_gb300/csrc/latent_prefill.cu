@@ -454,8 +454,6 @@ cudaError_t set_smem() {
 
 }  // namespace
 
-bool latent_prefill_items_ok(int B, int n_rows, int H) { return paged_tc_items_ok(B, n_rows, kTpb, H); }
-
 size_t latent_prefill_scratch_bytes(int B, int n_rows, int H, int Dv) {
   return region_bytes(kPagedMaxCtas, kPagedTcRows, Dv) + paged_tc_plan_bytes(B, n_rows, kTpb, H);
 }
