@@ -541,7 +541,8 @@ typedef struct {
  *   kv      bf16 rows of R + Dr (one projection's output), ldkv elements apart
  *   gain    [R] bf16: c = x / sqrt(mean(x^2) + eps) * gain; NULL: c = x
  *   q       bf16: head h of a row's rotary part (Dr elements) is hsq * h elements
- *           behind the row's first, rows ldq apart; q and q_out both NULL: keys only
+ *           behind the row's first, rows ldq apart, heads within rows or rows within
+ *           heads without overlap; q and q_out both NULL: keys only
  *   q_out   alike, ldqo and hsqo apart; q itself (same strides) to rotate in place;
  *           no other overlap.  The other elements of its rows are left as they are.
  * Pointers are aligned to 16 bytes, strides are multiples of 8.  Products and sums are

@@ -1148,6 +1148,12 @@ int check_latent_rows(int B, int H, int n_rows, const int32_t *row_start, const 
 // A stride in elements: whole 16-byte vectors, below the 2^40 bytes of a tensor map.
 bool stride_ok(int64_t ld, long long width) { return ld >= width && ld % 8 == 0 && ld < (1ll << 38); }
 
+// n rows of H heads of `width` elements, heads within rows or rows within heads: no two
+// overlap.
+bool heads_apart(int n, int H, int64_t ld, int64_t hs, int width) {
+  return ld >= (__int128)(H - 1) * hs + width || hs >= (__int128)(n - 1) * ld + width;
+}
+
 bool workspace_ok(const void *ws) { return aligned16(ws) && (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) == 0; }
 
 int check_attention(float scale, int window, int sinks, const void *q, const void *out, const float *lse) {
@@ -1173,8 +1179,10 @@ int mtp_latent_append(const MtpLatentCache *cache, const MtpRope *rope, int B, i
   if ((q == nullptr) != (q_out == nullptr)) return MTP_ERR_INVALID_ARG;
   if (q) {
     if (!aligned16(q) || !aligned16(q_out)) return MTP_ERR_INVALID_ARG;
-    if (!stride_ok(hsq, cache->Dr) || !stride_ok(ldq, (Hq - 1) * hsq + cache->Dr)) return MTP_ERR_INVALID_ARG;
-    if (!stride_ok(hsqo, cache->Dr) || !stride_ok(ldqo, (Hq - 1) * hsqo + cache->Dr)) return MTP_ERR_INVALID_ARG;
+    if (!stride_ok(ldq, cache->Dr) || !stride_ok(hsq, cache->Dr)) return MTP_ERR_INVALID_ARG;
+    if (!stride_ok(ldqo, cache->Dr) || !stride_ok(hsqo, cache->Dr)) return MTP_ERR_INVALID_ARG;
+    if (!heads_apart(n_rows, Hq, ldq, hsq, cache->Dr) || !heads_apart(n_rows, Hq, ldqo, hsqo, cache->Dr))
+      return MTP_ERR_INVALID_ARG;
     if (q == q_out && (ldq != ldqo || hsq != hsqo)) return MTP_ERR_INVALID_ARG;
   }
   if (!rope_ok(rope, cache->Dr, &rc)) return rc;
@@ -1223,8 +1231,7 @@ int mtp_latent_heads(int n_rows, int H, int K, int N, const void *x, int64_t ldx
   if (!aligned16(x) || !aligned16(w) || !aligned16(y) || x == y || w == y) return MTP_ERR_INVALID_ARG;
   if (!stride_ok(ldx, K) || !stride_ok(hsx, K) || !stride_ok(ldy, N) || !stride_ok(hsy, N)) return MTP_ERR_INVALID_ARG;
   if (!stride_ok(ldw, transposed ? N : K) || !stride_ok(hsw, 8)) return MTP_ERR_INVALID_ARG;
-  // y's rows are apart, heads within rows or rows within heads
-  if (ldy < (__int128)(H - 1) * hsy + N && hsy < (__int128)(n_rows - 1) * ldy + N) return MTP_ERR_INVALID_ARG;
+  if (!heads_apart(n_rows, H, ldy, hsy, N)) return MTP_ERR_INVALID_ARG;
   if (!workspace_ok(ws)) return MTP_ERR_INVALID_ARG;
   if (ws_bytes < kAlign) return MTP_ERR_WORKSPACE;
   LatentHeadsArgs a{};
