@@ -1190,6 +1190,8 @@ int mtp_latent_append(const MtpLatentCache *cache, const MtpRope *rope, int B, i
   // the launch counts its warps in 32 bits
   if ((long long)n_rows * ((q ? Hq : 0) * cache->Dr / 256 + 3) >= (1ll << 31)) return MTP_ERR_UNSUPPORTED_SHAPE;
   if (ws_bytes < kAlign) return MTP_ERR_WORKSPACE;
+  DevInfo di;
+  if ((rc = device_info(&di))) return rc;
   LatentAppendArgs a{};
   a.B = B; a.Hq = q ? Hq : 0; a.R = cache->R; a.Dr = cache->Dr;
   a.page = cache->page; a.page_shift = page_shift(cache->page); a.n_pages = cache->n_pages;
@@ -1207,7 +1209,7 @@ int mtp_latent_append(const MtpLatentCache *cache, const MtpRope *rope, int B, i
   a.status = static_cast<int *>(ws);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   NvtxRange r("mtp latent append");
-  cudaError_t e = launch_latent_append(a, s, use_pdl());
+  cudaError_t e = launch_latent_append(a, di.sms, s, use_pdl());
   if (e == cudaSuccess) e = cudaGetLastError();
   return cuda_rc(e);
 }

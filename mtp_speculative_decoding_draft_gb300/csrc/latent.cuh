@@ -25,7 +25,7 @@ struct LatentAppendArgs {
   long long ldkv, ldq, hsq, ldqo, hsqo;
   int *status;
 };
-cudaError_t launch_latent_append(const LatentAppendArgs &a, cudaStream_t s, bool pdl);
+cudaError_t launch_latent_append(const LatentAppendArgs &a, int sms, cudaStream_t s, bool pdl);
 
 // y[n, h, :] = W[h] x[n, h, :], or, with pages, of the rows of a cache's sequences
 // (x shared by the heads).

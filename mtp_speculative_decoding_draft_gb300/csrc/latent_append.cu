@@ -263,11 +263,16 @@ cudaError_t launch_append(const LatentAppendArgs &a, int items, cudaStream_t s, 
 
 }  // namespace
 
-cudaError_t launch_latent_append(const LatentAppendArgs &a, cudaStream_t s, bool pdl) {
+cudaError_t launch_latent_append(const LatentAppendArgs &a, int sms, cudaStream_t s, bool pdl) {
   // 16-byte accesses need the pairs' halves in whole vectors
   const bool wide = a.rot % 16 == 0;
   const int items = ((a.q ? a.Hq : 0) + 1) * a.Dr / (wide ? 16 : 8);
-  if ((long long)a.n_rows * items < 152ll * 256)
+  // One item a lane until each SM has a block's worth of items (38912 on 152), two from there on.
+  // us (one / two, Dr 64): 4 rows of 128 heads 2.4 / 2.7, 256 of 16 3.3 / 3.4, 512 of 16 (34816 items)
+  // 3.1 / 3.1, 256 of 40 (41984) 4.6 / 3.8 and 3.0 / 2.9 (64 sequences, one), 256 of 128 10.5 / 6.7,
+  // 1024 of 16 5.3 / 4.9, 8190 of 16 21.7 / 18.0, of 40 37.0 / 25.2, of 128 93.0 / 62.5;
+  // 1024 of 40 with 24 elements that rotate 9.0 / 6.9.
+  if ((long long)a.n_rows * items < 256ll * sms)
     return wide ? launch_append<8, 1>(a, items, s, pdl) : launch_append<4, 1>(a, items, s, pdl);
   return wide ? launch_append<8, 2>(a, items, s, pdl) : launch_append<4, 2>(a, items, s, pdl);
 }

@@ -54,7 +54,7 @@ struct Lay {
 
 struct PrefillParams {
   PagedTcParams tc;  // mk: the keys' and values' rows; mv: the shared key parts; mq: the queries
-  int Dn, w;         // plain elements of a key; elements of a head in a row
+  int w;             // elements of a head in a row of keys and values
   int n_keys;
   const int *key_start;
 };
@@ -467,7 +467,6 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs &lp, void *scratch, in
   a.min_tiles = 2;  // of a share (one: 16 rows over 3000 19.1 us and 19.2, 256 rows of 16 heads 15.1 and 14.5)
   pp.tc.item_cost = kItemCost;
   pp.tc.rope = lp.Dr;
-  pp.Dn = lp.Dn;
   pp.w = lp.Dn + lp.Dv;
   pp.n_keys = lp.n_keys;
   pp.key_start = lp.key_start;
