@@ -600,8 +600,10 @@ int mtp_latent_expand(const MtpLatentCache *cache, int B, int H, int N, int n_ke
  *   ws     mtp_latent_attn_workspace_size() bytes, 256-byte aligned: enough, too, for every
  *          call of no more sequences and no more rows
  * Scores, statistics and sums are fp32; the softmax weights are rounded to bf16 for
- * their product with the latents.  What a row without keys gives, NaN and infinities, and
- * what unseen positions may hold are as for mtp_paged_attn.
+ * their product with the latents, however few the rows.  What a row without keys gives, NaN
+ * and infinities, and what unseen positions may hold are as for mtp_paged_attn.
+ * n_rows / B, rows past row_start[B] included, chooses between kernels (the same function):
+ * a decoding batch is fastest in arrays of the rows that it has.
  */
 size_t mtp_latent_attn_workspace_size(int B, int n_rows, int Hq, int R);
 int mtp_latent_attn(const MtpLatentCache *cache, int B, int Hq, int n_rows, const int32_t *row_start,

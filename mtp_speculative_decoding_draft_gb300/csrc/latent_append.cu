@@ -9,8 +9,9 @@
 //   (x0, x1) -> scale (x0 cos - x1 sin, x1 cos + x0 sin)
 //
 // Bound by the bytes of the queries (each row read and written once): 8190 rows of 40 heads
-// take 21.5 us, 102 MB at 70% of the copy rate; the rest is each warp's chain of position, page
-// entry and store.  Four rows of 128 heads: 2.5 us, a launch.
+// take 25 us, 102 MB at 61% of the copy rate (in graphs of 20, where a part of them stays in L2,
+// 21.9); the rest is each warp's chain of position, page entry and store.  Four rows of 128
+// heads in such a graph: 2.6 us, a launch.
 // A warp takes one unit: the first unit of a row is its latent, held in registers between
 // the sum of squares and the product with the gain; the others are runs of 32 x U items (an
 // item: the two vectors of VEC elements that rotate together) of the heads, the key counting

@@ -16,9 +16,15 @@
 // product of 64 rows runs at half the rate of one of 128, so the zeros cost nothing.)
 // S of 64 rows arrives in the lanes l < 16 of each 32.
 //
-// Bound by the cache's bytes: 32 x 1 row of 16 heads over 16384-32749 keys (R 512) take 171 us, 907 MB
-// at 78% of the copy rate; one row of 16 heads over 512 keys takes 10 us, one over 4096 13 us,
-// in latencies (its plan 2, first scores 5, states and joining 4).
+// Bound by the cache's bytes: 32 x 1 row of 16 heads over 16384-32749 keys (R 512) take 167-178 us, 907 MB
+// at 75-80% of the copy rate; one row of 16 heads over 512 keys takes 10 us, one over 4096 13 us,
+// in latencies (its plan 2, first scores 5, states and joining 4; all in graphs of 20).
+//
+// P is rounded to bf16 for its product: half a step a weight, 2^-8 sum p |c| at most, about what
+// the output's own rounding costs (against 64 bits 0.0017 relative, as with fp32 weights).  The rest
+// of P as a second bf16 term, for sequences of up to 16 packed rows, doubled that product in each
+// tile's chain of scores, softmax and product: 167 -> 213 us, 64 x 1 row of 16 heads over 4096
+// keys 66 -> 81 (R 256: 40 -> 58).
 //
 // S_{i+1} is issued ahead of O += P_i V_i, so that the softmax of one tile runs under
 // the products of another.  Tensor memory (512 columns): O 256 | S_0 S_1 128 | P_0 P_1 128.
@@ -441,7 +447,10 @@ cudaError_t launch(const PagedTcParams &sp, int ctas, cudaStream_t s, bool pdl) 
 }  // namespace
 
 // More packed rows than two blocks of 64 hold, at the mean number of rows a sequence, go to
-// pairs of CTAs.  us (64-row blocks / pairs), R 512:
+// pairs of CTAs.  The mean is all that the host knows, and rows past the last sequence count: 64
+// sequences of one row of 16 heads over 4096 keys take 66 us, in arrays of 1024 rows 150;
+// beside a chunk of 512 rows 227, the chunk alone 79.  us (64-row blocks / pairs), R 512, every
+// sequence alike:
 //             4 of 4096 keys   16 of 2048    48 of 1024    64 of 4096
 //   1 x 128   21.4 / 24.6      28.0 / 30.2   43.5 / 47.9   130 / 161
 //   4 x 40    25.8 / 24.6      35.3 / 32.2   55.3 / 49.1   181 / 164

@@ -11,10 +11,16 @@
 // twice, 1664 instead of 1088 products a (row, key).  Paired, a product of 64 cycles reads
 // 6 KB of shared memory and not 8; alone, a CTA's reads would bind before its products.
 //
-// 64 x 4 rows of 128 heads over 1024-8192 keys take 327-335 us: 503 GFLOP so counted, 260 us at
-// the matrix rate; without loads 250 us.  What is left are keys on their way: six blocks of the ring in flight
-// are what shared memory has room for (with four 407 us).  R = 256: 12 ragged chunks of 40
-// heads 349 us, 79% of the rate.
+// In graphs of 20, 64 x 4 rows of 128 heads over 1024-8192 keys take 327-335 us (350-383 a call among
+// others): 503 GFLOP so counted, 260 us at the matrix rate; without loads 250 us.  What is left
+// are keys on their way: six blocks of the ring in flight are what shared memory has room for
+// (with four 407 us).  R = 256: 12 ragged chunks of 40 heads 340-352 us, 79% of the rate (a call
+// among others 302-365, with the contexts drawn).
+//
+// P is rounded to bf16 for its product: half a step a weight, 2^-8 sum p |c| at most, about what
+// the output's own rounding costs (against 64 bits 0.0019 relative, with fp32 weights
+// 0.0017).  The rest of P as a second bf16 term would be one product more with V, 31% more
+// of what binds here (R = 256: 44-47%).
 //
 // S_{i+1} is issued ahead of O += P_i V_i, so that the softmax of one tile runs under the
 // scores of the next.  Queries take 144 of the 227 KB of shared memory (R = 512), so keys

@@ -267,7 +267,9 @@ cudaError_t launch_latent_combine(const PagedTcParams &sp, int shares, int sms, 
   cudaLaunchConfig_t cfg{};
   // More than eight shares an item: by blocks.  us (by blocks / by warps), R 512: one row of 16 heads,
   // 4 of 4096 keys 14.8 / 20.4, 8 of 2048 14.5 / 16.6, 16 of 2048 19.6 / 18.7; one of 128 heads, 16 of
-  // 2048 35.6 / 28.0.  (Of the places of the line, kPagedMaxCtas are for gaps.)
+  // 2048 35.6 / 28.0.  (Of the places of the line, kPagedMaxCtas are for gaps.)  The host does not
+  // know an item's shares: one sequence of 131072 keys (16 heads) takes 45 us, among 20 of 512 keys,
+  // where the long one's states are joined by warps, 68 (the short alone 15).
   const bool many = 8 * (sp.n_items - kPagedMaxCtas) < shares;
   // what is resident at once: with four blocks an SM of the first kind a call of two keys took 10.0
   // us, with two 9.1; with two of the second kind 16 x 4 rows of 128 heads took 60.7, with four 55.2

@@ -13,11 +13,12 @@
 // next one's products.
 //
 // Cached rows are the same for every head, so a pair keeps its 256 rows (K up to 512: 128 KB
-// a CTA) and walks the heads over them; only weights, from L2, pass through the ring.  8 ragged
-// prompts of 16 heads: 23 us against 26 with rows brought for each head; 12288 keys of 128
-// heads are the same 287 us both ways.  Those are 207 us of products (the matrix rate) when
-// nothing is stored and 238 us when the stores stay in L2: the rest is 805 MB of output on
-// their way to memory, which a plain fill of that size writes in 200 us.
+// a CTA) and walks the heads over them; only weights, from L2, pass through the ring.  In graphs
+// of 20, 8 ragged prompts of 16 heads: 23 us against 26 with rows brought for each head; 12288
+// keys of 128 heads are the same 287 us both ways (308-316 a call among others).  Those are 207 us
+// when nothing is stored (412 GFLOP, 2.0 PFLOP/s; the library's product, which the floors
+// count with, reaches 1.93) and 238 us when the stores stay in L2: the rest is 805 MB of output
+// on their way to memory, which a plain fill of that size writes in 200 us.
 //
 // Tiles of cached rows never cross a sequence, since page pieces start on whole pages.
 // The number of tiles is the device's to know: each CTA sums up the sequences' tiles
@@ -61,7 +62,7 @@ struct RowTile {
 
 // The sequences' row tiles before each thread's run of sequences, and the first kNear
 // tiles themselves: looked up through the row starts, a tile's place took two round trips
-// of the producer, which its ring of four stages does not cover.
+// of the producer, which its ring (four stages, in pairs six, with kept rows five) does not cover.
 constexpr int kNear = 1024;
 struct TileTable {
   int before[kThreads + 1];

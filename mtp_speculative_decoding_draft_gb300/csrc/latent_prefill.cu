@@ -17,10 +17,15 @@
 // products cost the issuing warp 160 cycles an instruction of 64.  The scores begin with the
 // shared part, which comes earlier.
 //
-// Bound by the products: 4096 rows over 12288, 32 heads, take 572-604 us, 78% of the matrix
-// rate at most, reading 4 KB of queries and 4 KB of keys from shared memory per 64 cycles, all
-// that it gives.  Without softmax 509 us, without loads 574.  Fresh prompts are bound by an item's start and end
-// (16 of 1000 rows, 16 heads: 126 us for 43 us of products; an item 17 us, its five tiles 7).
+// Bound by the products: 4096 rows over 12288, 32 heads, take 559-604 us in graphs of 20 (611-626 a
+// call among others), 80% of the matrix rate at most, reading 4 KB of queries and 4 KB of keys from
+// shared memory per 64 cycles, all that it gives.  Without softmax 509 us, without loads 574.
+// Fresh prompts are bound by an item's start and end (16 of 1000 rows, 16 heads: 126 us for 43 us
+// of products; an item 17 us, its five tiles 7).
+//
+// P is rounded to bf16 for its product: half a step a weight, 2^-8 sum p |v| at most (against 64 bits
+// 0.0020-0.0024 relative, with fp32 weights 0.0017, the output's own rounding).  The rest of P
+// as a second bf16 term would be 40% more products (Dn = Dv = 128, Dr 64), which bind here.
 //
 // Tensor memory (512 columns): S_0 | S_1 | O_0 | O_1, 128 each.  Warps 0-3 and 4-7 are
 // the groups' softmax, warp 8 brings keys and values, warp 9 issues the products, warp 10 brings
