@@ -31,6 +31,7 @@
 // brings keys, warp 5 (of the first CTA) issues the products of both, warp 6 brings queries,
 // warp 7 brings values and clears rows of them that no row sees.  Barriers that the issuer
 // waits for lie in the first CTA and count both; those that products complete lie in both.
+// Waits are at cluster scope, but for values that a CTA brings and clears for itself (zbar).
 #include "internal.h"
 #include "latent.cuh"
 #include "paged_tc.cuh"
@@ -143,7 +144,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (i + 1 < w.i1) locate(i + 1, need_next, y_next);  // its table entry loads under this tile's waits
         const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, need)) * prow * 128);
         for (int x = 0; x < NB; ++x) {
-          ok = __all_sync(kFull, mbar_wait(&k_empty[s], ph, p.status));
+          ok = __all_sync(kFull, mbar_wait_cluster(&k_empty[s], ph, p.status));
           if (!ok) break;
           const uint32_t bar = dsmem_addr(&k_full[s], 0);
           if (lane == 0) expect_tx_cluster(bar, bytes);
@@ -165,7 +166,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ph ^= 1u;
         }
         // the round before the first: never filled
-        if (!mbar_wait(&k_full[s], ph ^ 1u, p.status)) break;
+        if (!mbar_wait_cluster(&k_full[s], ph ^ 1u, p.status)) break;
       }
   } else if (warp == kValues) {
     // -------------------------------------------------- values: this CTA's 128 elements of a
@@ -183,7 +184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int y = need ? paged_page(p, w.b, k0) * p.page : 0;
         const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(kFull, need)) * prow * 128);
         const bool whole = (t0 + kTK <= w.r.hi && t0 >= w.r.lo) || t0 + kTK <= w.r.sink_end;
-        ok = __all_sync(kFull, mbar_wait(&v_empty[s], ph, p.status));
+        ok = __all_sync(kFull, mbar_wait_cluster(&v_empty[s], ph, p.status));
         if (!ok) break;
         unsigned char *tile = vring + s * L::VTILE, *dst = tile + grp * L::VGRP + pc * prow * 128;
         if (whole) {
@@ -218,13 +219,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           s = VST - 1;
           ph ^= 1u;
         }
-        if (!mbar_wait(&v_full[s], ph ^ 1u, p.status)) break;
+        if (!mbar_wait_cluster(&v_full[s], ph ^ 1u, p.status)) break;
       }
   } else if (warp == kQuery) {
     // -------------------------------------------------- the blocks' queries
     if (lane == 0) {
       for (int seg = 0; w.valid(); w.next(), ++seg) {
-        if (seg > 0 && !mbar_wait(q_empty, (uint32_t)(seg - 1) & 1u, p.status)) break;
+        if (seg > 0 && !mbar_wait_cluster(q_empty, (uint32_t)(seg - 1) & 1u, p.status)) break;
         const int t = w.t0 + rank * tpg;
         const bool any = t < w.t1();  // else this CTA's rows are none: whatever lies there
         for (int x = 0; x < NB; ++x) {
@@ -247,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // A wait that gives up flags the status; the waits after it are skipped and
       // the rest is issued on whatever is there, so that no barrier is left short.
       auto await = [&](uint64_t *bar, uint32_t parity) {
-        if (ok) ok = mbar_wait(bar, parity, p.status);
+        if (ok) ok = mbar_wait_cluster(bar, parity, p.status);
       };
       int it = 0, seg = 0, ks = 0, vs = 0;  // tiles whose scores were issued; stages
       uint32_t kph = 0, vph = 0, oph = 1;
@@ -287,12 +288,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (i > 0) {
             const int j = it - (i < nt ? 2 : 1);  // the tile before
             if (i == 1) {
-              if (ok) ok = mbar_wait_cluster(o_empty, oph, p.status);
+              await(o_empty, oph);
               oph ^= 1u;
             }
-            // (cluster scope: O's reads, P, a rescaled O and zeros of the second CTA)
-            if (ok) ok = mbar_wait_cluster(&p_full[j & 1], (uint32_t)(j >> 1) & 1u, p.status);
-            if (ok) ok = mbar_wait_cluster(&v_full[vs], vph, p.status);
+            await(&p_full[j & 1], (uint32_t)(j >> 1) & 1u);
+            await(&v_full[vs], vph);
             tc_fence_after();
             if (leader) {
               const uint64_t v = vd + (uint64_t)(vs * (L::VTILE >> 4));
@@ -312,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (leader) mma_commit_pair(drain);  // nothing is in flight when the tensor memory is freed
       __syncwarp();
-      mbar_wait(drain, 0, p.status);
+      mbar_wait_cluster(drain, 0, p.status);
     }
   } else {
     // -------------------------------------------------- softmax: a thread a row
@@ -332,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int k0 = w.r.tile(i) * kTK;
         const bool whole = k0 + kTK <= all_hi && (k0 >= all_lo || k0 + kTK <= min(p.sinks, all_hi));
         const uint32_t ts = tmem + lanebase + L::S(it & 1);
-        if (ok) ok = mbar_wait(&s_full[it & 1], (uint32_t)(it >> 1) & 1u, p.status);
+        if (ok) ok = mbar_wait_cluster(&s_full[it & 1], (uint32_t)(it >> 1) & 1u, p.status);
         __syncwarp();
         if (i == w.i0) trace_mark(kTkLatentAttn, 0);
         tc_fence_after();
@@ -366,7 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // The product of the tile before may still be running.  (A barrier for odd and
             // one for even tiles: this tile's scores show that the product two tiles before
             // is done, so that a parity never stands for two phases that are both possible.)
-            if (ok) ok = mbar_wait(&o_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u, p.status);
+            if (ok) ok = mbar_wait_cluster(&o_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u, p.status);
             __syncwarp();
             tc_fence_after();
             rescale_columns<kDV / 32>(to, f);
@@ -398,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       // ---- the block's output, or this segment's state
-      if (ok) ok = mbar_wait(&o_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u, p.status);
+      if (ok) ok = mbar_wait_cluster(&o_done[(it - 1) & 1], (uint32_t)((it - 1) >> 1) & 1u, p.status);
       __syncwarp();
       tc_fence_after();
       trace_mark(kTkLatentAttn, 1);

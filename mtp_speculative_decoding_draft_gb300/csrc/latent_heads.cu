@@ -251,12 +251,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
       const bool bring = KEEP && row_tile(u) != at;
       if (bring) {
         at = row_tile(u);
-        if (nkept > 0) ok = __all_sync(kFull, mbar_wait(kept_free, (uint32_t)(nkept - 1) & 1u, p.status));
+        if (nkept > 0) ok = __all_sync(kFull, mbar_wait_cluster(kept_free, (uint32_t)(nkept - 1) & 1u, p.status));
         ++nkept;
       }
       for (int kb = 0; kb < hp.kbs && ok; ++kb, ++i) {
         const int s = (int)(i % kStages);
-        if (i >= (uint32_t)kStages) ok = mbar_wait(&empty[s], ((i / kStages) - 1u) & 1u, p.status);
+        if (i >= (uint32_t)kStages) ok = mbar_wait_cluster(&empty[s], ((i / kStages) - 1u) & 1u, p.status);
         ok = __all_sync(kFull, ok);
         if (!ok) break;
         unsigned char *st = ring + s * kStageBytes;
@@ -308,10 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
     }
     if (!ok && rank == 0)  // let copies still in flight land before the CTAs exit
       for (uint32_t q = i > (uint32_t)kStages ? i - kStages : 0u; q < i; ++q)
-        if (!mbar_wait(&full[q % kStages], (q / kStages) & 1u, p.status)) break;
+        if (!mbar_wait_cluster(&full[q % kStages], (q / kStages) & 1u, p.status)) break;
     if (!ok && rank == 0 && nkept > 0)
       for (int x = 0; x < hp.kbs; ++x)
-        if (!mbar_wait(&kept[x], (uint32_t)(nkept - 1) & 1u, p.status)) break;
+        if (!mbar_wait_cluster(&kept[x], (uint32_t)(nkept - 1) & 1u, p.status)) break;
   } else if (warp == kIssuer) {
     if (rank == 0) {
       const uint32_t idesc = idesc_bf16_f32(128 * CTAS, 256) - ((uint32_t)(256 - hp.NT) >> 3 << 17) + (TRANS ? 1u << 16 : 0u);
@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
         if (!ok) break;
         for (int kb = 0; kb < hp.kbs && ok; ++kb, ++i) {
           const int s = (int)(i % kStages);
-          ok = mbar_wait(&full[s], (i / kStages) & 1u, p.status);
-          if (brought && ok) ok = mbar_wait(&kept[kb], (uint32_t)(nkept - 1) & 1u, p.status);
+          ok = mbar_wait_cluster(&full[s], (i / kStages) & 1u, p.status);
+          if (brought && ok) ok = mbar_wait_cluster(&kept[kb], (uint32_t)(nkept - 1) & 1u, p.status);
           ok = __all_sync(kFull, ok);
           if (!ok) break;
           tc_fence_after();
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_heads_kernel(const __grid_
         uint4 *dst = reinterpret_cast<uint4 *>(p.k_rope + (long long)(r.row0 + row) * p.ldkr);
         for (int e = 0; e < p.Dr / 8; ++e) dst[e] = __ldg(src + e);
       }
-      ok = __all_sync(kFull, ok && mbar_wait(&done[buf], (n >> 1) & 1u, p.status));
+      ok = __all_sync(kFull, ok && mbar_wait_cluster(&done[buf], (n >> 1) & 1u, p.status));
       if (!ok) break;
       tc_fence_after();
       if (n == 0) trace_mark(kTkLatentHeads, 1);
